@@ -109,7 +109,10 @@ enum {
   RSSM_DEVERR_CURSOR = 2u,   /* cursor outside [0, L]                 */
   RSSM_DEVERR_ACCEPT = 4u,   /* accepted length outside [0, T]        */
   RSSM_DEVERR_TIMEOUT = 8u,  /* a bounded wait on a tile copy ran out */
-  RSSM_DEVERR_SEQLEN = 16u   /* ragged window offsets out of order or wider than max_T */
+  RSSM_DEVERR_SEQLEN = 16u,  /* ragged window offsets out of order or wider than max_T */
+  RSSM_DEVERR_PAGES = 32u,   /* key-value cache: pool empty, table row full, a window past
+                                its slot's pages, a page id outside the pool */
+  RSSM_DEVERR_POSITION = 64u /* rotary position outside the table */
 };
 
 /*
@@ -398,6 +401,208 @@ rssm_status rssm_set_plan(rssm_handle *h, int32_t plan);
  * next launch. Never on in production calls.
  */
 rssm_status rssm_debug_withhold(rssm_handle *h, int32_t barrier);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Full-attention layers of a hybrid model: the paged key-value cache beside the
+ * replay store, and the attention that reads it. (The pull requests above serve
+ * models whose other layers are softmax attention; vLLM PR #64699, Overview:
+ * Qwen3.5 hybrid layers. They define no interface for those layers: this one
+ * is this library's own, in the manner of the calls above.)
+ *
+ * A slot's committed tokens are length[s]; its keys and values lie in pages of
+ * page_size tokens, page table[s][i] holding tokens [i page_size,
+ * (i + 1) page_size) of every layer. refs[page] counts the tables that name a
+ * page; a page with refs 0 is free. A step goes
+ *     rssm_kv_reserve   room for the window's tokens in the slots' pages
+ *     per attention layer: rssm_kv_append (rotate q, k; write k, v at positions
+ *         length[s] + i), then rssm_attn_decode or, for prompts,
+ *         rssm_attn_prefill
+ *     rssm_kv_commit    length[s] += accepted tokens
+ * so rejected draft tokens are simply written over by the next window, as the
+ * replay store's records are.
+ *
+ * Layouts (row-major):
+ *   q : [N][HQ][D], k, v : [N][HKV][D] in dtype, tokens `stride` elements apart
+ *       (heads and dimensions contiguous), so that views of one projection's
+ *       output serve as they are; 16-byte aligned, strides in whole 16 bytes
+ *   o, q_out : [N][HQ][D] in dtype, contiguous, 16-byte aligned
+ *   lse : [N][HQ] fp32: ln of the row's sum of exponentials (may be null)
+ *   k_pages, v_pages : [n_layers][n_pages][HKV][page_size][D] in dtype
+ *   table : [n_slots][max_pages] int32, -1 where no page is held
+ *   held, length : [n_slots] int32         refs : [n_pages] int32
+ * Query head h reads key head h / (HQ / HKV).
+ *
+ * Null rows, errors, alignment of index arrays, streams and graph capture are
+ * as above. Calls on one cache share its work buffer and tables: order them on
+ * one stream (or by events). A row that sets an error bit is skipped and its
+ * outputs are left as they are, except where a call says otherwise. Unless a
+ * call says otherwise two live rows of one call must not name the same slot.
+ *
+ * Non-finite values in keys and values that a query must not see (rejected
+ * drafts, other sequences' tokens, unused places of a page) never reach its
+ * output: they are left out by selection.
+ */
+typedef struct rssm_kv_config {
+  int32_t n_layers;   /* attention layers that share the tables             */
+  int32_t n_slots;
+  int32_t HQ;         /* query heads, a multiple of HKV, at most 64 x HKV   */
+  int32_t HKV;        /* key-value heads                                    */
+  int32_t D;          /* head size: 64, 128 or 256                          */
+  int32_t n_pages;
+  int32_t page_size;  /* tokens: 16, 32, 64, 128 or 256                     */
+  int32_t max_pages;  /* table entries of a slot                            */
+  int32_t dtype;      /* F32, BF16 or F16: cache, inputs and outputs        */
+  float scale;        /* of the scores, > 0                                 */
+} rssm_kv_config;
+
+/* All non-null; k_pages, v_pages and work 16-byte aligned. Before the first
+ * call the caller sets table to -1 and held, length, refs, work and err_word
+ * to 0. Borrowed for the life of the handle. */
+typedef struct rssm_kv_buffers {
+  void *k_pages;
+  void *v_pages;
+  int32_t *table;
+  int32_t *held;
+  int32_t *length;
+  int32_t *refs;
+  void *work;
+  uint32_t *err_word;
+} rssm_kv_buffers;
+
+typedef struct rssm_kv_sizes {
+  size_t k_pages;
+  size_t v_pages;
+  size_t table;
+  size_t held;
+  size_t length;
+  size_t refs;
+  size_t work;
+  size_t err_word;
+} rssm_kv_sizes;
+
+typedef struct rssm_kv_handle rssm_kv_handle;
+
+rssm_status rssm_kv_required_bytes(const rssm_kv_config *cfg, rssm_kv_sizes *out);
+rssm_status rssm_kv_alloc(const rssm_kv_config *cfg, const rssm_kv_buffers *buf,
+                          rssm_kv_handle **out);
+void rssm_kv_free(rssm_kv_handle *h);
+
+/*
+ * Pages for the next window: row r's slot gets free pages, lowest first, until
+ * it holds room for length[s] + T_r tokens, T_r = T, or cu_seqlens[r+1] -
+ * cu_seqlens[r] where cu_seqlens (device int32[B + 1]) is not null. Rows are
+ * served in order; a row that finds too few free pages, and every later row
+ * that needs any, gets none (RSSM_DEVERR_PAGES), as does a row whose table is
+ * too short.
+ */
+rssm_status rssm_kv_reserve(rssm_kv_handle *h, const int32_t *slot,
+                            const int32_t *cu_seqlens, int32_t B, int32_t T,
+                            void *stream);
+
+/*
+ * length[s] += accept_len[r] (device int32[B], 0 <= a <= T_r, else
+ * RSSM_DEVERR_ACCEPT), or the whole window T_r where accept_len is null.
+ */
+rssm_status rssm_kv_commit(rssm_kv_handle *h, const int32_t *slot,
+                           const int32_t *accept_len, const int32_t *cu_seqlens,
+                           int32_t B, int32_t T, void *stream);
+
+/*
+ * Slot dst[r] becomes a continuation of slot src[r]: it gives back what it
+ * held, then takes src's committed tokens. Full pages are shared; the last,
+ * partly filled page is copied whole, so that both slots can go on writing.
+ * With deep non-zero every page is copied. Sources may repeat; a dst must be
+ * named once and not be a source of the call; rows with a null src or dst are
+ * skipped. Rows are served in order; a row that finds too few free pages
+ * leaves dst empty (RSSM_DEVERR_PAGES).
+ */
+rssm_status rssm_kv_fork(rssm_kv_handle *h, const int32_t *src,
+                         const int32_t *dst, int32_t B, int32_t deep,
+                         void *stream);
+
+/* Gives back the slots' pages (a shared page stays with the others); the slots
+ * end empty. */
+rssm_status rssm_kv_release(rssm_kv_handle *h, const int32_t *slot, int32_t B,
+                            void *stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with U pages in use, the
+ * n-th used page behind the first U places goes to the n-th free place within
+ * them, in every layer, and the tables follow. Pages keep their order
+ * otherwise; the pool's tail is then free.
+ */
+rssm_status rssm_kv_compact(rssm_kv_handle *h, void *stream);
+
+/* Rotary positions: pair i < pairs of a head turns dimensions i and i + pairs
+ * by the angle position * frequency_i, read from `table`, device
+ * fp32[max_pos][2][pairs] (cosines, then sines). Positions have `axes` axes
+ * (1..3; time, height, width): the first sections[0] pairs go by axis 0, the
+ * next sections[1] by axis 1, and so on; with `interleaved` non-zero pair i
+ * goes by axis a = i % axes where i < axes * sections[a], else by axis 0.
+ * The sections sum to pairs; pairs is a multiple of 8, 2 pairs <= D, and the
+ * dimensions behind them are left as they are. */
+typedef struct rssm_rope {
+  const float *table;
+  int32_t max_pos;
+  int32_t pairs;
+  int32_t axes;
+  int32_t sections[3];
+  int32_t interleaved;
+} rssm_rope;
+
+/*
+ * One layer's new tokens: q_out = rotated q, and rotated k and v written to the
+ * slots' pages at cache positions length[s] + i. Row r's tokens are
+ * [r T, (r + 1) T) of N = B T, or [cu_seqlens[r], cu_seqlens[r+1]) of N.
+ * positions is device int32[axes][N]; null: a token's place in its cache on
+ * every axis. rope null: no rotation. q and q_out may both be null (keys and
+ * values only), and q_out may be q itself where q is contiguous. Two rows may
+ * not write the same slot. A token past its slot's pages sets
+ * RSSM_DEVERR_PAGES, one with a position outside [0, max_pos)
+ * RSSM_DEVERR_POSITION: that token is skipped.
+ */
+rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
+                           const void *k, const void *v, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride,
+                           const rssm_rope *rope, const int32_t *positions,
+                           const int32_t *cu_seqlens, const int32_t *slot,
+                           int32_t B, int32_t T, int32_t N, void *q_out,
+                           void *stream);
+
+/*
+ * Attention of a window of T (1 <= T <= 64) new tokens per row over the
+ * slot's pages of one layer: token t of row r sees cache positions
+ * [0, length[s] + t], its own key among them (appended before):
+ *     o = sum_j softmax_j(scale q . k_j) v_j.
+ * q is [B T][HQ][D]. A slot may be named by several rows. A row whose window
+ * is not within its pages sets RSSM_DEVERR_PAGES and is skipped; a table entry
+ * outside the pool sets it too and counts as keys and values of zero.
+ */
+rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
+                             int64_t q_stride, const int32_t *slot, int32_t B,
+                             int32_t T, void *o, float *lse, void *stream);
+
+/*
+ * Causal attention over prompts, packed: sequence r's query tokens are
+ * [cu_seqlens[r], cu_seqlens[r+1]) of N, its keys and values
+ * [cu_keys[r], cu_keys[r+1]) of M (cu_keys null: those of the query tokens,
+ * M = N). With Lq queries and Lk keys query i sees keys j <= Lk - Lq + i, so
+ * keys of earlier chunks come before the chunk's own; a query that sees none
+ * (Lk < Lq) gives o = 0 and lse = -inf. The cache is not read. slot (may be
+ * null) skips rows with a null slot. Offsets that decrease or leave [0, N] or
+ * [0, M] set RSSM_DEVERR_SEQLEN and skip the sequence.
+ */
+rssm_status rssm_attn_prefill(rssm_kv_handle *h, const void *q, const void *k,
+                              const void *v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride,
+                              const int32_t *cu_seqlens, const int32_t *cu_keys,
+                              const int32_t *slot, int32_t B, int32_t N,
+                              int32_t M, void *o, float *lse, void *stream);
+
+/* As rssm_get_device_error, for a cache's error word. */
+rssm_status rssm_kv_get_device_error(rssm_kv_handle *h, uint32_t *out,
+                                     int32_t clear, void *stream);
 
 const char *rssm_status_string(rssm_status s);
 

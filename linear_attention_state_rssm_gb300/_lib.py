@@ -19,7 +19,8 @@ STATUS_NAMES = {0: "RSSM_OK", 1: "RSSM_ERR_INVALID_ARG", 2: "RSSM_ERR_UNSUPPORTE
 ALGO = {"gdn": 0, "kda": 1}
 DTYPE = {"f32": 0, "bf16": 1, "f16": 2}
 COMMIT = {"lazy": 0, "fold_every": 1}
-DEVERR = {"slot": 1, "cursor": 2, "accept": 4, "timeout": 8, "seqlen": 16}
+DEVERR = {"slot": 1, "cursor": 2, "accept": 4, "timeout": 8, "seqlen": 16, "pages": 32,
+          "position": 64}
 
 # Every entry point declared in include/rssm.h.
 SYMBOLS = ("rssm_required_bytes", "rssm_alloc", "rssm_free", "rssm_decode", "rssm_verify",
@@ -27,7 +28,11 @@ SYMBOLS = ("rssm_required_bytes", "rssm_alloc", "rssm_free", "rssm_decode", "rss
            "rssm_commit_ragged", "rssm_fold", "rssm_reset_slots", "rssm_conv_window",
            "rssm_conv_commit",
            "rssm_get_device_error", "rssm_set_plan", "rssm_debug_withhold",
-           "rssm_status_string", "rssm_version")
+           "rssm_status_string", "rssm_version",
+           "rssm_kv_required_bytes", "rssm_kv_alloc", "rssm_kv_free", "rssm_kv_reserve",
+           "rssm_kv_commit", "rssm_kv_fork", "rssm_kv_release", "rssm_kv_compact",
+           "rssm_kv_append", "rssm_attn_decode", "rssm_attn_prefill",
+           "rssm_kv_get_device_error")
 
 
 class RssmError(RuntimeError):
@@ -58,8 +63,32 @@ class rssm_sizes(ctypes.Structure):
                  "err_word")]
 
 
+class rssm_kv_config(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in
+                ("n_layers", "n_slots", "HQ", "HKV", "D", "n_pages", "page_size", "max_pages",
+                 "dtype")] + [("scale", ctypes.c_float)]
+
+
+_KV_BUFFERS = ("k_pages", "v_pages", "table", "held", "length", "refs", "work", "err_word")
+
+
+class rssm_kv_buffers(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in _KV_BUFFERS]
+
+
+class rssm_kv_sizes(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_size_t) for name in _KV_BUFFERS]
+
+
+class rssm_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _lib = None
 
 
@@ -94,6 +123,22 @@ def load() -> ctypes.CDLL:
         "rssm_get_device_error": ([_P, ctypes.POINTER(ctypes.c_uint32), _I, _P], _I),
         "rssm_set_plan": ([_P, _I], _I),
         "rssm_debug_withhold": ([_P, _I], _I),
+        "rssm_kv_required_bytes": ([ctypes.POINTER(rssm_kv_config),
+                                    ctypes.POINTER(rssm_kv_sizes)], _I),
+        "rssm_kv_alloc": ([ctypes.POINTER(rssm_kv_config), ctypes.POINTER(rssm_kv_buffers),
+                           ctypes.POINTER(_P)], _I),
+        "rssm_kv_free": ([_P], None),
+        "rssm_kv_reserve": ([_P, _P, _P, _I, _I, _P], _I),
+        "rssm_kv_commit": ([_P, _P, _P, _P, _I, _I, _P], _I),
+        "rssm_kv_fork": ([_P, _P, _P, _I, _I, _P], _I),
+        "rssm_kv_release": ([_P, _P, _I, _P], _I),
+        "rssm_kv_compact": ([_P, _P], _I),
+        "rssm_kv_append": ([_P, _I, _P, _P, _P, _L, _L, _L, ctypes.POINTER(rssm_rope), _P, _P, _P,
+                            _I, _I, _I, _P, _P], _I),
+        "rssm_attn_decode": ([_P, _I, _P, _L, _P, _I, _I, _P, _P, _P], _I),
+        "rssm_attn_prefill": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P],
+                              _I),
+        "rssm_kv_get_device_error": ([_P, ctypes.POINTER(ctypes.c_uint32), _I, _P], _I),
         "rssm_status_string": ([_I], ctypes.c_char_p),
         "rssm_version": ([], _I),
     }
@@ -264,3 +309,80 @@ def rssm_status_string(status: int) -> str:
 
 def rssm_version() -> int:
     return int(load().rssm_version())
+
+
+# ------------------------------------------- key-value cache and its attention
+def make_kv_config(n_layers=1, n_slots=1, HQ=1, HKV=1, D=128, n_pages=1, page_size=64,
+                   max_pages=1, dtype="bf16", scale=None) -> rssm_kv_config:
+    return rssm_kv_config(n_layers, n_slots, HQ, HKV, D, n_pages, page_size, max_pages,
+                          DTYPE[dtype], float(D ** -0.5 if scale is None else scale))
+
+
+def rssm_kv_required_bytes(cfg: rssm_kv_config) -> rssm_kv_sizes:
+    out = rssm_kv_sizes()
+    _check(load().rssm_kv_required_bytes(ctypes.byref(cfg), ctypes.byref(out)),
+           "rssm_kv_required_bytes")
+    return out
+
+
+def rssm_kv_alloc(cfg: rssm_kv_config, bufs: rssm_kv_buffers) -> int:
+    h = _P()
+    _check(load().rssm_kv_alloc(ctypes.byref(cfg), ctypes.byref(bufs), ctypes.byref(h)),
+           "rssm_kv_alloc")
+    return h.value
+
+
+def rssm_kv_free(handle: int) -> None:
+    load().rssm_kv_free(handle)
+
+
+def rssm_kv_reserve(handle, slot, cu_seqlens, B, T, stream=None):
+    _check(load().rssm_kv_reserve(handle, _ptr(slot), _ptr(cu_seqlens), B, T, _stream(stream)),
+           "rssm_kv_reserve")
+
+
+def rssm_kv_commit(handle, slot, accept_len, cu_seqlens, B, T, stream=None):
+    _check(load().rssm_kv_commit(handle, _ptr(slot), _ptr(accept_len), _ptr(cu_seqlens), B, T,
+                                 _stream(stream)), "rssm_kv_commit")
+
+
+def rssm_kv_fork(handle, src, dst, B, deep, stream=None):
+    _check(load().rssm_kv_fork(handle, _ptr(src), _ptr(dst), B, int(bool(deep)),
+                               _stream(stream)), "rssm_kv_fork")
+
+
+def rssm_kv_release(handle, slot, B, stream=None):
+    _check(load().rssm_kv_release(handle, _ptr(slot), B, _stream(stream)), "rssm_kv_release")
+
+
+def rssm_kv_compact(handle, stream=None):
+    _check(load().rssm_kv_compact(handle, _stream(stream)), "rssm_kv_compact")
+
+
+def rssm_kv_append(handle, layer, q, k, v, q_stride, k_stride, v_stride, rope, positions,
+                   cu_seqlens, slot, B, T, N, q_out, stream=None):
+    _check(load().rssm_kv_append(handle, layer, _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride,
+                                 v_stride, None if rope is None else ctypes.byref(rope),
+                                 _ptr(positions), _ptr(cu_seqlens), _ptr(slot), B, T, N,
+                                 _ptr(q_out), _stream(stream)), "rssm_kv_append")
+
+
+def rssm_attn_decode(handle, layer, q, q_stride, slot, B, T, o, lse, stream=None):
+    _check(load().rssm_attn_decode(handle, layer, _ptr(q), q_stride, _ptr(slot), B, T, _ptr(o),
+                                   _ptr(lse), _stream(stream)), "rssm_attn_decode")
+
+
+def rssm_attn_prefill(handle, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, cu_keys, slot,
+                      B, N, M, o, lse, stream=None):
+    _check(load().rssm_attn_prefill(handle, _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride,
+                                    v_stride, _ptr(cu_seqlens), _ptr(cu_keys), _ptr(slot), B, N,
+                                    M, _ptr(o), _ptr(lse), _stream(stream)), "rssm_attn_prefill")
+
+
+def rssm_kv_get_device_error(handle, clear=True, stream=None) -> int:
+    word = ctypes.c_uint32(0)
+    st = load().rssm_kv_get_device_error(handle, ctypes.byref(word), int(bool(clear)),
+                                         _stream(stream))
+    if st not in (RSSM_OK, 4):
+        raise RssmError(st, "rssm_kv_get_device_error")
+    return int(word.value)

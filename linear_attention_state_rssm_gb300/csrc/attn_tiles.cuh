@@ -1,0 +1,82 @@
+// Which sequence and query tile a CTA of a packed prompt launch works on: the
+// lengths are on the device, so each CTA finds its place by itself.
+#pragma once
+
+#include "attn_core.cuh"
+#include "kv_common.cuh"
+
+namespace rssm {
+
+struct PromptTile {
+  int tile;        // query tile of the sequence
+  int q0, k0;      // the sequence's first query token and key
+  int lq, lk;
+  int found;
+};
+
+// Offsets of sequence r; false for a null slot or offsets out of order.
+__device__ __forceinline__ bool prompt_span(const PromptParams& p, int r, bool tell, int& q0,
+                                            int& lq, int& k0, int& lk) {
+  const int s = p.slot != nullptr ? p.slot[r] : 0;
+  if (s < 0) return false;
+  uint32_t bad = 0;
+  if (s >= p.n_slots) bad = DEVERR_SLOT;
+  q0 = p.cu[r];
+  const int q1 = p.cu[r + 1];
+  if (q0 < 0 || q1 < q0 || q1 > p.N) bad |= DEVERR_SEQLEN;
+  k0 = q0;
+  int k1 = q1;
+  if (p.cuk != nullptr) {
+    k0 = p.cuk[r];
+    k1 = p.cuk[r + 1];
+  }
+  if (k0 < 0 || k1 < k0 || k1 > p.M) bad |= DEVERR_SEQLEN;
+  if (bad) {
+    if (tell) atomicOr(p.err, bad);
+    return false;
+  }
+  lq = q1 - q0;
+  lk = k1 - k0;
+  return true;
+}
+
+// Tile `index` of the launch (tiles of `toks` query tokens, sequences in
+// order, a sequence's last tile first: it sees the most keys). All NT threads
+// of the CTA; false when the launch has fewer tiles.
+template <int NT>
+__device__ __forceinline__ bool find_tile(const PromptParams& p, int toks, int index, bool tell,
+                                          PromptTile* out) {
+  __shared__ int sums[NT / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) out->found = 0;
+  int before = 0;
+  for (int r0 = 0; r0 < p.B; r0 += NT) {
+    const int r = r0 + tid;
+    int q0 = 0, k0 = 0, lq = 0, lk = 0, n = 0;
+    if (r < p.B && prompt_span(p, r, tell && index == 0, q0, lq, k0, lk))
+      n = (lq + toks - 1) / toks;
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(kFull, incl, d);
+      if (lane >= d) incl += y;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int at = before + incl - n, all = 0;
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < warp) at += sums[i];
+      all += sums[i];
+    }
+    if (at <= index && index < at + n) {
+      *out = PromptTile{at + n - 1 - index, q0, k0, lq, lk, 1};
+    }
+    before += all;
+    __syncthreads();
+    if (index < before && index != 0) break;  // tile 0's CTA looks every sequence over
+  }
+  __syncthreads();
+  return out->found != 0;
+}
+
+}  // namespace rssm

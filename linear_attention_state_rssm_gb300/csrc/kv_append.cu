@@ -1,0 +1,189 @@
+// New tokens of one layer: rotary positions on q and k, and the append of k
+// and v to the slots' pages, in one pass over the projection's output.
+//
+//     pair i < P of a head:  y_i     = x_i cos a - x_{i+P} sin a
+//                            y_{i+P} = x_{i+P} cos a + x_i sin a,
+//     a = position[axis(i)] * frequency_i (cosines and sines from a table);
+//     dimensions from 2 P on, and v, are copied.
+// With several axes (time, height, width) each pair turns by the position of
+// its own axis. Angles are looked up, not computed: a position times a
+// frequency in fp32 is off by 2^-24 of the angle, 0.06 rad at position 10^6.
+//
+// Every value is read once and written once: HBM-bound. One CTA per token; a
+// thread keeps its pair's cosines and sines in registers over the heads it
+// serves and has the loads of up to four heads in flight before it turns any.
+#include "attn_core.cuh"
+#include "kv_common.cuh"
+
+namespace rssm {
+
+namespace {
+
+constexpr int kAppendThreads = 128;
+constexpr int kHeadsAhead = 4;
+
+template <typename T>
+struct Vec16 {
+  static constexpr int E = 16 / (int)sizeof(T);
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&v)[E]) {
+    const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = attn_f32(t[i]);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&v)[E]) {
+    uint4 u;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+    if constexpr (std::is_same<T, float>::value) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
+    return u;
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads)
+    kv_append_kernel(const __grid_constant__ AppendParams p) {
+  using V = Vec16<T>;
+  constexpr int E = V::E;
+  const int tok = blockIdx.x, tid = threadIdx.x;
+  if (p.cu != nullptr && tok == 0) {
+    for (int r = tid; r < p.B; r += kAppendThreads) {
+      if (p.cu[r] < 0 || p.cu[r + 1] < p.cu[r] || p.cu[r + 1] > p.N) atomicOr(p.err, DEVERR_SEQLEN);
+    }
+  }
+  // the token's row and place in its window
+  int r, i;
+  if (p.cu == nullptr) {
+    r = tok / p.T;
+    i = tok - r * p.T;
+  } else {
+    int lo = 0, hi = p.B;  // last row that begins at or before the token
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu[mid] <= tok) lo = mid; else hi = mid;
+    }
+    r = lo;
+    i = tok - p.cu[r];
+    if (i < 0 || tok >= p.cu[r + 1]) return;  // outside every window
+  }
+  const int s = p.slot[r];
+  if (s < 0) return;
+  uint32_t bad = 0;
+  int len = 0;
+  if (s >= p.n_slots) {
+    bad = DEVERR_SLOT;
+  } else {
+    len = p.length[s];
+    const int held = p.held[s];
+    if (len < 0) {
+      bad = DEVERR_CURSOR;
+    } else if (held < 0 || held > p.max_pages || (long long)len + i >= ((long long)held << p.shift)) {
+      bad = DEVERR_PAGES;
+    }
+  }
+  int page = 0;
+  if (bad == 0) {
+    page = p.table[(size_t)s * p.max_pages + ((len + i) >> p.shift)];
+    if (page < 0 || page >= p.n_pages) bad = DEVERR_PAGES;
+  }
+  int pos[kMaxRopeAxes] = {len + i, len + i, len + i};
+  if (p.rope != nullptr && bad == 0) {
+#pragma unroll
+    for (int a = 0; a < kMaxRopeAxes; ++a) {
+      if (p.positions != nullptr && a < p.axes) pos[a] = p.positions[(size_t)a * p.N + tok];
+      if (a < p.axes && (pos[a] < 0 || pos[a] >= p.max_pos)) bad = DEVERR_POSITION;
+    }
+  }
+  if (bad) {
+    if (tid == 0) atomicOr(p.err, bad);
+    return;
+  }
+
+  const int ip = p.D / (2 * E);  // items of a head: two vectors each
+  const int np = p.P / E;        // of which turned
+  const int j = tid % ip, y0 = tid / ip, ny = kAppendThreads / ip;
+  const bool turn = j < np;
+  const int v0 = turn ? j : 2 * j, v1 = turn ? j + np : 2 * j + 1;  // np + np + 2 (j - np) = 2 j
+  float cs[E], sn[E];
+  if (turn) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int pair = j * E + e;
+      int axis = 0;
+      if (p.interleaved) {
+        const int a = pair % p.axes;
+        axis = pair < p.axes * p.sec[a] ? a : 0;
+      } else {
+        axis = pair < p.sec[0] ? 0 : pair < p.sec[0] + p.sec[1] ? 1 : 2;
+      }
+      const int at = axis == 0 ? pos[0] : axis == 1 ? pos[1] : pos[2];
+      const float* row = p.rope + (size_t)at * 2 * p.P;
+      cs[e] = __ldg(row + pair);
+      sn[e] = __ldg(row + p.P + pair);
+    }
+  }
+  const size_t head_bytes = ((size_t)p.D * sizeof(T)) << p.shift;
+  const size_t off = (size_t)page * head_bytes * p.HKV +
+                     (size_t)((len + i) & ((1 << p.shift) - 1)) * (p.D * sizeof(T));
+  const int hq = p.q != nullptr ? p.HQ : 0, heads = hq + 2 * p.HKV;
+  for (int y = y0; y < heads; y += ny * kHeadsAhead) {
+    uint4 a[kHeadsAhead], b[kHeadsAhead];
+#pragma unroll
+    for (int k = 0; k < kHeadsAhead; ++k) {
+      const int h = y + k * ny;
+      if (h < heads) {
+        const bool val = h >= hq + p.HKV;
+        const T* x = h < hq ? static_cast<const T*>(p.q) + tok * p.qs + (long long)h * p.D
+                     : !val ? static_cast<const T*>(p.k) + tok * p.ks + (long long)(h - hq) * p.D
+                            : static_cast<const T*>(p.v) + tok * p.vs +
+                                  (long long)(h - hq - p.HKV) * p.D;
+        a[k] = reinterpret_cast<const uint4*>(x)[val ? 2 * j : v0];
+        b[k] = reinterpret_cast<const uint4*>(x)[val ? 2 * j + 1 : v1];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kHeadsAhead; ++k) {
+      const int h = y + k * ny;
+      if (h < heads) {
+        const bool val = h >= hq + p.HKV;
+        if (turn && !val) {
+          float xa[E], xb[E], ya[E], yb[E];
+          V::unpack(a[k], xa);
+          V::unpack(b[k], xb);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            ya[e] = fmaf(xa[e], cs[e], -xb[e] * sn[e]);
+            yb[e] = fmaf(xb[e], cs[e], xa[e] * sn[e]);
+          }
+          a[k] = V::pack(ya);
+          b[k] = V::pack(yb);
+        }
+        uint4* to = h < hq ? reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) +
+                                                      ((size_t)tok * p.HQ + h) * p.D)
+                    : !val ? reinterpret_cast<uint4*>(p.kp + off + (h - hq) * head_bytes)
+                           : reinterpret_cast<uint4*>(p.vp + off + (h - hq - p.HKV) * head_bytes);
+        to[val ? 2 * j : v0] = a[k];
+        to[val ? 2 * j + 1 : v1] = b[k];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st) {
+  if (p.dt == DT_F32) {
+    kv_append_kernel<float><<<p.N, kAppendThreads, 0, st>>>(p);
+  } else if (p.dt == DT_BF16) {
+    kv_append_kernel<__nv_bfloat16><<<p.N, kAppendThreads, 0, st>>>(p);
+  } else {
+    kv_append_kernel<__half><<<p.N, kAppendThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace rssm

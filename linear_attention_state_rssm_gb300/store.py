@@ -159,3 +159,166 @@ class ConvWindows:
     def rssm_conv_commit(self, slot, accept_len, T, stream=None):
         _lib.rssm_conv_commit(self.window, self.draft, slot, accept_len, slot.numel(), T, self.D,
                               self.K, self.n_slots, self.dtype, self.err_word, stream)
+
+
+class RotaryTable:
+    """Cosines and sines of rotary positions for KVCache.rssm_kv_append.
+
+    table is fp32 [max_pos, 2, pairs]; sections gives how many of the pairs go
+    by each position axis (one axis, or time, height, width), in blocks or
+    interleaved (include/rssm.h, rssm_rope).
+    """
+
+    def __init__(self, table, sections=None, interleaved=False):
+        if table.dtype != torch.float32 or table.dim() != 3 or table.shape[1] != 2 \
+                or not table.is_contiguous():
+            raise ValueError("table: contiguous fp32 [max_pos, 2, pairs]")
+        sections = [table.shape[2]] if sections is None else list(sections)
+        if not 1 <= len(sections) <= 3:
+            raise ValueError("sections: one to three axes")
+        self.table, self.axes = table, len(sections)
+        sec = (_lib.ctypes.c_int32 * 3)(*(sections + [0] * (3 - len(sections))))
+        self.struct = _lib.rssm_rope(table.data_ptr(), table.shape[0], table.shape[2], self.axes,
+                                     sec, int(bool(interleaved)))
+
+    @classmethod
+    def from_base(cls, max_pos, pairs, base=10000.0, sections=None, interleaved=False,
+                  device="cuda"):
+        """Frequencies base^(-i / pairs), angles in 64 bits, rounded once."""
+        i = torch.arange(pairs, dtype=torch.float64, device=device)
+        angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] \
+            * base ** (-i / pairs)
+        return cls(torch.stack((angle.cos(), angle.sin()), 1).float().contiguous(), sections,
+                   interleaved)
+
+
+class KVCache:
+    """Paged keys and values of the full-attention layers, ``n_slots`` requests.
+
+    Buffers (row-major):
+      k_pages, v_pages [n_layers, n_pages, HKV, page_size, D]  dtype
+      table            [n_slots, max_pages] int32 (-1: no page)
+      held, length     [n_slots] int32: pages held, committed tokens
+      refs             [n_pages] int32: tables that name the page
+      work, err_word   scratch of the calls; error bits (_lib.DEVERR)
+
+    q, k, v may be views whose tokens are strided (slices of one projection's
+    output); outputs are contiguous. The contract of each call is that of the C
+    entry point of the same name.
+    """
+
+    def __init__(self, n_layers=1, n_slots=1, HQ=1, HKV=1, D=128, n_pages=1, page_size=64,
+                 max_pages=None, dtype="bf16", scale=None, device="cuda"):
+        max_pages = n_pages if max_pages is None else max_pages
+        self.cfg = _lib.make_kv_config(n_layers, n_slots, HQ, HKV, D, n_pages, page_size,
+                                       max_pages, dtype, scale)
+        self.n_layers, self.n_slots, self.HQ, self.HKV, self.D = n_layers, n_slots, HQ, HKV, D
+        self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
+        self.dtype, self.scale = dtype, self.cfg.scale
+        self.device = torch.device(device)
+        sizes = _lib.rssm_kv_required_bytes(self.cfg)  # validates the configuration
+        dev, t = self.device, _TORCH[dtype]
+        shape = (n_layers, n_pages, HKV, page_size, D)
+        self.k_pages = torch.zeros(shape, dtype=t, device=dev)
+        self.v_pages = torch.zeros(shape, dtype=t, device=dev)
+        self.table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=dev)
+        self.held = torch.zeros(n_slots, dtype=torch.int32, device=dev)
+        self.length = torch.zeros(n_slots, dtype=torch.int32, device=dev)
+        self.refs = torch.zeros(n_pages, dtype=torch.int32, device=dev)
+        self.work = torch.zeros(sizes.work, dtype=torch.uint8, device=dev)
+        self.err_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        bufs = _lib.rssm_kv_buffers(*(x.data_ptr() for x in (
+            self.k_pages, self.v_pages, self.table, self.held, self.length, self.refs,
+            self.work, self.err_word)))
+        with torch.cuda.device(dev):
+            self.handle = _lib.rssm_kv_alloc(self.cfg, bufs)
+
+    # ---------------------------------------------------------------- pages
+    def rssm_kv_reserve(self, slot, T=1, cu_seqlens=None, stream=None):
+        """Pages for the next T tokens of each row (or for its cu_seqlens)."""
+        _lib.rssm_kv_reserve(self.handle, slot, cu_seqlens, slot.numel(), T, stream)
+
+    def rssm_kv_commit(self, slot, T=1, accept_len=None, cu_seqlens=None, stream=None):
+        """length += accepted tokens (the whole window where accept_len is None)."""
+        _lib.rssm_kv_commit(self.handle, slot, accept_len, cu_seqlens, slot.numel(), T, stream)
+
+    def rssm_kv_fork(self, src, dst, deep=False, stream=None):
+        """Slot dst[r] continues slot src[r]: full pages shared (deep: copied)."""
+        if src.numel() != dst.numel():
+            raise ValueError("one source per destination")
+        _lib.rssm_kv_fork(self.handle, src, dst, src.numel(), deep, stream)
+
+    def rssm_kv_release(self, slot, stream=None):
+        _lib.rssm_kv_release(self.handle, slot, slot.numel(), stream)
+
+    def rssm_kv_compact(self, stream=None):
+        """Pages in use move to the front of the pool."""
+        _lib.rssm_kv_compact(self.handle, stream)
+
+    # ------------------------------------------------------------ attention
+    def rssm_kv_append(self, layer, q, k, v, slot, T=1, q_out=None, rope=None, positions=None,
+                       cu_seqlens=None, stream=None):
+        """Rotate q (into q_out) and k, write k and v to the slots' pages."""
+        n, ks = self._tokens(k, self.HKV)
+        _, vs = self._tokens(v, self.HKV, n)
+        qs = self._tokens(q, self.HQ, n)[1] if q is not None else 0
+        if q_out is not None:
+            self._output(q_out, n)
+        if positions is not None and (rope is None or positions.dtype != torch.int32
+                                      or positions.numel() != rope.axes * n
+                                      or not positions.is_contiguous()):
+            raise ValueError("positions: contiguous int32 [axes, tokens], with a rotary table")
+        _lib.rssm_kv_append(self.handle, layer, q, k, v, qs, ks, vs,
+                            None if rope is None else rope.struct, positions, cu_seqlens, slot,
+                            slot.numel(), T, n, q_out, stream)
+
+    def rssm_attn_decode(self, layer, q, slot, T, o, lse=None, stream=None):
+        """T new tokens per row over the slot's pages (their keys appended before)."""
+        B = slot.numel()
+        _, qs = self._tokens(q, self.HQ, B * T)
+        self._output(o, B * T, lse)
+        _lib.rssm_attn_decode(self.handle, layer, q, qs, slot, B, T, o, lse, stream)
+
+    def rssm_attn_prefill(self, q, k, v, cu_seqlens, slot, o, cu_keys=None, lse=None,
+                          stream=None):
+        """Causal attention over packed prompts (cu_seqlens int32, B + 1)."""
+        n, qs = self._tokens(q, self.HQ)
+        m, ks = self._tokens(k, self.HKV, n if cu_keys is None else None)
+        _, vs = self._tokens(v, self.HKV, m)
+        self._output(o, n, lse)
+        _lib.rssm_attn_prefill(self.handle, q, k, v, qs, ks, vs, cu_seqlens, cu_keys, slot,
+                               cu_seqlens.numel() - 1, n, m, o, lse, stream)
+
+    def rssm_kv_get_device_error(self, clear=True, stream=None) -> int:
+        return _lib.rssm_kv_get_device_error(self.handle, clear, stream)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _lib.rssm_kv_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # ------------------------------------------------------------- helpers
+    def _tokens(self, x, heads, n=None):
+        """Tokens and token stride of [n, heads, D] (heads and D contiguous)."""
+        shape, stride = x.shape, x.stride()
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.D \
+                or (n is not None and shape[0] != n):
+            raise ValueError(f"expected {n or 'N'} x {heads} x {self.D}, got {tuple(shape)}")
+        if x.dtype != _TORCH[self.dtype] or (stride[2] != 1 or stride[1] != self.D
+                                             and heads > 1):
+            raise ValueError("the cache's dtype, with contiguous heads")
+        return shape[0], stride[0] if shape[0] > 1 else heads * self.D
+
+    def _output(self, o, n, lse=None):
+        if o.dtype != _TORCH[self.dtype] or o.numel() != n * self.HQ * self.D \
+                or not o.is_contiguous():
+            raise ValueError("outputs: contiguous, the cache's dtype, [tokens, HQ, D]")
+        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * self.HQ
+                                or not lse.is_contiguous()):
+            raise ValueError("lse: contiguous fp32 [tokens, HQ]")
