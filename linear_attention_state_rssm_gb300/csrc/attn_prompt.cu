@@ -123,36 +123,31 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant_
 }
 
 template <typename F>
-cudaError_t pick(int D, int dt, F f) {
-#define RSSM_CASE(TT, DD) \
-  if (D == DD) return f(attn_prompt_kernel<TT, DD>, PromptCfg<TT, DD>::SMEM);
-#define RSSM_CASES(TT) RSSM_CASE(TT, 64) RSSM_CASE(TT, 128) RSSM_CASE(TT, 256)
-  if (dt == DT_F32) {
-    RSSM_CASES(float)
-  } else if (dt == DT_BF16) {
-    RSSM_CASES(__nv_bfloat16)
-  } else {
-    RSSM_CASES(__half)
+cudaError_t pick(int D, F f) {
+  switch (D) {
+    case 64: return f(attn_prompt_kernel<float, 64>, PromptCfg<float, 64>::SMEM);
+    case 128: return f(attn_prompt_kernel<float, 128>, PromptCfg<float, 128>::SMEM);
+    case 256: return f(attn_prompt_kernel<float, 256>, PromptCfg<float, 256>::SMEM);
+    default: return cudaErrorInvalidValue;
   }
-#undef RSSM_CASES
-#undef RSSM_CASE
-  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t attn_prompt_prepare(int D, int dt) {
-  return pick(D, dt, [](auto kernel, int smem) {
+  if (dt != DT_F32) return attn_prompt_tc_prepare(D, dt);
+  return pick(D, [](auto kernel, int smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
 }
 
 cudaError_t attn_prompt_launch(const PromptParams& p, cudaStream_t st) {
+  if (p.dt != DT_F32) return attn_prompt_tc_launch(p, st);
   // every sequence has at most one tile that is not full of tokens
   const int toks = 64 / p.G;
   const long long ctas = ((long long)p.N / toks + p.B) * p.HKV;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  return pick(p.D, p.dt, [&](auto kernel, int smem) {
+  return pick(p.D, [&](auto kernel, int smem) {
     kernel<<<(unsigned)ctas, 128, smem, st>>>(p);
     return cudaGetLastError();
   });

@@ -148,5 +148,7 @@ cudaError_t attn_decode_launch(const DecodeParams& p, int D, int dt, int num_sms
 int attn_decode_block_rows(int D, int dt, int rows);  // rows of a block for T G rows
 cudaError_t attn_prompt_prepare(int D, int dt);
 cudaError_t attn_prompt_launch(const PromptParams& p, cudaStream_t st);
+cudaError_t attn_prompt_tc_prepare(int D, int dt);  // 16-bit types
+cudaError_t attn_prompt_tc_launch(const PromptParams& p, cudaStream_t st);
 
 }  // namespace rssm
