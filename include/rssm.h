@@ -577,7 +577,8 @@ rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
  *     o = sum_j softmax_j(scale q . k_j) v_j.
  * q is [B T][HQ][D]. A slot may be named by several rows. A row whose window
  * is not within its pages sets RSSM_DEVERR_PAGES and is skipped; a table entry
- * outside the pool sets it too and counts as keys and values of zero.
+ * outside the pool sets it too and leaves that row's output undefined (nothing
+ * outside the pool is read).
  */
 rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
                              int64_t q_stride, const int32_t *slot, int32_t B,

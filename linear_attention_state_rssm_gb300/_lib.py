@@ -151,18 +151,32 @@ def load() -> ctypes.CDLL:
 
 
 def _ptr(x):
-    """Device pointer of a tensor (None -> NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    """Device pointer of a tensor (None -> NULL, an address -> itself)."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return x
-    return x.data_ptr()
+
+
+def _bind_current_stream():
+    """The current stream's handle without the Stream object that
+    torch.cuda.current_stream() builds around it (2 us of a call's 10)."""
+    global _current_stream
+    import torch
+    torch.cuda.init()
+    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+    def _current_stream():
+        return raw(device())
+    return _current_stream()
+
+
+_current_stream = _bind_current_stream
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

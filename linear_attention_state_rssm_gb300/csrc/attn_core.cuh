@@ -13,9 +13,12 @@
 // is what the tensor cores read (relative error 2^-9 for bf16, independent from
 // weight to weight, below the rounding of the output).
 //
-// Rows of shared memory are D values; 16-byte unit u of row r lies at unit
+// Blocks in shared memory are cut in columns of 128 bytes: row r of a column is
+// 128 bytes after row r - 1, and within it 16-byte unit u lies at unit
 // u ^ (r % 8), so that eight rows' same unit falls in eight different bank
-// groups (ldmatrix and the fp32 loads below are free of conflicts).
+// groups (ldmatrix and the fp32 loads below are free of conflicts). That is
+// what a TMA box of 128 bytes by rows by columns writes under the 128-byte
+// swizzle.
 //
 // A key that a row must not see is left out by selection: its x becomes -inf,
 // so p = 0. That leaves 0 * v, which is not 0 where v is infinite or NaN
@@ -26,6 +29,8 @@
 
 #include <cmath>
 #include <type_traits>
+
+#include <cuda.h>
 
 #include "rssm_common.cuh"
 
@@ -105,18 +110,24 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// byte offset of 16-byte unit u of row r, rows of D values of T
-template <typename T, int D>
+// Tiled TMA loads; the inner coordinate is a multiple of 16 bytes.
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                          int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+// Byte offset of 16-byte unit u of row r in a block of ROWS rows.
+template <int ROWS>
 __device__ __forceinline__ uint32_t unit_off(int r, int u) {
-  return (uint32_t)r * (D * (uint32_t)sizeof(T)) + (uint32_t)((u ^ (r & 7)) << 4);
+  return (uint32_t)((u >> 3) * (ROWS * 128) + r * 128 + (((u ^ r) & 7) << 4));
 }
-template <typename T, int D>
-__device__ __forceinline__ const T& elem(const unsigned char* base, int r, int d) {
-  constexpr int E = 16 / (int)sizeof(T);
-  return *reinterpret_cast<const T*>(base + unit_off<T, D>(r, d / E) + (d % E) * sizeof(T));
-}
-
-template <typename T, int D, int MB>
+// MB blocks of 16 rows; QR, KR: rows of the query block and of a block of keys
+// in shared memory (their columns' heights); a chunk is one block of keys or
+// several on end.
+template <typename T, int D, int MB, int QR, int KR>
 struct WarpAttn {
   static constexpr bool F32 = std::is_same<T, float>::value;
   // lane (g, t) = (lane / 4, lane % 4): columns col(i, t), + 1 of rows g (first
@@ -128,8 +139,16 @@ struct WarpAttn {
   static __device__ __forceinline__ int col(int i, int t) {
     return F32 ? 16 * (i >> 1) + 4 * t + 2 * (i & 1) : 8 * i + 2 * t;
   }
+  // 16-byte unit u of key r of a chunk
+  static __device__ __forceinline__ uint32_t key_off(int r, int u) {
+    return (uint32_t)(r / KR) * (KR * D * (uint32_t)sizeof(T)) + unit_off<KR>(r % KR, u);
+  }
+  static __device__ __forceinline__ float4 key4(const unsigned char* base, int r, int u) {
+    return *reinterpret_cast<const float4*>(base + key_off(r, u));
+  }
+  template <int ROWS>
   static __device__ __forceinline__ float4 vec4(const unsigned char* base, int r, int u) {
-    return *reinterpret_cast<const float4*>(base + unit_off<float, D>(r, u));
+    return *reinterpret_cast<const float4*>(base + unit_off<ROWS>(r, u));
   }
 
   __device__ __forceinline__ void clear() {
@@ -164,14 +183,14 @@ struct WarpAttn {
         float4 q[MB][2];
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
-          q[b][0] = vec4(qs, 16 * b + g, u);
-          q[b][1] = vec4(qs, 16 * b + g + 8, u);
+          q[b][0] = vec4<QR>(qs, 16 * b + g, u);
+          q[b][1] = vec4<QR>(qs, 16 * b + g + 8, u);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float4 k = vec4(ks, 8 * n + 2 * t + e, u);
+            const float4 k = key4(ks, 8 * n + 2 * t + e, u);
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
 #pragma unroll
@@ -195,11 +214,11 @@ struct WarpAttn {
         uint32_t kf[NT / 2][4];
 #pragma unroll
         for (int n = 0; n < NT / 2; ++n)
-          ldsm4(kf[n], kb + unit_off<T, D>(16 * n + (i >> 1) * 8 + r, 2 * kk + (i & 1)));
+          ldsm4(kf[n], kb + key_off(16 * n + (i >> 1) * 8 + r, 2 * kk + (i & 1)));
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
           uint32_t a[4];
-          ldsm4(a, qb + unit_off<T, D>(16 * b + (i & 1) * 8 + r, 2 * kk + (i >> 1)));
+          ldsm4(a, qb + unit_off<QR>(16 * b + (i & 1) * 8 + r, 2 * kk + (i >> 1)));
 #pragma unroll
           for (int n = 0; n < NT / 2; ++n) {
             mma16<T>(x[b][2 * n], a, kf[n][0], kf[n][1]);
@@ -229,7 +248,7 @@ struct WarpAttn {
           }
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
-            const float4 v = vec4(vs, 8 * n + j, 4 * i + t);
+            const float4 v = key4(vs, 8 * n + j, 4 * i + t);
 #pragma unroll
             for (int b = 0; b < MB; ++b) {
 #pragma unroll
@@ -261,7 +280,7 @@ struct WarpAttn {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
           uint32_t vf[4];
-          ldsm4_t(vf, vb + unit_off<T, D>(16 * n + (i & 1) * 8 + r, 2 * d + (i >> 1)));
+          ldsm4_t(vf, vb + key_off(16 * n + (i & 1) * 8 + r, 2 * d + (i >> 1)));
 #pragma unroll
           for (int b = 0; b < MB; ++b) {
             mma16<T>(o[b][2 * d], a[b], vf[0], vf[1]);
@@ -277,27 +296,28 @@ struct WarpAttn {
   __device__ __forceinline__ void pv_select(const float (&p)[MB][NT][4], const unsigned char* vs,
                                          int key0, const int (&lim)[MB][2], int lane) {
     const int t = lane & 3;
-    for (int j = 0; j < 8 * NT; ++j) {
-      const int from = (lane & ~3) | ((j & 7) >> 1);
 #pragma unroll
-      for (int b = 0; b < MB; ++b) {
-        float p0 = 0.f, p1 = 0.f;
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        const int from = (lane & ~3) | (j >> 1), key = 8 * n + j;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n == j >> 3) {
-            p0 = (j & 1) ? p[b][n][1] : p[b][n][0];
-            p1 = (j & 1) ? p[b][n][3] : p[b][n][2];
+        for (int b = 0; b < MB; ++b) {
+          // both of the holder's two, then one of them: an index that is not
+          // known when compiling would put p into local memory for every use
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = __shfl_sync(kFull, p[b][n][e], from);
+          const float p0 = (j & 1) ? w[1] : w[0], p1 = (j & 1) ? w[3] : w[2];
+          const bool s0 = key0 + key < lim[b][0], s1 = key0 + key < lim[b][1];
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            constexpr int E = 16 / (int)sizeof(T);  // col(i, t) is even: two of one unit
+            const T* v = reinterpret_cast<const T*>(vs + key_off(key, col(i, t) / E)) + col(i, t) % E;
+            const float v0 = attn_f32(v[0]), v1 = attn_f32(v[1]);
+            if (s0) o[b][i][0] = fmaf(p0, v0, o[b][i][0]), o[b][i][1] = fmaf(p0, v1, o[b][i][1]);
+            if (s1) o[b][i][2] = fmaf(p1, v0, o[b][i][2]), o[b][i][3] = fmaf(p1, v1, o[b][i][3]);
           }
-        }
-        p0 = __shfl_sync(kFull, p0, from);
-        p1 = __shfl_sync(kFull, p1, from);
-        const bool s0 = key0 + j < lim[b][0], s1 = key0 + j < lim[b][1];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const float v0 = attn_f32(elem<T, D>(vs, j, col(i, t)));
-          const float v1 = attn_f32(elem<T, D>(vs, j, col(i, t) + 1));
-          if (s0) o[b][i][0] = fmaf(p0, v0, o[b][i][0]), o[b][i][1] = fmaf(p0, v1, o[b][i][1]);
-          if (s1) o[b][i][2] = fmaf(p1, v0, o[b][i][2]), o[b][i][3] = fmaf(p1, v1, o[b][i][3]);
         }
       }
     }
@@ -378,13 +398,12 @@ struct WarpAttn {
     }
   }
 
-  // o += p v. Keys from `end` on are zeros and seen by no row, so those that
-  // some rows see and others do not lie in [all, end).
+  // o += p v
   template <int NT>
   __device__ __forceinline__ void add(const float (&p)[MB][NT][4], const unsigned char* vs,
-                                      int key0, const int (&lim)[MB][2], int all, int end,
-                                      int lane) {
-    if (key0 + 8 * NT > all && all < end && key0 < end && any_unfinite<NT>(vs, lane)) {
+                                      int key0, const int (&lim)[MB][2], int all, int lane) {
+    static_assert(8 * NT % KR == 0, "whole blocks of keys");
+    if (key0 + 8 * NT > all && any_unfinite<NT>(vs, lane)) {
       pv_select<NT>(p, vs, key0, lim, lane);
     } else {
       pv<NT>(p, vs, lane);

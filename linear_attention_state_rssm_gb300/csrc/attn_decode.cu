@@ -3,45 +3,65 @@
 // For row r with slot s: query token t (its key and value already appended at
 // cache position length[s] + t) sees the cache positions 0 .. length[s] + t.
 // The T G query rows of one key head (G query heads share it) form blocks of
-// 16 MB rows; a block reads the keys and values of its head once, from HBM.
+// 16, 32 or 64 rows (48 for D = 256); a block reads the keys and values of its head once.
 //
 // Bytes bound it: 2 D values per key and head, 2 T G D products with them. So
-// the loads have to be many and wide, and the work has to be even whatever the
-// lengths: the tiles (128 keys) of every (row, key head, block) are laid on
-// one line, and each CTA of one wave takes an equal stretch of it. A stretch
-// that begins or ends inside a row leaves a part (running maximum, sum and
-// unnormalised output) in the work buffer; the last CTA to leave one for a row
-// joins them, in the order of the keys whoever it is, so results do not depend
-// on the order of arrival.
+// the loads have to be wide, many, and never pause, and the work has to be even
+// whatever the lengths. The chunks (16 or 32 keys) of every (row, key head,
+// block) are laid on one line, each row's behind a gap that stands for what it
+// costs to begin and end one, and each CTA of one wave takes an equal
+// stretch of the line. A stretch that begins or ends inside a row leaves a part
+// (running maximum, sum and unnormalised output) in the work buffer; the last
+// CTA to leave one for a row joins them, in the order of the keys whoever it
+// is, so results do not depend on the order of arrival.
 //
-// Within a CTA each warp streams its own chunks of 16 keys (chunk w, w + NW,
-// ...) through a private ring of shared memory by 16-byte async copies, keys
-// and values as separate units; no barrier between warps until the row ends.
+// In a CTA one producer warp walks the stretch ahead of the others, over the
+// ends of rows too: it looks the pages up and has one thread issue one TMA box
+// per 16 keys and one per 16 values into a ring. Each stream (one
+// warp per 16 rows of the block) takes every NG-th chunk of the CTA; streams meet only
+// where a row ends, while the ring fills with the next row's chunks.
 #include "attn_core.cuh"
+#include "attn_tma.h"
 #include "kv_common.cuh"
 
 namespace rssm {
 
 namespace {
 
-constexpr int kChunk = 16;  // keys of a warp's step: within one page (pages of 16 k keys)
+constexpr int kBox = 16;        // keys of a TMA box: within one page (pages of 16 k keys)
+constexpr int kGapKeys = 256;   // what beginning and ending a row costs, as keys
+constexpr int kLeastKeys = 512; // keys that a CTA takes at least (of longer rows)
+constexpr int kRowParts = 96;   // parts of the longest row, about: one CTA joins them
 
-template <typename T, int D, int MB>
+template <typename T, int D, int MW>
 struct DecCfg {
-  static constexpr int NW = std::is_same<T, float>::value && D == 256 ? 4 : 8;
-  static constexpr int NT = NW * 32;
-  static constexpr int ROWS = 16 * MB;
-  static constexpr int TILE = kChunk * NW;             // keys of a tile
-  static constexpr int UNIT = kChunk * D * (int)sizeof(T);
-  static constexpr int NS = 196608 / NW / UNIT;        // units in a warp's ring
-  static constexpr int RING = NS * UNIT;               // bytes per warp
+  static constexpr bool F32 = std::is_same<T, float>::value;
+  // Outputs live in registers, D / 2 a lane: seven warps of 255 registers for
+  // D = 256, ten of 168 for 128, fifteen of 128 for 64 (eight of 255 for fp32,
+  // whose FMAs want more). A quarter of the registers belongs to each quarter
+  // of the SM. Where they suffice a step takes 32 keys: what a step costs
+  // whatever its size (waits, maxima over lanes) is most of it.
+  static constexpr int CPS = D == 256 ? 1 : F32 || D == 128 ? 2 : 3;  // CTAs per SM
+  static constexpr int NW = F32 ? (D == 256 ? 4 : 3) : D == 256 ? 6 : 4;
+  static constexpr int CH = F32 || D == 256 ? 16 : 32;  // keys of a chunk
+  static constexpr int GAP = kGapKeys / CH;
+  static constexpr int CT = NW * 32;                   // threads of the streams
+  static constexpr int NT = CT + 32;                   // and the producer warp
+  static constexpr int NG = NW / MW;                   // streams of a CTA
+  static constexpr int ROWS = 16 * MW;
+  static constexpr int UNIT = CH * D * (int)sizeof(T);
   static constexpr int QBYTES = ROWS * D * (int)sizeof(T);
-  static constexpr int OP = D + 8;                     // row pitch of the warps' outputs (floats)
-  static constexpr int STATS = 2 * NW * ROWS * 4;      // every warp's m and l
-  static constexpr int SMEM = NW * RING + QBYTES + STATS + ROWS * 8 + 256;
-  static_assert(NS >= 3, "keys, values and the next keys");
-  static_assert(NW * ROWS * OP * 4 <= NW * RING, "the warps' outputs fit the ring");
-  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static constexpr int OP = 72;                        // row pitch of 64 columns of outputs
+  static constexpr int OBYTES = NG > 1 ? NG * ROWS * OP * 4 : 0;
+  static constexpr int REST = 1024 + 2 * QBYTES + OBYTES + 2 * NG * ROWS * 4 + ROWS * 8 + 1024;
+  static constexpr int MOST = (228 / CPS - 1) * 1024;  // a CTA's share of the SM
+  static_assert(NW % MW == 0, "whole streams");
+  static constexpr int FIT = (MOST - REST) / UNIT;
+  static constexpr int NU = FIT < 32 ? FIT : 32;       // units in the ring
+  static constexpr int SMEM = NU * UNIT + REST;
+  static constexpr int PART = ROWS * (D + 2);          // floats of a part
+  static_assert(NU >= 2 * NG, "a chunk for each stream");
+  static_assert(CPS * kMaxSms * 2 * PART <= kPartFloats, "work buffer");
 };
 
 // keys of row r (committed and new), 0 for a null or refused row
@@ -67,6 +87,12 @@ __device__ __forceinline__ int row_keys(const DecodeParams& p, int r, bool tell,
   return n;
 }
 
+// places of a row's chunks of CH keys on the line, with the gap before them
+template <int CH>
+__device__ __forceinline__ long long places(int keys) {
+  return keys > 0 ? ((long long)keys + CH - 1) / CH + kGapKeys / CH : 0;
+}
+
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -76,361 +102,557 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
   return x;
 }
 
-template <typename T, int D, int MB>
-__global__ void __launch_bounds__(DecCfg<T, D, MB>::NT, 1)
-    attn_decode_kernel(const __grid_constant__ DecodeParams p) {
-  using C = DecCfg<T, D, MB>;
-  constexpr int NW = C::NW;
-  extern __shared__ __align__(1024) unsigned char sm[];
-  unsigned char* qs = sm + NW * C::RING;
-  float* sm_m = reinterpret_cast<float*>(qs + C::QBYTES);  // [NW][ROWS]
-  float* sm_l = sm_m + NW * C::ROWS;
-  float* row_m = sm_l + NW * C::ROWS;                      // [ROWS]
-  float* row_l = row_m + C::ROWS;
-  long long* scan = reinterpret_cast<long long*>(row_l + C::ROWS);  // [NW + 3]
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char* ring = sm + warp * C::RING;
-  const int items = p.HKV * p.nmb;
-  const size_t head_bytes = ((size_t)D * sizeof(T)) << p.shift;   // one head of a page
-  const size_t page_bytes = head_bytes * p.HKV;
+// A stretch of one (row, key head, block): chunks [c0, c1).
+struct Seg {
+  int row, slot, keys, h, mb, c0, c1, chunks;
+  long long item0;  // place of its first chunk on the line
+  int more, pad;    // 0: the stretch is done
+};
 
-  // ---- this CTA's stretch of the line of tiles
-  long long mine = 0;
+// The CTA's stretch of the line, one Seg after the other.
+template <int CH>
+struct Line {
+  static constexpr int kGap = kGapKeys / CH;
+  long long pos, end, row0;
+  int row;
+  __device__ __forceinline__ bool next(const DecodeParams& p, Seg& g) {
+    const int items = p.HKV * p.nmb;
+    while (pos < end) {
+      g.keys = row_keys(p, row, false, g.slot);
+      const int cost = (int)places<CH>(g.keys);
+      if (pos >= row0 + (long long)cost * items) {
+        row0 += (long long)cost * items;
+        ++row;
+        continue;
+      }
+      const int item = (int)((pos - row0) / cost);
+      const int off = (int)((pos - row0) % cost);
+      const int len = (long long)cost - off <= end - pos ? cost - off : (int)(end - pos);
+      g.row = row;
+      g.h = item / p.nmb;
+      g.mb = item % p.nmb;
+      g.chunks = cost - kGap;
+      g.c0 = max(0, off - kGap);
+      g.c1 = max(0, off + len - kGap);
+      g.item0 = row0 + (long long)item * cost + kGap;
+      pos += len;
+      if (g.c1 > g.c0) return true;
+    }
+    return false;
+  }
+};
+
+struct KvMaps {
+  CUtensorMap k, v;
+};
+
+template <typename T, int D, int MW>
+__global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
+    attn_decode_kernel(const __grid_constant__ DecodeParams p,
+                       const __grid_constant__ KvMaps maps) {
+  using C = DecCfg<T, D, MW>;
+  constexpr int NG = C::NG, NW = C::NW;
+  extern __shared__ unsigned char sm_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
+  unsigned char* qs = ring + C::NU * C::UNIT;                  // [2][QBYTES]
+  float* os = reinterpret_cast<float*>(qs + 2 * C::QBYTES);    // [NG][ROWS][OP]
+  float* sm_m = os + C::OBYTES / 4;                            // [NG][ROWS]
+  float* sm_l = sm_m + NG * C::ROWS;
+  float* row_m = sm_l + NG * C::ROWS;                          // [ROWS]
+  float* row_l = row_m + C::ROWS;
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_l + C::ROWS);  // [NU] a unit has landed
+  uint64_t* empty = full + C::NU;                              // [NU] its stream has read it
+  uint64_t* qfull = empty + C::NU;                             // [2] a segment is described
+  uint64_t* qempty = qfull + 2;                                // [2] and done
+  long long* scan = reinterpret_cast<long long*>(qempty + 2);  // [3 (NW + 1) + 2]
+  Seg* segs = reinterpret_cast<Seg*>(scan + 3 * (NW + 1) + 3); // [2]
+  volatile int* issued = reinterpret_cast<volatile int*>(segs + 2);  // units on their way
+  int* flag = const_cast<int*>(issued) + 1;  // [4] no output; joins; a wait ran out (by turns)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], 1), mbar_init(&empty[u], MW);
+    for (int i = 0; i < 2; ++i) mbar_init(&qfull[i], 33), mbar_init(&qempty[i], NW);
+    *issued = 0;
+    for (int i = 0; i < 4; ++i) flag[i] = 0;
+    fence_mbar_init();
+  }
+  // ---- the line's length and its longest row, and the row that holds this
+  // CTA's first place: one look at the lengths for up to NT rows, else two
+  const int items = p.HKV * p.nmb;
+  long long mine = 0, most = 0, first_w = 0;
   for (int r = tid; r < p.B; r += C::NT) {
     int s;
-    const int n = row_keys(p, r, blockIdx.x == 0, s);
-    mine += (n + C::TILE - 1) / C::TILE;
+    const long long w = places<C::CH>(row_keys(p, r, blockIdx.x == 0, s)) * items;
+    if (r < C::NT) first_w = w;
+    mine += w;
+    most = w > most ? w : most;
   }
+  const long long first_incl = warp_scan(first_w, lane);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(kFull, mine, d);
-  if (lane == 0) scan[warp] = mine;
+  for (int d = 16; d > 0; d >>= 1) {
+    mine += __shfl_xor_sync(kFull, mine, d);
+    const long long y = __shfl_xor_sync(kFull, most, d);
+    most = y > most ? y : most;
+  }
+  if (lane == 31) {
+    scan[warp] = mine;
+    scan[NW + 1 + warp] = most;
+    scan[2 * (NW + 1) + warp] = first_incl;
+  }
   __syncthreads();
-  long long total = 0;
-  for (int w = 0; w < NW; ++w) total += scan[w];
-  __syncthreads();
-  total *= items;
-  const long long share = (total + gridDim.x - 1) / gridDim.x;
-  long long pos = share * blockIdx.x;
-  const long long end = pos + share < total ? pos + share : total;
-  if (pos >= end) return;
-
-  // ---- the row that holds tile `pos`
-  int row = 0;
-  long long row0 = 0;  // its first tile
-  for (int r0 = 0; r0 < p.B; r0 += C::NT) {
-    const int r = r0 + tid;
-    int s, n = 0;
-    if (r < p.B) n = row_keys(p, r, false, s);
-    const long long w = (long long)((n + C::TILE - 1) / C::TILE) * items;
+  long long total = 0, longest = 0, at = 0, firsts = 0;
+  for (int w = 0; w <= NW; ++w) {
+    total += scan[w];
+    longest = scan[NW + 1 + w] > longest ? scan[NW + 1 + w] : longest;
+    if (w < warp) at += scan[2 * (NW + 1) + w];
+    firsts += scan[2 * (NW + 1) + w];
+  }
+  long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long few = longest / items / kRowParts + 1;
+  share = share > few ? share : few;
+  // not less than kLeastKeys, or a whole row where the longest has fewer
+  const long long row_cost = longest / items;
+  const long long least =
+      row_cost < C::GAP + kLeastKeys / C::CH ? row_cost : C::GAP + kLeastKeys / C::CH;
+  share = share > least ? share : least;
+  Line<C::CH> line;
+  line.pos = share * blockIdx.x;
+  line.end = line.pos + share < total ? line.pos + share : total;
+  if (line.pos >= line.end) return;
+  at += first_incl - first_w;
+  long long* found = scan + 3 * (NW + 1);  // row, its first place
+  if (at <= line.pos && line.pos < at + first_w) {
+    found[0] = tid;
+    found[1] = at;
+  }
+  long long before = firsts;
+  for (int r0 = C::NT; r0 < p.B && before <= line.pos; r0 += C::NT) {
+    int s;
+    const long long w =
+        r0 + tid < p.B ? places<C::CH>(row_keys(p, r0 + tid, false, s)) * items : 0;
     const long long incl = warp_scan(w, lane);
+    __syncthreads();  // the last sums have been read
     if (lane == 31) scan[warp] = incl;
-    if (tid == 0) scan[NW] = -1;
     __syncthreads();
-    long long at = row0 + incl - w;
-    for (int i = 0; i < warp; ++i) at += scan[i];
-    if (at <= pos && pos < at + w) {
-      scan[NW] = r;
-      scan[NW + 1] = at;
+    long long first = before + incl - w;
+    for (int i = 0; i <= NW; ++i) {
+      if (i < warp) first += scan[i];
+      before += scan[i];
     }
-    long long sum = 0;
-    for (int i = 0; i < NW; ++i) sum += scan[i];
-    __syncthreads();
-    const long long found = scan[NW];
-    if (found >= 0) {
-      row = (int)found;
-      row0 = scan[NW + 1];
-      break;
+    if (first <= line.pos && line.pos < first + w) {
+      found[0] = r0 + tid;
+      found[1] = first;
     }
-    row0 += sum;
-    __syncthreads();
   }
   __syncthreads();
+  line.row = (int)found[0];
+  line.row0 = found[1];
 
-  while (pos < end) {
-    int slot;
-    const int keys = row_keys(p, row, false, slot);
-    const int tiles = (keys + C::TILE - 1) / C::TILE;
-    if (tiles == 0) {
-      ++row;
-      continue;
+  const long long begin = line.pos;
+  bool dead = false;  // a bounded wait ran out
+  if (warp == NW) {
+    // ---- producer
+    Seg sg;
+    int n = 0, ns = 0;  // chunks and segments issued
+    while (!dead) {
+      sg.more = line.next(p, sg);
+      // the segment's description and its query rows (zeros after the last),
+      // into the half that the segment before the last has left
+      const int half = ns & 1;
+      if (ns >= 2) dead = !mbar_wait_bounded(&qempty[half], (uint32_t)((ns / 2 - 1) & 1));
+      dead = __any_sync(kFull, dead);
+      if (dead) break;
+      if (lane == 1) {  // lane 0 has bulk copies on their way, which a release would wait for
+        segs[half] = sg;
+        mbar_arrive(&qfull[half]);
+      }
+      if (sg.more) {
+        constexpr int QU = D * (int)sizeof(T) / 16;  // units per row
+        const int base = sg.mb * C::ROWS, R = min(C::ROWS, p.T * p.G - base);
+        const uint32_t qd = smem_addr(qs + half * C::QBYTES);
+#pragma unroll 4
+        for (int i = lane; i < C::ROWS * QU; i += 32) {
+          const int rr = i / QU, u = i % QU;
+          const int tr = base + (rr < R ? rr : 0);
+          const T* q = static_cast<const T*>(p.q) + ((long long)sg.row * p.T + tr / p.G) * p.qs +
+                       (long long)(sg.h * p.G + tr % p.G) * D;
+          cp_async16_or_zero(qd + unit_off<C::ROWS>(rr, u), reinterpret_cast<const uint4*>(q) + u,
+                             rr < R);
+        }
+      }
+      __syncwarp();
+      cp_async_arrive(&qfull[half]);
+      ++ns;
+      if (!sg.more) break;
+      const int32_t* tab = p.table + (size_t)sg.slot * p.max_pages;
+      // the boxes of the segment's chunks, 32 looked up at a time
+      constexpr int BPC = C::CH / kBox;  // boxes of a chunk
+      const int b_end = min(sg.c1 * BPC, (sg.keys + kBox - 1) / kBox);
+      for (int cb = sg.c0; cb < sg.c1 && !dead; cb += 32 / BPC) {
+        const int box = cb * BPC + lane;
+        int row = -1;  // of the pool: ((layer pages + page) HKV + head) page_size + token
+        if (box < b_end) {
+          const long long tok = (long long)box * kBox;
+          int page = tab[tok >> p.shift];
+          if (page < 0 || page >= p.n_pages) {
+            page = 0;  // the row's output is undefined; nothing outside the pool is read
+            atomicOr(p.err, DEVERR_PAGES);
+          }
+          row = (int)((((p.page0 + page) * p.HKV + sg.h) << p.shift) +
+                      (tok & ((1 << p.shift) - 1)));
+        }
+        const int cnt = min(32 / BPC, sg.c1 - cb);
+        for (int i = 0; i < cnt; ++i) {
+          int at_row[BPC];
+#pragma unroll
+          for (int b = 0; b < BPC; ++b) at_row[b] = __shfl_sync(kFull, row, i * BPC + b);
+          if (lane == 0) {
+            // a box behind the last key is not loaded: the one before it stands
+            // in its place, and no row sees it
+            int boxes = 0;
+#pragma unroll
+            for (int b = 0; b < BPC; ++b) boxes += at_row[b] >= 0;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const int u = 2 * n + kv, at_u = u % C::NU;
+              if (!dead && u >= C::NU &&
+                  !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1)))
+                dead = true;
+              if (!dead) {
+                mbar_expect_tx(&full[at_u], C::UNIT);
+#pragma unroll
+                for (int b = 0; b < BPC; ++b)
+                  tma_load3(smem_addr(ring + at_u * C::UNIT + b * (C::UNIT / BPC)),
+                            kv == 0 ? &maps.k : &maps.v, 0, at_row[b < boxes ? b : 0], 0,
+                            &full[at_u]);
+              }
+            }
+            if (!dead) *issued = 2 * n + 2;
+          }
+          ++n;
+        }
+        dead = __any_sync(kFull, dead);
+      }
     }
-    if (pos >= row0 + (long long)tiles * items) {
-      row0 += (long long)tiles * items;
-      ++row;
-      continue;
+    // every copy has landed before the CTA leaves
+    if (lane == 0) {
+      for (int u = max(0, 2 * n - C::NU); u < 2 * n && !dead; ++u)
+        dead = !mbar_wait_bounded(&full[u % C::NU], (uint32_t)((u / C::NU) & 1));
+      if (dead) atomicOr(p.err, DEVERR_TIMEOUT);
     }
-    const int item = (int)((pos - row0) / tiles);
-    const int t0 = (int)((pos - row0) % tiles);
-    const long long item0 = row0 + (long long)item * tiles;
-    const int t1 = (long long)tiles - t0 <= end - pos ? tiles : t0 + (int)(end - pos);
-    const int h = item / p.nmb, mb = item % p.nmb;
-    const int base = mb * C::ROWS;                     // first of the block's T G rows
+    return;
+  }
+
+  // ---- streams
+  const int grp = warp / MW, wr = 16 * (warp % MW);  // the warp's stream, its first row
+  const int g = lane >> 2, tq = lane & 3;
+  int n0 = 0;    // the segment's first chunk among the CTA's
+  int seen = 0;  // units known to be on their way
+  for (int ns = 0;; ++ns) {
+    const int half = ns & 1;
+    // The streams meet at barriers, so they stop together: a wait that ran out
+    // is told here, by turns in two places (the next turn's word is written
+    // only once every stream has read this one's).
+    dead = dead || !mbar_wait_bounded(&qfull[half], (uint32_t)((ns >> 1) & 1));
+    if (dead) flag[2 + half] = 1;
+    named_sync(1, C::CT);
+    const Seg sg = segs[half];
+    if (flag[2 + half] != 0 || !sg.more) break;
+    const int base = sg.mb * C::ROWS;                  // first of the block's T G rows
     const int R = min(C::ROWS, p.T * p.G - base);      // rows in use
-
-    // ---- query rows (zeros behind the last)
-    constexpr int QU = D * (int)sizeof(T) / 16;        // units per row
-    for (int i = tid; i < C::ROWS * QU; i += C::NT) {
-      const int rr = i / QU, u = i % QU;
-      const bool live = rr < R;
-      const int tr = live ? base + rr : 0;
-      const T* q = static_cast<const T*>(p.q) + ((long long)row * p.T + tr / p.G) * p.qs +
-                   (long long)(h * p.G + tr % p.G) * D;
-      *reinterpret_cast<uint4*>(qs + unit_off<T, D>(rr, u)) =
-          live ? reinterpret_cast<const uint4*>(q)[u] : make_uint4(0, 0, 0, 0);
-    }
-    __syncthreads();
-
-    // ---- how many keys the lane's rows see
-    const int first = keys - p.T;  // committed keys
-    int lim[MB][2];
+    // how many keys the lane's rows see
+    const int first = sg.keys - p.T;  // committed keys
+    int lim[1][2];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = min(16 * b + 8 * e + (lane >> 2), R - 1);
-        lim[b][e] = first + (base + rr) / p.G + 1;
-      }
-    }
-    const int fewest = first + base / p.G + 1;
-
-    // ---- the warp's stream: chunks t0 NW + warp, + NW, ... below t1 NW
-    const int c0 = t0 * NW + warp;
-    const int c_end = min(t1 * NW, (keys + kChunk - 1) / kChunk);
-    const int nc = c0 < c_end ? (c_end - c0 + NW - 1) / NW : 0;
-    const int32_t* tab = p.table + (size_t)slot * p.max_pages;
-    WarpAttn<T, D, MB> w;
+    for (int e = 0; e < 2; ++e)
+      lim[0][e] = first + (base + min(wr + 8 * e + g, R - 1)) / p.G + 1;
+    const int fewest = first + (base + min(wr, R - 1)) / p.G + 1;
+    WarpAttn<T, D, 1, C::ROWS, kBox> w;
     w.clear();
-    int page = nc > 0 ? tab[(c0 * kChunk) >> p.shift] : 0;
-    const unsigned char* at = nullptr;  // the chunk's first key within the pool
-    bool known = false;
-    auto issue = [&](int u) {  // unit u: keys (even) or values (odd) of chunk u / 2
-      if (u < 2 * nc) {
-        const int key0 = (c0 + (u >> 1) * NW) * kChunk;
-        if ((u & 1) == 0) {
-          known = page >= 0 && page < p.n_pages;
-          if (!known && lane == 0) atomicOr(p.err, DEVERR_PAGES);
-          const size_t off = (size_t)(known ? page : 0) * page_bytes + h * head_bytes +
-                             (size_t)(key0 & ((1 << p.shift) - 1)) * (D * sizeof(T));
-          at = p.kp + off;
-          if ((u >> 1) + 1 < nc) page = tab[(key0 + NW * kChunk) >> p.shift];
-        } else {
-          at = p.vp + (at - p.kp);
-        }
-        const uint32_t dst = smem_addr(ring + (u % C::NS) * C::UNIT);
-        const int live = known ? keys - key0 : 0;
-#pragma unroll 8
-        for (int i = lane; i < kChunk * QU; i += 32) {
-          const int rr = i / QU, un = i % QU;
-          cp_async16_or_zero(dst + unit_off<T, D>(rr, un), at + (size_t)i * 16, rr < live);
+    const unsigned char* qw = qs + half * C::QBYTES + wr * 128;
+
+    // A slot serves one stream's unit after another's, and copies may land out
+    // of order. A parity tells a phase only from its neighbours: so a stream
+    // first sees that its unit is on its way, which the producer says after
+    // the slot's last unit was read, then that it has landed.
+    auto landed = [&](int u) {
+      if (u >= seen && (seen = *issued) <= u) {
+        const unsigned long long t0 = global_ns();
+        while ((seen = *issued) <= u) {
+          if (global_ns() - t0 > kWaitLimitNs) return false;
         }
       }
-      cp_async_commit();
+      return mbar_wait_bounded(&full[u % C::NU], (uint32_t)((u / C::NU) & 1));
     };
-#pragma unroll
-    for (int u = 0; u < C::NS; ++u) issue(u);
-    for (int i = 0; i < nc; ++i) {
-      // one group per unit: the oldest has landed when NS - 1 are on their way
-      const int key0 = (c0 + i * NW) * kChunk;
-      float x[MB][2][4];
-      cp_async_wait<C::NS - 1>();
+    const int nc = sg.c1 - sg.c0;
+    for (int i = (grp + NG - n0 % NG) % NG; i < nc && !dead; i += NG) {
+      const int key0 = (sg.c0 + i) * C::CH, u = 2 * (n0 + i);
+      const int uk = u % C::NU, uv = (u + 1) % C::NU;
+      float x[1][C::CH / 8][4];
+      dead = !landed(u);
+      w.template weights<C::CH / 8>(x, qw, ring + uk * C::UNIT, key0, lim, fewest, p.c, lane);
       __syncwarp();
-      w.template weights<2>(x, qs, ring + ((2 * i) % C::NS) * C::UNIT, key0, lim, fewest, p.c,
-                            lane);
-      __syncwarp();
-      issue(2 * i + C::NS);
-      cp_async_wait<C::NS - 1>();
-      __syncwarp();
-      w.template add<2>(x, ring + ((2 * i + 1) % C::NS) * C::UNIT, key0, lim, fewest, keys, lane);
-      __syncwarp();
-      issue(2 * i + 1 + C::NS);
+      if (lane == 0) mbar_arrive(&empty[uk]);
+      dead |= !landed(u + 1);
+      w.template add<C::CH / 8>(x, ring + uv * C::UNIT, key0, lim, fewest, lane);
+      dead = __any_sync(kFull, dead);
+      if (lane == 0) mbar_arrive(&empty[uv]);
     }
-    cp_async_wait<0>();
+    n0 += nc;
     w.finish();
 
-    // ---- join the warps
-    const int g = lane >> 2, tq = lane & 3;
-    if (tq == 0) {
-#pragma unroll
-      for (int b = 0; b < MB; ++b) {
+    if (dead) flag[0] = 1;  // no output from here on
+
+    // ---- join the streams
+    const bool whole = sg.c0 == 0 && sg.c1 == sg.chunks;
+    const bool head = sg.item0 < begin;  // the row began in an earlier CTA
+    float* part = p.part + (size_t)(2 * blockIdx.x + (head ? 0 : 1)) * C::PART;
+    auto out_row = [&](int rr) {
+      const int tr = base + rr;
+      return ((size_t)sg.row * p.T + tr / p.G) * p.HQ + sg.h * p.G + tr % p.G;
+    };
+    float f[2], inv[2];
+    if constexpr (NG > 1) {
+      if (tq == 0) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sm_m[warp * C::ROWS + 16 * b + 8 * e + g] = w.m[b][e];
-          sm_l[warp * C::ROWS + 16 * b + 8 * e + g] = w.l[b][e];
+          sm_m[grp * C::ROWS + wr + 8 * e + g] = w.m[0][e];
+          sm_l[grp * C::ROWS + wr + 8 * e + g] = w.l[0][e];
+        }
+      }
+      named_sync(1, C::CT);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = wr + 8 * e + g;
+      float mx = w.m[0][e], sum = w.l[0][e];
+      f[e] = 1.f;
+      if constexpr (NG > 1) {
+#pragma unroll
+        for (int k = 0; k < NG; ++k) mx = fmaxf(mx, sm_m[k * C::ROWS + rr]);
+        const float mu = mx == kNegInf ? 0.f : mx;
+        f[e] = exp2_fast(w.m[0][e] - mu);
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < NG; ++k)
+          sum += sm_l[k * C::ROWS + rr] * exp2_fast(sm_m[k * C::ROWS + rr] - mu);
+      }
+      inv[e] = 1.f / sum;
+      if (grp == 0 && tq == 0 && rr < R) {
+        row_l[rr] = inv[e];
+        if (!whole) {
+          part[C::ROWS * D + rr] = mx;
+          part[C::ROWS * (D + 1) + rr] = sum;
+        } else if (p.lse != nullptr && !dead) {
+          p.lse[out_row(rr)] = lse_of(mx, sum);
         }
       }
     }
-    __syncthreads();  // statistics written; every warp is done with its ring
-    float* ow = reinterpret_cast<float*>(sm) + warp * C::ROWS * C::OP;
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
+    if constexpr (NG == 1) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int rr = 16 * b + 8 * e + g;
-        if (rr < R) {
-          float mx = kNegInf;
-#pragma unroll
-          for (int k = 0; k < NW; ++k) mx = fmaxf(mx, sm_m[k * C::ROWS + rr]);
-          const float mu = mx == kNegInf ? 0.f : mx;
-          const float f = exp2_fast(w.m[b][e] - mu);
+        const int rr = wr + 8 * e + g;
+        if (rr < R && !dead) {
+          T* o = static_cast<T*>(p.o) + out_row(rr) * D;
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
-            *reinterpret_cast<float2*>(ow + rr * C::OP + w.col(i, tq)) =
-                make_float2(w.o[b][i][2 * e] * f, w.o[b][i][2 * e + 1] * f);
-          }
-          if (warp == 0 && tq == 0) {
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < NW; ++k)
-              sum += sm_l[k * C::ROWS + rr] * exp2_fast(sm_m[k * C::ROWS + rr] - mu);
-            row_m[rr] = mx;
-            row_l[rr] = sum;
+            const float a = w.o[0][i][2 * e], b = w.o[0][i][2 * e + 1];
+            if (whole) {
+              store2(o + w.col(i, tq), a * inv[e], b * inv[e]);
+            } else {
+              *reinterpret_cast<float2*>(part + rr * D + w.col(i, tq)) = make_float2(a, b);
+            }
           }
         }
       }
-    }
-    __syncthreads();
-
-    const bool whole = t0 == 0 && t1 == tiles;
-    const bool head = item0 < share * blockIdx.x;  // the row began in an earlier CTA
-    float* part = p.part + (size_t)(2 * blockIdx.x + (head ? 0 : 1)) * (kPartFloats + kPartStats);
-    const float* os = reinterpret_cast<const float*>(sm);
-    for (int i = tid; i < R * (D / 2); i += C::NT) {
-      const int rr = i / (D / 2), d = 2 * (i % (D / 2));
-      float2 a = make_float2(0.f, 0.f);
+    } else {
 #pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const float2 y =
-            *reinterpret_cast<const float2*>(os + (k * C::ROWS + rr) * C::OP + d);
-        a.x += y.x;
-        a.y += y.y;
-      }
-      if (whole) {
-        const float inv = 1.f / row_l[rr];
-        const int tr = base + rr;
-        T* o = static_cast<T*>(p.o) + (((size_t)row * p.T + tr / p.G) * p.HQ + h * p.G + tr % p.G) * D;
-        store2(o + d, a.x * inv, a.y * inv);
-      } else {
-        *reinterpret_cast<float2*>(part + rr * D + d) = a;
-      }
-    }
-    if (tid < R) {
-      if (!whole) {
-        part[kPartFloats + tid] = row_m[tid];
-        part[kPartFloats + 64 + tid] = row_l[tid];
-      } else if (p.lse != nullptr) {
-        const int tr = base + tid;
-        p.lse[((size_t)row * p.T + tr / p.G) * p.HQ + h * p.G + tr % p.G] =
-            lse_of(row_m[tid], row_l[tid]);
+      for (int s = 0; s < D / 64; ++s) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = wr + 8 * e + g;
+          if (rr < R) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float2*>(os + (grp * C::ROWS + rr) * C::OP + w.col(i, tq)) =
+                  make_float2(w.o[0][8 * s + i][2 * e] * f[e],
+                              w.o[0][8 * s + i][2 * e + 1] * f[e]);
+          }
+        }
+        named_sync(1, C::CT);
+        const bool ok = flag[0] == 0;
+#pragma unroll 2
+        for (int i = tid; i < R * 16; i += C::CT) {
+          const int rr = i / 16, d = 4 * (i % 16);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < NG; ++k) {
+            const float4 y =
+                *reinterpret_cast<const float4*>(os + (k * C::ROWS + rr) * C::OP + d);
+            a.x += y.x;
+            a.y += y.y;
+            a.z += y.z;
+            a.w += y.w;
+          }
+          if (!whole) {
+            *reinterpret_cast<float4*>(part + rr * D + 64 * s + d) = a;
+          } else if (ok) {
+            const float r = row_l[rr];
+            T* o = static_cast<T*>(p.o) + out_row(rr) * D + 64 * s + d;
+            store2(o, a.x * r, a.y * r);
+            store2(o + 2, a.z * r, a.w * r);
+          }
+        }
+        if (s + 1 < D / 64) named_sync(1, C::CT);
       }
     }
 
     if (!whole) {
       // ---- the last part to arrive joins the row's parts
-      const int cta0 = (int)(item0 / share);
-      const int parts = (int)((item0 + tiles - 1) / share) - cta0 + 1;
-      __threadfence();
-      __syncthreads();
+      const int cta0 = (int)(sg.item0 / share);
+      const int parts = (int)((sg.item0 + sg.chunks - 1) / share) - cta0 + 1;
+      named_sync(1, C::CT);
       if (tid == 0) {
+        __threadfence();  // the CTA's part, and after the count the others'
         const int n = atomicAdd(p.count + cta0, 1);
         if (n == parts - 1) p.count[cta0] = 0;  // free for the next call
-        scan[NW + 2] = n == parts - 1;
+        flag[1] = n == parts - 1;
         __threadfence();
       }
-      __syncthreads();
-      if (scan[NW + 2]) {
-        const size_t stride = kPartFloats + kPartStats;
+      named_sync(1, C::CT);
+      if (flag[1]) {
+        const size_t stride = C::PART;
         // part k of the row: the first CTA's second slot, then first slots
         const float* parts0 = p.part + (size_t)(2 * cta0 + 1) * stride;
         const float* partsn = p.part + (size_t)(2 * cta0) * stride;
         auto at_part = [&](int k) { return k == 0 ? parts0 : partsn + (size_t)2 * k * stride; };
-        float* wt = reinterpret_cast<float*>(sm);  // [parts][R] weights
-        for (int i = tid; i < parts * R; i += C::NT)
-          wt[i] = __ldcg(at_part(i / R) + kPartFloats + i % R);
-        __syncthreads();
-        if (tid < R) {
-          float mx = kNegInf;
-          for (int k = 0; k < parts; ++k) mx = fmaxf(mx, wt[k * R + tid]);
-          row_m[tid] = mx;
-        }
-        __syncthreads();
-        for (int i = tid; i < parts * R; i += C::NT) {
-          const float mu = row_m[i % R] == kNegInf ? 0.f : row_m[i % R];
-          wt[i] = exp2_fast(wt[i] - mu);
-        }
-        __syncthreads();
-        if (tid < R) {
-          float sum = 0.f;
-          for (int k = 0; k < parts; ++k)
-            sum += wt[k * R + tid] * __ldcg(at_part(k) + kPartFloats + 64 + tid);
-          row_l[tid] = sum;
-        }
-        __syncthreads();
-        for (int i = tid; i < R * (D / 4); i += C::NT) {
-          const int rr = i / (D / 4), d = 4 * (i % (D / 4));
-          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        {
+          // all rows' statistics at once, LPR lanes to a row
+          constexpr int LPR = C::ROWS <= 16 ? 8 : C::ROWS <= 48 ? 4 : 2;
+          static_assert(C::ROWS * LPR <= C::CT || C::F32, "a lane group for each row");
+          const int sub = tid % LPR;
+          for (int rr = tid / LPR; rr < C::ROWS; rr += C::CT / LPR) {
+            float mx = kNegInf, sum = 0.f;
+            if (rr < R) {
 #pragma unroll 4
-          for (int k = 0; k < parts; ++k) {
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(at_part(k) + rr * D + d));
-            const float f = wt[k * R + rr];
-            a.x = fmaf(f, y.x, a.x);
-            a.y = fmaf(f, y.y, a.y);
-            a.z = fmaf(f, y.z, a.z);
-            a.w = fmaf(f, y.w, a.w);
+              for (int k = sub; k < parts; k += LPR) {
+                const float mk = __ldcg(at_part(k) + C::ROWS * D + rr);
+                const float lk = __ldcg(at_part(k) + C::ROWS * (D + 1) + rr);
+                const float to = fmaxf(mx, mk), mu = to == kNegInf ? 0.f : to;
+                sum = sum * exp2_fast(mx - mu) + lk * exp2_fast(mk - mu);
+                mx = to;
+              }
+            }
+#pragma unroll
+            for (int d = 1; d < LPR; d <<= 1) {
+              const float mk = __shfl_xor_sync(kFull, mx, d), lk = __shfl_xor_sync(kFull, sum, d);
+              const float to = fmaxf(mx, mk), mu = to == kNegInf ? 0.f : to;
+              // the same order on both sides, so that every lane has the same sum
+              const float a = sum * exp2_fast(mx - mu), b = lk * exp2_fast(mk - mu);
+              sum = (sub & d) ? b + a : a + b;
+              mx = to;
+            }
+            if (sub == 0 && rr < R) {
+              row_m[rr] = mx == kNegInf ? 0.f : mx;
+              row_l[rr] = 1.f / sum;
+              if (p.lse != nullptr && flag[0] == 0) p.lse[out_row(rr)] = lse_of(mx, sum);
+            }
           }
-          const float inv = 1.f / row_l[rr];
-          const int tr = base + rr;
-          T* o = static_cast<T*>(p.o) +
-                 (((size_t)row * p.T + tr / p.G) * p.HQ + h * p.G + tr % p.G) * D;
-          store2(o + d, a.x * inv, a.y * inv);
-          store2(o + d + 2, a.z * inv, a.w * inv);
         }
-        if (tid < R && p.lse != nullptr) {
-          const int tr = base + tid;
-          p.lse[((size_t)row * p.T + tr / p.G) * p.HQ + h * p.G + tr % p.G] =
-              lse_of(row_m[tid], row_l[tid]);
+        named_sync(1, C::CT);
+        const bool ok = flag[0] == 0;
+        // kJoin values of four a thread at a time, so that a part's loads go out
+        // together: the loop over the parts is one trip to L2 each
+        constexpr int kJoin = C::ROWS >= 32 ? 8 : 4;
+        for (int i0 = tid; i0 < R * (D / 4); i0 += C::CT * kJoin) {
+          float4 a[kJoin];
+#pragma unroll
+          for (int j = 0; j < kJoin; ++j) a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int k = 0; k < parts; ++k) {
+            const float* pk = at_part(k);
+            float4 y[kJoin];
+            float fk[kJoin];
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              const int i = i0 + j * C::CT;
+              if (i < R * (D / 4)) {
+                y[j] = __ldcg(reinterpret_cast<const float4*>(pk) + i);
+                fk[j] = __ldcg(pk + C::ROWS * D + i / (D / 4));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < kJoin; ++j) {
+              const int i = i0 + j * C::CT;
+              if (i < R * (D / 4)) {
+                const float e = exp2_fast(fk[j] - row_m[i / (D / 4)]);
+                a[j].x = fmaf(e, y[j].x, a[j].x);
+                a[j].y = fmaf(e, y[j].y, a[j].y);
+                a[j].z = fmaf(e, y[j].z, a[j].z);
+                a[j].w = fmaf(e, y[j].w, a[j].w);
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kJoin; ++j) {
+            const int i = i0 + j * C::CT;
+            if (i < R * (D / 4) && ok) {
+              const int rr = i / (D / 4), d = 4 * (i % (D / 4));
+              const float r = row_l[rr];
+              T* o = static_cast<T*>(p.o) + out_row(rr) * D + d;
+              store2(o, a[j].x * r, a[j].y * r);
+              store2(o + 2, a[j].z * r, a[j].w * r);
+            }
+          }
         }
       }
     }
-    __syncthreads();  // shared memory is free for the next stretch
-    pos += t1 - t0;
+    // shared memory, and this half of the segments, are free for the next
+    if (NG > 1 || !whole) named_sync(1, C::CT);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&qempty[half]);
   }
+  if (dead && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
 }
 
-// blocks of 16 rows a warp carries at once: outputs of 16 MB D values in
-// registers (128 a lane at most)
-int blocks_for(int D, int dt, int rows) {
-  if (dt == DT_F32 || D == 256 || rows <= 16) return 1;
-  if (D == 128 || rows <= 32) return 2;
-  return 4;
+// warps that share a stream's keys, sixteen rows each
+int warps_for(int D, int dt, int rows) {
+  if (dt == DT_F32 || rows <= 16) return 1;
+  return rows <= 32 ? 2 : D == 256 ? 3 : 4;
 }
 
 template <typename F>
-cudaError_t pick(int D, int dt, int mb, F f) {
-#define RSSM_CASE(TT, DD, MM) \
-  if (D == DD && mb == MM) return f(attn_decode_kernel<TT, DD, MM>, DecCfg<TT, DD, MM>::NT, DecCfg<TT, DD, MM>::SMEM);
-#define RSSM_CASES16(TT)                                                  \
-  RSSM_CASE(TT, 64, 1) RSSM_CASE(TT, 64, 2) RSSM_CASE(TT, 64, 4)          \
-  RSSM_CASE(TT, 128, 1) RSSM_CASE(TT, 128, 2) RSSM_CASE(TT, 256, 1)
+cudaError_t pick(int D, int dt, int mw, F f) {
+#define RSSM_CASE(TT, DD, MM)                                                      \
+  if (D == DD && mw == MM)                                                         \
+    return f(attn_decode_kernel<TT, DD, MM>, DecCfg<TT, DD, MM>::NT, DecCfg<TT, DD, MM>::SMEM, \
+             DecCfg<TT, DD, MM>::CPS);
+#define RSSM_CASES(TT, MM) RSSM_CASE(TT, 64, MM) RSSM_CASE(TT, 128, MM) RSSM_CASE(TT, 256, MM)
+#define RSSM_CASES16(TT)                                                           \
+  RSSM_CASES(TT, 1) RSSM_CASES(TT, 2) RSSM_CASE(TT, 64, 4) RSSM_CASE(TT, 128, 4)   \
+  RSSM_CASE(TT, 256, 3)
   if (dt == DT_F32) {
-    RSSM_CASE(float, 64, 1) RSSM_CASE(float, 128, 1) RSSM_CASE(float, 256, 1)
+    RSSM_CASES(float, 1)
   } else if (dt == DT_BF16) {
     RSSM_CASES16(__nv_bfloat16)
   } else {
     RSSM_CASES16(__half)
   }
 #undef RSSM_CASES16
+#undef RSSM_CASES
 #undef RSSM_CASE
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int attn_decode_block_rows(int D, int dt, int rows) { return 16 * blocks_for(D, dt, rows); }
+int attn_decode_block_rows(int D, int dt, int rows) { return 16 * warps_for(D, dt, rows); }
 
 cudaError_t attn_decode_prepare(int D, int dt) {
-  for (int mb = 1; mb <= 4; mb *= 2) {
-    if (mb > blocks_for(D, dt, 64)) break;
-    const cudaError_t e = pick(D, dt, mb, [](auto kernel, int, int smem) {
+  for (int rows = 16; rows <= 64; rows *= 2) {
+    const cudaError_t e = pick(D, dt, warps_for(D, dt, rows), [](auto kernel, int, int smem, int) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
@@ -438,11 +660,37 @@ cudaError_t attn_decode_prepare(int D, int dt) {
   return cudaSuccess;
 }
 
-cudaError_t attn_decode_launch(const DecodeParams& p, int D, int dt, int num_sms,
+// The pool as rows of 128-byte columns: a box is one chunk of one head.
+cudaError_t attn_decode_maps(void* maps, const void* k, const void* v, long long rows, int D,
+                             int dt) {
+  static_assert(sizeof(KvMaps) == kKvMapBytes, "two tensor maps");
+  if (tma_encoder() == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t es = dtype_bytes(dt), inner = 128 / es;
+  const cuuint64_t dims[3] = {inner, (cuuint64_t)rows, D * es / 128};
+  const cuuint64_t strides[2] = {D * es, 128};
+  const cuuint32_t box[3] = {(cuuint32_t)inner, kBox, (cuuint32_t)(D * es / 128)};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  KvMaps* m = static_cast<KvMaps*>(maps);
+  for (int i = 0; i < 2; ++i) {
+    if (tma_encoder()(i == 0 ? &m->k : &m->v,
+                      dt == DT_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                      : dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      3, const_cast<void*>(i == 0 ? k : v), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st) {
-  const int grid = num_sms < kMaxParts ? num_sms : kMaxParts;
-  return pick(D, dt, blocks_for(D, dt, p.T * p.G), [&](auto kernel, int nt, int smem) {
-    kernel<<<grid, nt, smem, st>>>(p);
+  const int sms = num_sms < kMaxSms ? num_sms : kMaxSms;
+  const KvMaps& m = *static_cast<const KvMaps*>(maps);
+  return pick(D, dt, warps_for(D, dt, p.T * p.G), [&](auto kernel, int nt, int smem, int cps) {
+    kernel<<<cps * sms, nt, smem, st>>>(p, m);
     return cudaGetLastError();
   });
 }

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant_
     const int tr = live ? rr : 0;
     const T* q = static_cast<const T*>(p.q) + (long long)(tl.q0 + i0 + tr / p.G) * p.qs +
                  (long long)(h * p.G + tr % p.G) * D;
-    *reinterpret_cast<uint4*>(qs + unit_off<T, D>(rr, u)) =
+    *reinterpret_cast<uint4*>(qs + unit_off<C::ROWS>(rr, u)) =
         live ? reinterpret_cast<const uint4*>(q)[u] : make_uint4(0, 0, 0, 0);
   }
 
@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant_
         const long long key = tl.k0 + (live ? key0 + rr : 0);
         const T* k = static_cast<const T*>(p.k) + key * p.ks + (long long)h * D;
         const T* v = static_cast<const T*>(p.v) + key * p.vs + (long long)h * D;
-        cp_async16_or_zero(kd + unit_off<T, D>(rr, u), reinterpret_cast<const uint4*>(k) + u, live);
-        cp_async16_or_zero(vd + unit_off<T, D>(rr, u), reinterpret_cast<const uint4*>(v) + u, live);
+        cp_async16_or_zero(kd + unit_off<C::KEYS>(rr, u), reinterpret_cast<const uint4*>(k) + u, live);
+        cp_async16_or_zero(vd + unit_off<C::KEYS>(rr, u), reinterpret_cast<const uint4*>(v) + u, live);
       }
     }
     cp_async_commit();
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant_
   const int fewest = max(0, past + i0 + r_first / p.G + 1);
   const int most = max(0, past + i0 + r_last / p.G + 1);
 
-  WarpAttn<T, D, 1> w;
+  WarpAttn<T, D, 1, C::ROWS, C::KEYS> w;
   w.clear();
   const int nt = (keys + C::KEYS - 1) / C::KEYS;
   issue(0);
@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant_
     const int key0 = j * C::KEYS;
     if (key0 < most && 16 * warp < R) {
       float x[1][C::KEYS / 8][4];
-      w.template weights<C::KEYS / 8>(x, qs + 16 * warp * D * sizeof(T), ks, key0, lim, fewest,
+      w.template weights<C::KEYS / 8>(x, qs + 16 * warp * 128, ks, key0, lim, fewest,
                                       p.c, lane);
-      w.template add<C::KEYS / 8>(x, ks + C::TBYTES, key0, lim, fewest, keys, lane);
+      w.template add<C::KEYS / 8>(x, ks + C::TBYTES, key0, lim, fewest, lane);
     }
     __syncthreads();
     issue(j + 2);

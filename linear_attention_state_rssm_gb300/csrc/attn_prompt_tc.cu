@@ -32,6 +32,7 @@
 // against one exponential per pair on the special-function units.
 #include "attn_tc.cuh"
 #include "attn_tiles.cuh"
+#include "attn_tma.h"
 #include "kv_common.cuh"
 
 namespace rssm {
@@ -73,7 +74,7 @@ __device__ __noinline__ void again(const PromptParams& p, const PromptTile& tl, 
       const int rr = min(r0 + i / QU, rows - 1), u = i % QU;
       const T* q = static_cast<const T*>(p.q) + (long long)(tok0 + rr / p.G) * p.qs +
                    (long long)(h * p.G + rr % p.G) * D;
-      *reinterpret_cast<uint4*>(qs + unit_off<T, D>(i / QU, u)) =
+      *reinterpret_cast<uint4*>(qs + unit_off<16>(i / QU, u)) =
           reinterpret_cast<const uint4*>(q)[u];
     }
     int lim[1][2];
@@ -84,7 +85,7 @@ __device__ __noinline__ void again(const PromptParams& p, const PromptTile& tl, 
     }
     const int fewest = max(0, past + (tok0 - tl.q0) + r0 / p.G + 1);
     const int keys = max(0, past + (tok0 - tl.q0) + min(r0 + 15, rows - 1) / p.G + 1);
-    WarpAttn<T, D, 1> w;
+    WarpAttn<T, D, 1, 16, 16> w;
     w.clear();
     for (int key0 = 0; key0 < keys; key0 += 16) {
       __syncwarp();
@@ -97,13 +98,13 @@ __device__ __noinline__ void again(const PromptParams& p, const PromptTile& tl, 
         const uint4* vg = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + key * p.vs +
                                                          (long long)h * D) + u;
         const uint4 z = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(ks + unit_off<T, D>(kr, u)) = live ? *kg : z;
-        *reinterpret_cast<uint4*>(vs + unit_off<T, D>(kr, u)) = live ? *vg : z;
+        *reinterpret_cast<uint4*>(ks + unit_off<16>(kr, u)) = live ? *kg : z;
+        *reinterpret_cast<uint4*>(vs + unit_off<16>(kr, u)) = live ? *vg : z;
       }
       __syncwarp();
       float x[1][2][4];
       w.template weights<2>(x, qs, ks, key0, lim, fewest, p.c, lane);
-      w.template add<2>(x, vs, key0, lim, fewest, keys, lane);
+      w.template add<2>(x, vs, key0, lim, fewest, lane);
     }
     w.finish();
 #pragma unroll
@@ -437,28 +438,10 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   if (warp == 4 * C::NS) tmem_dealloc512(tb);
 }
 
-using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                            const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-Encode encoder() {
-  static const Encode fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<Encode>(f);
-  }();
-  return fn;
-}
-
 bool encode(CUtensorMap* map, int dt, int rank, const void* base, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box) {
   const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return encoder()(map, dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+  return tma_encoder()(map, dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                    (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -484,7 +467,7 @@ cudaError_t pick(int D, int dt, F f) {
 }  // namespace
 
 cudaError_t attn_prompt_tc_prepare(int D, int dt) {
-  if (encoder() == nullptr) return cudaErrorNotSupported;
+  if (tma_encoder() == nullptr) return cudaErrorNotSupported;
   return pick(D, dt, [](auto kernel, int, int smem, int) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });

@@ -111,15 +111,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&r)[1
       : "memory");
 }
 
-// Tiled TMA loads; the inner coordinate is a multiple of 64 values.
-__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                          int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-      : "memory");
-}
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int x, int y,
                                           int z, int w, uint64_t* bar) {
   asm volatile(

@@ -15,6 +15,7 @@ struct rssm_kv_handle {
   int shift;            // log2(page_size)
   size_t layer_bytes;   // one layer's keys (or values)
   size_t page_bytes;    // one page of one layer's keys (or values)
+  alignas(64) unsigned char maps[kKvMapBytes];  // the pool's tensor maps
 };
 
 namespace {
@@ -41,6 +42,9 @@ rssm_status check_config(const rssm_kv_config* c) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0)
     return RSSM_ERR_UNSUPPORTED;
   // token positions are 32-bit, and a plan's sums over rows too
+  // and the pool's rows (one token of one head) are addressed in 31 bits
+  if ((long long)c->n_layers * c->n_pages * c->HKV > 0x7fffffffll / c->page_size)
+    return RSSM_ERR_UNSUPPORTED;
   if (c->n_pages > (1 << 28) || c->max_pages > (1 << 20)) return RSSM_ERR_UNSUPPORTED;
   return RSSM_OK;
 }
@@ -143,6 +147,10 @@ rssm_status rssm_kv_alloc(const rssm_kv_config* cfg, const rssm_kv_buffers* buf,
     e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype);
   if (e == cudaSuccess) e = attn_prompt_prepare(cfg->D, cfg->dtype);
+  if (e == cudaSuccess)
+    e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
+                         (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
+                         cfg->D, cfg->dtype);
   if (e != cudaSuccess) {
     delete h;
     return RSSM_ERR_CUDA;
@@ -306,14 +314,13 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   char* work = static_cast<char*>(h->buf.work);
   DecodeParams p{};
   p.q = q;
-  p.kp = static_cast<unsigned char*>(h->buf.k_pages) + (size_t)layer * h->layer_bytes;
-  p.vp = static_cast<unsigned char*>(h->buf.v_pages) + (size_t)layer * h->layer_bytes;
   p.slot = slot;
   p.table = h->buf.table;
   p.held = h->buf.held;
   p.length = h->buf.length;
   p.o = o;
   p.lse = lse;
+  p.page0 = (long long)layer * c.n_pages;
   p.part = reinterpret_cast<float*>(work + w.part);
   p.count = reinterpret_cast<int32_t*>(work + w.count);
   p.err = h->buf.err_word;
@@ -331,7 +338,8 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   p.nmb = (T * p.G + rows - 1) / rows;
   p.c = (float)((double)c.scale * 1.4426950408889634);
   return from_cuda(
-      attn_decode_launch(p, c.D, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
+      attn_decode_launch(p, h->maps, c.D, c.dtype, h->num_sms,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 rssm_status rssm_attn_prefill(rssm_kv_handle* h, const void* q, const void* k, const void* v,

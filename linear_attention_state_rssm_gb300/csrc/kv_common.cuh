@@ -13,15 +13,17 @@ enum : uint32_t {
   DEVERR_POSITION = 64u,  // rotary position outside the table
 };
 
-constexpr int kMaxParts = 304;      // most CTAs of a decode launch: parts a row can be cut into
-constexpr int kPartFloats = 4096;   // a part's rows x D (16 x 256, 32 x 128 or 64 x 64)
-constexpr int kPartStats = 128;     // its running maxima and sums (64 rows each)
+constexpr int kMaxSms = 152;        // SMs that a decode launch uses at most
+constexpr int kMaxParts = 3 * kMaxSms;  // its CTAs: parts a row can be cut into
+// fp32 values of two parts per CTA: outputs, running maxima and sums of up to
+// 64 rows (two CTAs per SM for D = 256, three for smaller heads)
+constexpr size_t kPartFloats = (size_t)2 * 2 * kMaxSms * 64 * (256 + 4);
 constexpr int kMaxRopeAxes = 3;
 
 // Regions of the caller's work buffer (bytes); `count` is zero between calls.
 struct KvWork {
   size_t count;   // [kMaxParts] arrivals of the parts of a split row
-  size_t part;    // [2 kMaxParts][kPartFloats + kPartStats] fp32
+  size_t part;    // [kPartFloats]
   size_t moves;   // [1] number of page copies of the last plan
   size_t src;     // [n_pages] pages to copy from
   size_t dst;     // [n_pages] pages to copy to; free pages of a reservation
@@ -33,7 +35,7 @@ struct KvWork {
     const size_t n = up((size_t)n_pages * 4);
     count = 0;
     part = up(kMaxParts * 4);
-    moves = part + up((size_t)2 * kMaxParts * (kPartFloats + kPartStats) * 4);
+    moves = part + up(kPartFloats * 4);
     src = moves + 256;
     dst = src + n;
     map = dst + n;
@@ -106,8 +108,6 @@ struct AppendParams {
 
 struct DecodeParams {
   const void* q;
-  const unsigned char* kp;  // this layer's pages
-  const unsigned char* vp;
   const int32_t* slot;
   const int32_t* table;
   const int32_t* held;
@@ -118,6 +118,7 @@ struct DecodeParams {
   int32_t* count;
   uint32_t* err;
   long long qs;
+  long long page0;  // the layer's first page among all layers'
   int B, T, HQ, HKV, G, n_slots, n_pages, max_pages, shift;
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
   float c;      // scale * log2(e)
@@ -143,7 +144,11 @@ cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
 cudaError_t attn_decode_prepare(int D, int dt);
-cudaError_t attn_decode_launch(const DecodeParams& p, int D, int dt, int num_sms,
+// tensor maps of the pool (kKvMapBytes, 64-byte aligned) and the launch with them
+constexpr int kKvMapBytes = 256;
+cudaError_t attn_decode_maps(void* maps, const void* k, const void* v, long long rows, int D,
+                             int dt);
+cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st);
 int attn_decode_block_rows(int D, int dt, int rows);  // rows of a block for T G rows
 cudaError_t attn_prompt_prepare(int D, int dt);

@@ -215,6 +215,7 @@ class KVCache:
         self.n_layers, self.n_slots, self.HQ, self.HKV, self.D = n_layers, n_slots, HQ, HKV, D
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self.dtype, self.scale = dtype, self.cfg.scale
+        self._torch_dtype = _TORCH[dtype]
         self.device = torch.device(device)
         sizes = _lib.rssm_kv_required_bytes(self.cfg)  # validates the configuration
         dev, t = self.device, _TORCH[dtype]
@@ -306,17 +307,20 @@ class KVCache:
     # ------------------------------------------------------------- helpers
     def _tokens(self, x, heads, n=None):
         """Tokens and token stride of [n, heads, D] (heads and D contiguous)."""
-        shape, stride = x.shape, x.stride()
-        if len(shape) != 3 or shape[1] != heads or shape[2] != self.D \
-                or (n is not None and shape[0] != n):
-            raise ValueError(f"expected {n or 'N'} x {heads} x {self.D}, got {tuple(shape)}")
-        if x.dtype != _TORCH[self.dtype] or (stride[2] != 1 or stride[1] != self.D
-                                             and heads > 1):
+        D = self.D
+        try:
+            m, h, d = x.shape
+            s0, s1, s2 = x.stride()
+        except ValueError:
+            m = h = d = -1
+        if h != heads or d != D or (n is not None and m != n):
+            raise ValueError(f"expected {n or 'N'} x {heads} x {D}, got {tuple(x.shape)}")
+        if x.dtype != self._torch_dtype or s2 != 1 or (s1 != D and heads > 1):
             raise ValueError("the cache's dtype, with contiguous heads")
-        return shape[0], stride[0] if shape[0] > 1 else heads * self.D
+        return m, s0 if m > 1 else heads * D
 
     def _output(self, o, n, lse=None):
-        if o.dtype != _TORCH[self.dtype] or o.numel() != n * self.HQ * self.D \
+        if o.dtype != self._torch_dtype or o.numel() != n * self.HQ * self.D \
                 or not o.is_contiguous():
             raise ValueError("outputs: contiguous, the cache's dtype, [tokens, HQ, D]")
         if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * self.HQ
