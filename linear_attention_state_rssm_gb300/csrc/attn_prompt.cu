@@ -29,15 +29,14 @@ struct PromptCfg {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(128) attn_prompt_kernel(const __grid_constant__ PromptParams p) {
+__global__ void __launch_bounds__(PromptCfg<T, D>::NT) attn_prompt_kernel(const __grid_constant__ PromptParams p) {
   using C = PromptCfg<T, D>;
   extern __shared__ __align__(1024) unsigned char sm[];
-  __shared__ PromptTile sh_tile;
+  PromptTile tl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int toks = C::ROWS / p.G;  // query tokens of a tile
   const int h = (int)(blockIdx.x % (unsigned)p.HKV);    // heads of a tile side by side
-  if (!find_tile<C::NT>(p, toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0, &sh_tile)) return;
-  const PromptTile tl = sh_tile;
+  if (!find_tile(p, toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl)) return;
   const int i0 = tl.tile * toks;                        // first query token of the tile
   const int R = min(toks, tl.lq - i0) * p.G;            // rows in use
   const int past = tl.lk - tl.lq;                       // may be negative

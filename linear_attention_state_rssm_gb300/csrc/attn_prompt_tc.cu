@@ -47,7 +47,7 @@ struct TcCfg {
   static constexpr int UNIT = 128 * DU * 2;
   static constexpr int NU = D == 64 ? 8 : 5;         // units in the ring
   static constexpr int QS = 128 * D * 2;             // one stream's queries
-  static constexpr int NT = NS * 128 + 64;
+  static constexpr int NT = NS * 128 + 128;          // the producer's warpgroup: two warps work
   static constexpr int RING = NS * QS;               // its offset
   static constexpr int BARS = RING + NU * UNIT;
   static constexpr int SMEM = BARS + 512 + 1024;     // + alignment of the base
@@ -144,16 +144,15 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   uint64_t* empty = full + C::NU;                              // [NU] its products are done
   uint64_t* qfull = empty + C::NU;                             // queries have landed
   uint64_t* sfull = qfull + 1;                                 // [2] scores are in tensor memory
-  uint64_t* pfull = sfull + 2;                                 // [2] weights are
-  uint64_t* odone = pfull + 2;                                 // [2] a tile's P V is done
+  uint64_t* pfull = sfull + 2;                                 // [2][2] half the weights are
+  uint64_t* odone = pfull + 4;                                 // [2] a tile's P V is done
   uint32_t* tslot = reinterpret_cast<uint32_t*>(odone + 2);
-  __shared__ PromptTile sh_tile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  PromptTile tl;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int toks = 128 / p.G;                       // tokens of a stream
   const int h = (int)(blockIdx.x % (unsigned)p.HKV);  // heads of a tile side by side
-  if (!find_tile<C::NT>(p, C::NS * toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0, &sh_tile))
+  if (!find_tile(p, C::NS * toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl))
     return;
-  const PromptTile tl = sh_tile;
   const int i0 = tl.tile * C::NS * toks;
   const int past = tl.lk - tl.lq;
   // tiles of keys that each stream sees
@@ -170,7 +169,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     mbar_init(qfull, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sfull[b], 1);
-      mbar_init(&pfull[b], 128);
+      mbar_init(&pfull[2 * b], 128);
+      mbar_init(&pfull[2 * b + 1], 128);
       mbar_init(&odone[b], 1);
     }
     fence_mbar_init();
@@ -182,6 +182,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   const uint32_t tb = *tslot;
   bool dead = false;
 
+  if (warp >= 4 * C::NS) {
+  // three warpgroups at 168 registers: two take 232, the producers' keeps 40
+  if constexpr (C::NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 4 * C::NS) {
     // ---- producer: K(0), then for each tile the values and the next keys in
     // the order the products take them
@@ -221,45 +224,55 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     }
     __syncwarp();
   } else if (warp == 4 * C::NS + 1) {
-    // ---- products
-    if (lane == 0 && ntm > 0) {
+    // ---- products; the warp stays together and one lane issues
+    if (ntm > 0) {
       constexpr uint32_t id_qk = f16_idesc<T>(128, 128, false);
       constexpr uint32_t id_pv = f16_idesc<T>(128, C::DU, true);
-      const uint32_t qa = smem_addr(sm), ra = smem_addr(sm + C::RING);
+      const uint32_t el = elect_lane();
+      const uint32_t qd = sw128_kmajor_lo(smem_addr(sm));
+      const uint32_t kd = sw128_kmajor_lo(smem_addr(sm + C::RING));
+      const uint32_t vd = sw128_mnmajor_lo(smem_addr(sm + C::RING), 16384);
       auto ready = [&](int n) { tc_wait(&full[n % C::NU], (uint32_t)((n / C::NU) & 1), dead); };
       // S[buf] = Q_s K^T, keys in units n ..
       auto qk = [&](int s, int buf, int n) {
         for (int i = 0; i < C::UPT; ++i) {
           ready(n + i);
+          dead = __any_sync(kFull, dead);
           if (dead) return;
           tc_fence_after();
-          const uint32_t ua = ra + ((n + i) % C::NU) * C::UNIT;
+          const uint32_t a = qd + (s * C::QS + i * 32768) / 16;
+          const uint32_t b = kd + ((n + i) % C::NU) * (C::UNIT / 16);
 #pragma unroll
           for (int k = 0; k < C::DU / 16; ++k) {
-            const uint32_t in = (k / 4) * 16384 + (k % 4) * 32;
-            mma16_ss(tb + buf * 128, sw128_kmajor(qa + s * C::QS + i * 32768 + in),
-                     sw128_kmajor(ua + in), id_qk, i > 0 || k > 0);
+            const uint32_t in = ((k / 4) * 16384 + (k % 4) * 32) / 16;
+            mma16_ss(el, tb + buf * 128, a + in, b + in, id_qk, i > 0 || k > 0);
           }
         }
-        mma_commit(&sfull[buf]);
+        mma16_commit(el, &sfull[buf]);
       };
-      // O_s += P V, weights in buffer buf, values in units n ..
-      auto pv = [&](int s, int buf, int n, bool acc) {
-        for (int i = 0; i < C::UPT; ++i) {
-          ready(n + i);
+      // O_s += P V, weights in buffer buf (its turn's parity), values in units
+      // n ..; the first 64 keys' products begin when their weights are there
+      auto pv = [&](int s, int buf, uint32_t par, int n, bool acc) {
+        for (int i = 0; i < C::UPT; ++i) ready(n + i);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tc_wait(&pfull[2 * buf + half], par, dead);
+          dead = __any_sync(kFull, dead);
           if (dead) return;
           tc_fence_after();
-          const uint32_t ua = ra + ((n + i) % C::NU) * C::UNIT;
+          for (int i = 0; i < C::UPT; ++i) {
+            const uint32_t b = vd + ((n + i) % C::NU) * (C::UNIT / 16);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma16_ts(tb + C::O0 + s * D + i * 128, tb + buf * 128 + 8 * k,
-                     sw128_mnmajor(ua + k * 2048, 16384), id_pv, acc || k > 0);
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma16_ts(el, tb + C::O0 + s * D + i * 128, tb + buf * 128 + 8 * k, b + k * 128,
+                       id_pv, acc || k > 0);
+          }
         }
-        mma_commit(&odone[s]);
+        mma16_commit(el, &odone[s]);
       };
       auto free_units = [&](int n) {
         for (int i = 0; i < C::UPT; ++i)
-          if (!dead) mma_commit(&empty[(n + i) % C::NU]);
+          if (!dead) mma16_commit(el, &empty[(n + i) % C::NU]);
       };
       tc_wait(qfull, 0, dead);
       if constexpr (C::NS == 2) {
@@ -270,10 +283,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
         for (int j = 0; j < ntm; ++j) {
           const int nv = C::UPT * (2 * j + 1), nk = nv + C::UPT;
           for (int s = 0; s < 2; ++s) {
-            if (j < nt[s]) {
-              tc_wait(&pfull[s], (uint32_t)(j & 1), dead);
-              pv(s, s, nv, j > 0);
-            }
+            if (j < nt[s]) pv(s, s, (uint32_t)(j & 1), nv, j > 0);
             if (j + 1 < nt[s]) qk(s, s, nk);
           }
           free_units(nv);
@@ -291,19 +301,20 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
             qk(0, (j + 1) & 1, nk);
             free_units(nk);
           }
-          tc_wait(&pfull[j & 1], (uint32_t)((j >> 1) & 1), dead);
-          pv(0, j & 1, nv, j > 0);
+          pv(0, j & 1, (uint32_t)((j >> 1) & 1), nv, j > 0);
           free_units(nv);
         }
       }
-      if (dead) {  // products in flight end before their memory is given back
+      if (__any_sync(kFull, dead)) {  // products in flight end before their memory is given back
         bool late = false;
-        mma_commit(qfull);
+        mma16_commit(el, qfull);
         tc_wait(qfull, 1, late);
       }
     }
     __syncwarp();
+  }
   } else {
+    if constexpr (C::NS == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ---- softmax: thread `row` of stream s
     const int s = warp >> 2, row = tid & 127;
     const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
@@ -313,7 +324,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     const int lim = max(0, past + tok0 + rr / p.G + 1);        // keys the row sees
     const int fewest = __reduce_min_sync(kFull, lim);
     float m = kNegInf;                                         // reference maximum (raw score)
-    uint64_t l2 = f2(0.f, 0.f);
+    uint64_t l2[4];  // sums of the weights, in eight chains
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l2[i] = f2(0.f, 0.f);
     const float c = p.c;
     const int n_tiles = nt[s];
     for (int j = 0; j < n_tiles; ++j) {
@@ -334,31 +347,36 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
 #pragma unroll
         for (int i = 0; i < 128; ++i) x[i] = i < n ? x[i] : kNegInf;
       }
-      float mx = m;
+      float t[4] = {m, kNegInf, kNegInf, kNegInf};
 #pragma unroll
-      for (int i = 0; i < 128; i += 2) mx = max3(mx, x[i], x[i + 1]);
+      for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[i + 2 * k], x[i + 2 * k + 1]);
+      }
+      const float mx = max3(fmaxf(t[0], t[1]), t[2], t[3]);
       // move the reference: always from -inf, else when the row outgrew it
       const bool move = (mx - m) * c > 8.f;
       if (__any_sync(kFull, move)) {
         const float to = move ? mx : m;
         if (j > 0) {
           const float f = to == kNegInf ? 1.f : exp2_fast((m - to) * c);
-          float a, b;
-          un2(l2, a, b);
-          l2 = f2(a * f, b * f);
-          const int prev = j - 1;
-          tc_wait(&odone[s], (uint32_t)(prev & 1), dead);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            un2(l2[i], a, b);
+            l2[i] = f2(a * f, b * f);
+          }
+          tc_wait(&odone[s], (uint32_t)((j - 1) & 1), dead);
           dead = __any_sync(kFull, dead);
           tc_fence_after();
           const uint32_t to_o = tb + lane_at + C::O0 + s * D;
 #pragma unroll 1
-          for (int d = 0; d < D; d += 32) {
-            float o[32];
-            tmem_ld32(to_o + d, o);
-            tmem_ld_wait32(o);
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+            tmem_ld16(to_o + d, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(to_o + d, o);
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            tmem_st16(to_o + d, o);
           }
         }
         m = to;
@@ -374,24 +392,31 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
           un2(fma2(f2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), c2, b2), a, b);
           a = exp2_fast(a);
           b = exp2_fast(b);
-          l2 = add2(l2, f2(a, b));
+          l2[i & 3] = add2(l2[i & 3], f2(a, b));
           w[i] = pack2<T>(a, b);
         }
         tmem_st16u(ts + 16 * q, w);
+        if (q & 1) {
+          tmem_st_wait();
+          // A parity tells a phase only from its neighbours, so every phase of
+          // odone is seen before the next can end. With two streams the scores
+          // of tile j follow P V of tile j - 1; with one they do not.
+          if (C::NS == 1 && q == 1 && j > 0) tc_wait(&odone[s], (uint32_t)((j - 1) & 1), dead);
+          tc_fence_before();
+          mbar_arrive(&pfull[2 * buf + (q >> 1)]);
+        }
       }
-      tmem_st_wait();
-      // A parity tells a phase only from its neighbours, so every phase of odone
-      // is seen before the next can end. With two streams the scores of tile j
-      // follow P V of tile j - 1; with one they do not.
-      if (C::NS == 1 && j > 0) tc_wait(&odone[s], (uint32_t)((j - 1) & 1), dead);
-      tc_fence_before();
-      mbar_arrive(&pfull[buf]);
     }
 
-    // ---- output
-    float a, b;
-    un2(l2, a, b);
-    const float l = a + b;
+    // ---- output: through the stream's query block (its products are done) to
+    // rows of whole lines
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float a, b;
+      un2(l2[i], a, b);
+      l += a + b;
+    }
     const bool none = lim == 0;
     const float inv = none ? 0.f : 1.f / l;
     const size_t orow = (size_t)(tl.q0 + tok0 + rr / p.G) * p.HQ + h * p.G + rr % p.G;
@@ -401,29 +426,42 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       dead = __any_sync(kFull, dead);
       tc_fence_after();
     }
-    T* out = static_cast<T*>(p.o) + orow * D;
     const bool mine = row < R && !dead;
-#pragma unroll 1
+    unsigned char* st = sm + s * C::QS + (warp & 3) * (32 * D * 2);  // the warp's 32 rows
+#pragma unroll 2
     for (int d = 0; d < D; d += 32) {
       float o[32];
       if (n_tiles > 0) {
         tmem_ld32(tb + lane_at + C::O0 + s * D + d, o);
         tmem_ld_wait32(o);
       }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
       float t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) t = fmaf(o[i], 0.f, t);  // NaN where any is non-finite
+      for (int i = 0; i < 32; ++i) {
+        o[i] = none ? 0.f : o[i] * inv;
+        t = fmaf(o[i], 0.f, t);  // NaN where any is non-finite
+      }
       bad |= t != 0.f;
-      if (mine) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          *reinterpret_cast<uint4*>(out + d + i) =
-              make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
-                         pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7]));
+      for (int i = 0; i < 32; i += 8)
+        *reinterpret_cast<uint4*>(st + unit_off<32>(lane, (d + i) / 8)) =
+            make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
+                       pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7]));
+    }
+    __syncwarp();
+    if (!dead) {
+      constexpr int U = D * 2 / 16;  // 16-byte units of a row
+#pragma unroll 4
+      for (int i = lane; i < 32 * U; i += 32) {
+        const int r = i / U, u = i % U, at = 32 * (warp & 3) + r;
+        if (at < R) {
+          T* out = static_cast<T*>(p.o) +
+                   ((size_t)(tl.q0 + tok0 + at / p.G) * p.HQ + h * p.G + at % p.G) * D;
+          reinterpret_cast<uint4*>(out)[u] = *reinterpret_cast<const uint4*>(st + unit_off<32>(r, u));
+        }
       }
     }
+    __syncwarp();  // before any of these rows is written again
     if (mine && p.lse != nullptr) p.lse[orow] = none ? kNegInf : lse_of(m * c, l);
     bad = __any_sync(kFull, bad && mine);
     // the ring is free once every stream's products are done

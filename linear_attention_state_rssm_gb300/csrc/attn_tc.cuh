@@ -16,16 +16,18 @@
 
 namespace rssm {
 
-// K-major, 128-byte swizzle: 8-row groups 1024 bytes apart
-__device__ __forceinline__ uint64_t sw128_kmajor(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
+// Shared-memory descriptors under the 128-byte swizzle, as two words: the low
+// one holds the start address in sixteens, so that a step along the operand is
+// an addition (the fields do not overflow: addresses stay below 2^18).
+//  - K-major: 8-row groups 1024 bytes apart;
+//  - MN-major: the next 64 of the N index `lbo` bytes on, the next eight of
+//    the K index 1024 bytes on.
+constexpr uint32_t kSw128Hi = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t sw128_kmajor_lo(uint32_t saddr) {
+  return ((saddr >> 4) & 0x3FFFu) | (1u << 16);
 }
-// MN-major, 128-byte swizzle: next 64 of the N index `lbo` bytes on, next
-// eight of the K index 1024 bytes on
-__device__ __forceinline__ uint64_t sw128_mnmajor(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         (64ull << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint32_t sw128_mnmajor_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
 // kind::f16 instruction descriptor: fp32 accumulator, A K-major (or in tensor
 // memory), B K-major or MN-major
@@ -35,20 +37,41 @@ __host__ __device__ constexpr uint32_t f16_idesc(int M, int N, bool b_mn) {
   return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         bool acc) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t e;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(e));
+  return e;
+}
+// D (+)= A B, issued by the lane with `el` set of a warp that stays together:
+// operands are then the same in every lane and need no gathering from one (an
+// issue took 75 to 96 cycles inside a branch of one lane, more than the
+// product itself).
+__device__ __forceinline__ void mma16_ss(uint32_t el, uint32_t d, uint32_t a, uint32_t b,
+                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n.reg .pred p, q;\n.reg .b64 x, y;\nsetp.ne.b32 q, %6, 0;\nsetp.ne.b32 p, %5, 0;\n"
+      "mov.b64 x, {%1, %3};\nmov.b64 y, {%2, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kSw128Hi), "r"(idesc), "r"(acc), "r"(el)
       : "memory");
 }
-__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                         bool acc) {
+__device__ __forceinline__ void mma16_ts(uint32_t el, uint32_t d, uint32_t a, uint32_t b,
+                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n.reg .pred p, q;\n.reg .b64 y;\nsetp.ne.b32 q, %6, 0;\nsetp.ne.b32 p, %5, 0;\n"
+      "mov.b64 y, {%2, %3};\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(kSw128Hi), "r"(idesc), "r"(acc), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void mma16_commit(uint32_t el, uint64_t* bar) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(el)
       : "memory");
 }
 

@@ -11,7 +11,6 @@ struct PromptTile {
   int tile;        // query tile of the sequence
   int q0, k0;      // the sequence's first query token and key
   int lq, lk;
-  int found;
 };
 
 // Offsets of sequence r; false for a null slot or offsets out of order.
@@ -41,17 +40,15 @@ __device__ __forceinline__ bool prompt_span(const PromptParams& p, int r, bool t
 }
 
 // Tile `index` of the launch (tiles of `toks` query tokens, sequences in
-// order, a sequence's last tile first: it sees the most keys). All NT threads
-// of the CTA; false when the launch has fewer tiles.
-template <int NT>
+// order, a sequence's last tile first: it sees the most keys). Each warp finds
+// it by itself; false when the launch has fewer tiles.
 __device__ __forceinline__ bool find_tile(const PromptParams& p, int toks, int index, bool tell,
-                                          PromptTile* out) {
-  __shared__ int sums[NT / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) out->found = 0;
+                                          PromptTile& out) {
+  const int lane = threadIdx.x & 31;
   int before = 0;
-  for (int r0 = 0; r0 < p.B; r0 += NT) {
-    const int r = r0 + tid;
+  bool found = false;
+  for (int r0 = 0; r0 < p.B; r0 += 32) {
+    const int r = r0 + lane;
     int q0 = 0, k0 = 0, lq = 0, lk = 0, n = 0;
     if (r < p.B && prompt_span(p, r, tell && index == 0, q0, lq, k0, lk))
       n = (lq + toks - 1) / toks;
@@ -61,22 +58,21 @@ __device__ __forceinline__ bool find_tile(const PromptParams& p, int toks, int i
       const int y = __shfl_up_sync(kFull, incl, d);
       if (lane >= d) incl += y;
     }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int at = before + incl - n, all = 0;
-    for (int i = 0; i < NT / 32; ++i) {
-      if (i < warp) at += sums[i];
-      all += sums[i];
+    const int at = before + incl - n;
+    const unsigned has = __ballot_sync(kFull, at <= index && index < at + n);
+    if (has != 0) {
+      const int src = __ffs(has) - 1;
+      out.tile = __shfl_sync(kFull, at + n - 1 - index, src);
+      out.q0 = __shfl_sync(kFull, q0, src);
+      out.k0 = __shfl_sync(kFull, k0, src);
+      out.lq = __shfl_sync(kFull, lq, src);
+      out.lk = __shfl_sync(kFull, lk, src);
+      found = true;
+      if (index != 0) return true;  // tile 0's warps look every sequence over
     }
-    if (at <= index && index < at + n) {
-      *out = PromptTile{at + n - 1 - index, q0, k0, lq, lk, 1};
-    }
-    before += all;
-    __syncthreads();
-    if (index < before && index != 0) break;  // tile 0's CTA looks every sequence over
+    before += __shfl_sync(kFull, incl, 31);
   }
-  __syncthreads();
-  return out->found != 0;
+  return found;
 }
 
 }  // namespace rssm
