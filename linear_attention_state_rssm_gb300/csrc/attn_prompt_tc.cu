@@ -149,6 +149,9 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(odone + 2);
   PromptTile tl;
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
+  if (tid < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(tid == 0 ? &maps.q : tid == 1 ? &maps.k : &maps.v)
+                 : "memory");
   const int toks = 128 / p.G;                       // tokens of a stream
   const int h = (int)(blockIdx.x % (unsigned)p.HKV);  // heads of a tile side by side
   if (!find_tile(p, C::NS * toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl))
@@ -164,7 +167,25 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   }
   const int ntm = max(nt[0], nt[1]);
 
-  if (tid == 0) {
+  // The producer's warp sets the barriers up and sends for the first units
+  // while the products' warp waits for tensor memory.
+  bool dead = false;
+  int issued = 0;  // units sent for
+  auto unit = [&](const CUtensorMap* map, int tile, int part) {
+    const int u = issued % C::NU;
+    if (issued >= C::NU)
+      tc_wait(&empty[u], (uint32_t)((issued / C::NU - 1) & 1), dead);
+    ++issued;
+    if (dead) return;
+    mbar_expect_tx(&full[u], C::UNIT);
+    for (int d = 0; d < C::DU / 64; ++d)
+      tma_load3(smem_addr(sm + C::RING + u * C::UNIT + d * 16384), map, part * C::DU + 64 * d, h,
+                tl.k0 + tile * 128, &full[u]);
+  };
+  auto tile_units = [&](const CUtensorMap* map, int tile) {
+    for (int i = 0; i < C::UPT; ++i) unit(map, tile, i);
+  };
+  if (warp == 4 * C::NS && lane == 0) {
     for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], 1), mbar_init(&empty[u], 1);
     mbar_init(qfull, 1);
     for (int b = 0; b < 2; ++b) {
@@ -174,21 +195,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       mbar_init(&odone[b], 1);
     }
     fence_mbar_init();
-  }
-  if (warp == 4 * C::NS) tmem_alloc512(tslot);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = *tslot;
-  bool dead = false;
-
-  if (warp >= 4 * C::NS) {
-  // three warpgroups at 168 registers: two take 232, the producers' keeps 40
-  if constexpr (C::NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if (warp == 4 * C::NS) {
-    // ---- producer: K(0), then for each tile the values and the next keys in
-    // the order the products take them
-    if (lane == 0 && ntm > 0) {
+    if (ntm > 0) {
       mbar_expect_tx(qfull, (uint32_t)(C::NS * (D / 64) * p.G * toks * 128));
 #pragma unroll
       for (int s = 0; s < C::NS; ++s) {
@@ -196,21 +203,22 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
           tma_load4(smem_addr(sm + s * C::QS + d * 16384), &maps.q, 64 * d, 0, h,
                     tl.q0 + i0 + s * toks, qfull);
       }
-      int n = 0;
-      auto unit = [&](const CUtensorMap* map, int tile, int part) {
-        const int u = n % C::NU;
-        if (n >= C::NU) tc_wait(&empty[u], (uint32_t)((n / C::NU - 1) & 1), dead);
-        ++n;
-        if (dead) return;
-        mbar_expect_tx(&full[u], C::UNIT);
-        for (int d = 0; d < C::DU / 64; ++d)
-          tma_load3(smem_addr(sm + C::RING + u * C::UNIT + d * 16384), map,
-                    part * C::DU + 64 * d, h, tl.k0 + tile * 128, &full[u]);
-      };
-      auto tile_units = [&](const CUtensorMap* map, int tile) {
-        for (int i = 0; i < C::UPT; ++i) unit(map, tile, i);
-      };
       tile_units(&maps.k, 0);
+    }
+  }
+  if (warp == 4 * C::NS + 1) tmem_alloc512(tslot);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = *tslot;
+
+  if (warp >= 4 * C::NS) {
+  // three warpgroups at 168 registers: two take 232, the producers' keeps 40
+  if constexpr (C::NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  if (warp == 4 * C::NS) {
+    // ---- producer: after K(0), for each tile the values and the next keys in
+    // the order the products take them
+    if (lane == 0 && ntm > 0) {
       for (int j = 0; j < ntm; ++j) {
         if (C::NS == 1 && j + 1 < ntm) tile_units(&maps.k, j + 1);
         tile_units(&maps.v, j);
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       }
       // every copy has landed before the CTA leaves
       bool late = false;
-      for (int k = max(0, n - C::NU); k < n; ++k)
+      for (int k = max(0, issued - C::NU); k < issued; ++k)
         tc_wait(&full[k % C::NU], (uint32_t)((k / C::NU) & 1), late);
       dead |= late;
     }
@@ -435,13 +443,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
         tmem_ld32(tb + lane_at + C::O0 + s * D + d, o);
         tmem_ld_wait32(o);
       }
-      float t = 0.f;
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         o[i] = none ? 0.f : o[i] * inv;
-        t = fmaf(o[i], 0.f, t);  // NaN where any is non-finite
+        t[i & 3] = fmaf(o[i], 0.f, t[i & 3]);  // NaN where any is non-finite
       }
-      bad |= t != 0.f;
+      bad |= t[0] + t[1] + (t[2] + t[3]) != 0.f;
 #pragma unroll
       for (int i = 0; i < 32; i += 8)
         *reinterpret_cast<uint4*>(st + unit_off<32>(lane, (d + i) / 8)) =
@@ -452,13 +460,12 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     if (!dead) {
       constexpr int U = D * 2 / 16;  // 16-byte units of a row
 #pragma unroll 4
-      for (int i = lane; i < 32 * U; i += 32) {
-        const int r = i / U, u = i % U, at = 32 * (warp & 3) + r;
-        if (at < R) {
-          T* out = static_cast<T*>(p.o) +
-                   ((size_t)(tl.q0 + tok0 + at / p.G) * p.HQ + h * p.G + at % p.G) * D;
-          reinterpret_cast<uint4*>(out)[u] = *reinterpret_cast<const uint4*>(st + unit_off<32>(r, u));
-        }
+      for (int i = 0; i < U; ++i) {
+        const int r = (32 * i + lane) / U, u = lane % U;
+        const size_t to = __shfl_sync(kFull, orow, r);  // the row's place, from its thread
+        if (32 * (warp & 3) + r < R)
+          reinterpret_cast<uint4*>(static_cast<T*>(p.o) + to * D)[u] =
+              *reinterpret_cast<const uint4*>(st + unit_off<32>(r, u));
       }
     }
     __syncwarp();  // before any of these rows is written again
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   if (dead && lane == 0) atomicOr(p.err, DEVERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 4 * C::NS) tmem_dealloc512(tb);
+  if (warp == 4 * C::NS + 1) tmem_dealloc512(tb);
 }
 
 bool encode(CUtensorMap* map, int dt, int rank, const void* base, const cuuint64_t* dims,
