@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
                  : "memory");
   const int toks = 128 / p.G;                       // tokens of a stream
   const int h = (int)(blockIdx.x % (unsigned)p.HKV);  // heads of a tile side by side
-  if (!find_tile(p, C::NS * toks, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl))
+  if (!find_tile(p, C::NS * toks * p.G, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl))
     return;
   const int i0 = tl.tile * C::NS * toks;
   const int past = tl.lk - tl.lq;

@@ -39,10 +39,10 @@ __device__ __forceinline__ bool prompt_span(const PromptParams& p, int r, bool t
   return true;
 }
 
-// Tile `index` of the launch (tiles of `toks` query tokens, sequences in
-// order, a sequence's last tile first: it sees the most keys). Each warp finds
+// Tile `index` of the launch (tiles of `rows` query rows, a row being a token
+// and one of the G query heads of a key head; sequences in order, a sequence's last tile first: it sees the most keys). Each warp finds
 // it by itself; false when the launch has fewer tiles.
-__device__ __forceinline__ bool find_tile(const PromptParams& p, int toks, int index, bool tell,
+__device__ __forceinline__ bool find_tile(const PromptParams& p, int rows, int index, bool tell,
                                           PromptTile& out) {
   const int lane = threadIdx.x & 31;
   int before = 0;
@@ -51,7 +51,7 @@ __device__ __forceinline__ bool find_tile(const PromptParams& p, int toks, int i
     const int r = r0 + lane;
     int q0 = 0, k0 = 0, lq = 0, lk = 0, n = 0;
     if (r < p.B && prompt_span(p, r, tell && index == 0, q0, lq, k0, lk))
-      n = (lq + toks - 1) / toks;
+      n = (int)(((long long)lq * p.G + rows - 1) / rows);
     int incl = n;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
