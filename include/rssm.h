@@ -536,7 +536,7 @@ rssm_status rssm_kv_compact(rssm_kv_handle *h, void *stream);
 
 /* Rotary positions: pair i < pairs of a head turns dimensions i and i + pairs
  * by the angle position * frequency_i, read from `table`, device
- * fp32[max_pos][2][pairs] (cosines, then sines). Positions have `axes` axes
+ * fp32[max_pos][2][pairs] (cosines, then sines), 16-byte aligned. Positions have `axes` axes
  * (1..3; time, height, width): the first sections[0] pairs go by axis 0, the
  * next sections[1] by axis 1, and so on; with `interleaved` non-zero pair i
  * goes by axis a = i % axes where i < axes * sections[a], else by axis 0.

@@ -246,7 +246,7 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
   if ((q == nullptr) != (q_out == nullptr)) return RSSM_ERR_INVALID_ARG;
   AppendParams p{};
   if (rope != nullptr) {
-    if (rope->table == nullptr || !aligned4(rope->table) || rope->max_pos < 1)
+    if (rope->table == nullptr || !aligned16(rope->table) || rope->max_pos < 1)
       return RSSM_ERR_INVALID_ARG;
     if (rope->axes < 1 || rope->axes > kMaxRopeAxes) return RSSM_ERR_UNSUPPORTED;
     if (rope->pairs < 1 || 2 * (int64_t)rope->pairs > c.D) return RSSM_ERR_INVALID_ARG;

@@ -42,17 +42,35 @@ __device__ __forceinline__ int cta_scan(int x, int* sums, int tid, int& total) {
   return incl - x + (warp > 0 ? before : 0);
 }
 
+// Eight neighbouring pages' reference counts per thread: a block of 8192 pages
+// costs one trip to memory and one scan. Pages outside the pool count as used.
+constexpr int kPerThread = 8;
+constexpr int kPlanBlock = kPlanThreads * kPerThread;
+__device__ __forceinline__ void load_refs(const PageParams& p, int first, int (&r)[kPerThread]) {
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i)
+    r[i] = first + i < p.n_pages ? __ldcg(p.refs + first + i) : 1;
+}
+
 // The lowest `want` pages with refs == 0, in order, into list; how many there are.
 __device__ __forceinline__ int free_pages(const PageParams& p, int32_t* list, int want, int* sums,
                                           int tid) {
   int got = 0;
-  for (int b = 0; b < p.n_pages && got < want; b += kPlanThreads) {
-    const int i = b + tid;
-    const int f = i < p.n_pages && __ldcg(p.refs + i) == 0;
-    int n;
-    const int at = got + cta_scan(f, sums, tid, n);
-    if (f && at < want) list[at] = i;
-    got += n;
+  for (int b = 0; b < p.n_pages && got < want; b += kPlanBlock) {
+    const int first = b + tid * kPerThread;
+    int r[kPerThread], n = 0, all;
+    load_refs(p, first, r);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) n += r[i] == 0;
+    int at = got + cta_scan(n, sums, tid, all);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (r[i] == 0) {
+        if (at < want) list[at] = first + i;
+        ++at;
+      }
+    }
+    got += all;
   }
   __syncthreads();
   return got < want ? got : want;
@@ -64,29 +82,31 @@ __device__ __forceinline__ bool page_ok(const PageParams& p, int page) {
   return false;
 }
 
-// One reference less to each page of the rows' slots; the slots end empty. A
-// warp per row.
-__device__ __forceinline__ void release_rows(const PageParams& p, int tid) {
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int r = warp; r < p.B; r += kPlanThreads / 32) {
+// Eight lanes to a row: 128 rows at a time, so that a plan for a batch is a few
+// trips to memory long, not a few per row.
+constexpr int kRowLanes = 8;
+constexpr int kRowsAtOnce = kPlanThreads / kRowLanes;
+
+// One reference less to each page of the rows' slots; the slots end empty.
+__global__ void __launch_bounds__(kPlanThreads) plan_release_kernel(const PageParams p) {
+  const int sub = threadIdx.x % kRowLanes;
+  for (int r = threadIdx.x / kRowLanes; r < p.B; r += kRowsAtOnce) {
     const int s = p.slot[r];
-    if (s < 0 || (p.parent != nullptr && p.parent[r] < 0)) continue;
-    if (s >= p.n_slots || (p.parent != nullptr && (p.parent[r] >= p.n_slots || p.parent[r] == s))) {
-      if (lane == 0) atomicOr(p.err, DEVERR_SLOT);
+    if (s < 0) continue;
+    if (s >= p.n_slots) {
+      if (sub == 0) atomicOr(p.err, DEVERR_SLOT);
       continue;
     }
     int32_t* row = p.table + (size_t)s * p.max_pages;
     const int held = min(max(p.held[s], 0), p.max_pages);
-    for (int i = lane; i < held; i += 32) {
+#pragma unroll 4
+    for (int i = sub; i < held; i += kRowLanes) {
       const int page = row[i];
-      if (page_ok(p, page) && atomicSub(p.refs + page, 1) <= 0) {
-        atomicAdd(p.refs + page, 1);  // never below zero
-        atomicOr(p.err, DEVERR_PAGES);
-      }
+      if (page_ok(p, page)) atomicSub(p.refs + page, 1);
       row[i] = -1;
     }
-    __syncwarp();
-    if (lane == 0) p.held[s] = 0, p.length[s] = 0;
+    __syncwarp(0xffu << (threadIdx.x & 24));  // the row's lanes have read held
+    if (sub == 0) p.held[s] = 0, p.length[s] = 0;
   }
 }
 
@@ -126,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_reserve_kernel(const PagePa
     int n;
     const int at = total + cta_scan(need, sums, tid, n);
     if (r < p.B) p.rows[r] = at;
-    total += n;
+    total = min(total + n, 1 << 30);
   }
   if (tid == 0) p.rows[p.B] = total;
   __syncthreads();
@@ -149,88 +169,106 @@ __global__ void __launch_bounds__(kPlanThreads) plan_reserve_kernel(const PagePa
   }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_release_kernel(const PageParams p) {
-  release_rows(p, threadIdx.x);
+// What a row of a fork takes: `whole` shared pages, `need` new ones.
+struct ForkRow {
+  int s, d, held, len, whole, need;
+};
+__device__ __forceinline__ ForkRow fork_row(const PageParams& p, int r, bool tell) {
+  ForkRow f{-1, -1, 0, 0, 0, 0};
+  if (r >= p.B) return f;
+  const int s = p.parent[r], d = p.slot[r];
+  if (s < 0 || d < 0) return f;
+  if (s >= p.n_slots || d >= p.n_slots || s == d) {
+    if (tell) atomicOr(p.err, DEVERR_SLOT);
+    return f;
+  }
+  const int len = p.length[s], held = p.held[s];
+  f.d = d;
+  f.held = min(max(p.held[d], 0), p.max_pages);
+  if (len < 0 || len > ((long long)min(max(held, 0), p.max_pages) << p.shift)) {
+    if (tell) atomicOr(p.err, len < 0 ? DEVERR_CURSOR : DEVERR_PAGES);
+    return f;  // the destination ends empty
+  }
+  f.s = s;
+  f.len = len;
+  f.whole = p.deep ? 0 : len >> p.shift;
+  f.need = (int)(((long long)len + (1 << p.shift) - 1) >> p.shift) - f.whole;
+  return f;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PageParams p) {
   __shared__ int sums[32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int page = 1 << p.shift;
-  release_rows(p, tid);
-  __syncthreads();
-  // what each row shares and what it needs new
-  auto row_of = [&](int r, int& s, int& d, int& len, int& whole, int& need) {
-    s = p.parent[r];
-    d = p.slot[r];
-    if (s < 0 || d < 0 || s >= p.n_slots || d >= p.n_slots || s == d) return false;
-    len = p.length[s];
-    if (len < 0 || len > ((long long)min(max(p.held[s], 0), p.max_pages) << p.shift)) {
-      atomicOr(p.err, len < 0 ? DEVERR_CURSOR : DEVERR_PAGES);
-      return false;
-    }
-    const int pages = (int)(((long long)len + page - 1) >> p.shift);
-    whole = p.deep ? 0 : len >> p.shift;
-    need = pages - whole;
-    return true;
-  };
+  asm volatile("griddepcontrol.launch_dependents;");  // the copies' launch
+  __shared__ ForkRow rows[kPlanThreads];
+  const int tid = threadIdx.x, sub = tid % kRowLanes;
+  // every row's needs before any length is changed (p.rows: first new page)
   int total = 0;
   for (int b = 0; b < p.B; b += kPlanThreads) {
-    const int r = b + tid;
-    int s, d, len, whole, need = 0;
-    if (r < p.B && !row_of(r, s, d, len, whole, need)) need = 0;
+    const ForkRow f = fork_row(p, b + tid, true);
+    if (b == 0) rows[tid] = f;
     int n;
-    const int at = total + cta_scan(need, sums, tid, n);
-    if (r < p.B) p.rows[r] = at;
-    total += n;
+    const int at = total + cta_scan(f.need, sums, tid, n);
+    if (b + tid < p.B) p.rows[b + tid] = at;
+    total = min(total + n, 1 << 30);
   }
   if (tid == 0) p.rows[p.B] = total;
   __syncthreads();
-  for (int r = warp; r < p.B; r += kPlanThreads / 32) {
-    int s, d, len, whole, need;
-    if (p.deep || !row_of(r, s, d, len, whole, need)) continue;
-    for (int i = lane; i < whole; i += 32) {
-      const int pg = p.table[(size_t)s * p.max_pages + i];
-      if (page_ok(p, pg)) atomicAdd(p.refs + pg, 1);
+  // the destinations give back what they hold and share the sources' full
+  // pages (no page is handed out in between, so none is lost by the order)
+  for (int b = 0; b < p.B; b += kRowsAtOnce) {
+    const int r = b + tid / kRowLanes;
+    const ForkRow f = r < kPlanThreads ? rows[r] : fork_row(p, r, false);
+    if (f.d < 0) continue;
+    int32_t* to = p.table + (size_t)f.d * p.max_pages;
+    const int32_t* from = p.table + (size_t)max(f.s, 0) * p.max_pages;
+#pragma unroll 4
+    for (int i = sub; i < max(f.held, f.whole); i += kRowLanes) {
+      const int old = i < f.held ? to[i] : -1, pg = i < f.whole ? from[i] : -1;
+      if (i < f.held && page_ok(p, old)) atomicSub(p.refs + old, 1);
+      if (i < f.whole && page_ok(p, pg)) atomicAdd(p.refs + pg, 1);
+      to[i] = pg;
     }
   }
   __syncthreads();
   const int got = total > 0 ? free_pages(p, p.dst, min(total, p.n_pages), sums, tid) : 0;
-  __syncthreads();
   int moves = 0;
-  for (int b = 0; b < p.B; b += kPlanThreads / 32) {
-    const int r = b + warp;
-    int s, d, len, whole, need;
-    if (r >= p.B || !row_of(r, s, d, len, whole, need)) continue;
+  for (int b = 0; b < p.B; b += kRowsAtOnce) {
+    const int r = b + tid / kRowLanes;
+    // lengths and pages held of sources are as they were: none is a destination
+    const ForkRow f = r < kPlanThreads ? rows[r] : fork_row(p, r, false);
+    if (f.d < 0) continue;
+    int32_t* to = p.table + (size_t)f.d * p.max_pages;
+    const int32_t* from = p.table + (size_t)max(f.s, 0) * p.max_pages;
     const int at = p.rows[r];
-    const int32_t* from = p.table + (size_t)s * p.max_pages;
-    int32_t* to = p.table + (size_t)d * p.max_pages;
-    if (at + need > got) {  // not enough pages: the row shares nothing after all
-      for (int i = lane; i < whole; i += 32) {
+    const bool fits = f.s >= 0 && (f.need == 0 || at + f.need <= got);
+    if (f.s >= 0 && !fits) {  // not enough pages: the row shares nothing after all
+      for (int i = sub; i < f.whole; i += kRowLanes) {
         if (from[i] >= 0 && from[i] < p.n_pages) atomicSub(p.refs + from[i], 1);
+        to[i] = -1;
       }
-      if (lane == 0) atomicOr(p.err, DEVERR_PAGES);
-      continue;
+      if (sub == 0) atomicOr(p.err, DEVERR_PAGES);
     }
-    for (int i = lane; i < whole + need; i += 32) {
-      const int pg = from[i];
-      if (i < whole) {
-        to[i] = pg;
-      } else {
-        const int at_i = at + i - whole, fresh = p.dst[at_i];
-        to[i] = fresh;
+    if (fits) {
+      for (int i = sub; i < f.need; i += kRowLanes) {
+        const int pg = from[f.whole + i], fresh = p.dst[at + i];
+        to[f.whole + i] = fresh;
         p.refs[fresh] = 1;
-        p.src[at_i] = page_ok(p, pg) ? pg : fresh;
+        p.src[at + i] = page_ok(p, pg) ? pg : fresh;
       }
+      moves = max(moves, at + f.need);
     }
-    if (lane == 0) p.held[d] = whole + need, p.length[d] = len;
-    moves = max(moves, at + need);
+    if (sub == 0) {
+      p.held[f.d] = fits ? f.whole + f.need : 0;
+      p.length[f.d] = fits ? f.len : 0;
+    }
   }
-  if (lane == 0) sums[warp] = moves;
+  moves = __reduce_max_sync(kFull, moves);
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 0; w < kPlanThreads / 32; ++w) moves = max(moves, sums[w]);
-    *p.moves = moves;
+  if (tid % 32 == 0) sums[tid / 32] = moves;
+  __syncthreads();
+  if (tid < 32) {
+    moves = __reduce_max_sync(kFull, sums[tid]);
+    if (tid == 0) *p.moves = moves;
   }
 }
 
@@ -238,26 +276,42 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PageParam
 // (U pages are in use) to the n-th free place within them.
 __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const PageParams p) {
   __shared__ int sums[32];
+  asm volatile("griddepcontrol.launch_dependents;");  // the copies' launch
   const int tid = threadIdx.x;
-  int used = 0;
-  for (int b = 0; b < p.n_pages; b += kPlanThreads) {
-    const int i = b + tid;
-    used += __syncthreads_count(i < p.n_pages && p.refs[i] > 0);
+  int r[kPerThread], used = 0, n = 0;
+  for (int b = 0; b < p.n_pages; b += kPlanBlock) {
+    const int first = b + tid * kPerThread;
+    load_refs(p, first, r);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) n += first + i < p.n_pages && r[i] > 0;
   }
+  cta_scan(n, sums, tid, used);
   int holes = 0, movers = 0;
-  for (int b = 0; b < p.n_pages; b += kPlanThreads) {
-    const int i = b + tid;
-    const bool in = i < p.n_pages;
-    const bool live = in && p.refs[i] > 0;
-    const int h = in && i < used && !live, m = in && i >= used && live;
-    int nh, nm;
-    const int ah = holes + cta_scan(h, sums, tid, nh);
-    const int am = movers + cta_scan(m, sums, tid, nm);
-    if (h) p.dst[ah] = i;
-    if (m) p.src[am] = i;
-    if (in) p.map[i] = i;
-    holes += nh;
-    movers += nm;
+  for (int b = 0; b < p.n_pages; b += kPlanBlock) {
+    const int first = b + tid * kPerThread;
+    if (p.n_pages > kPlanBlock) load_refs(p, first, r);  // else they are at hand
+    int both = 0, all;  // free places in the low half word, pages to move in the high one
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (first + i < p.n_pages) {
+        both += first + i < used ? r[i] <= 0 : (r[i] > 0) << 16;
+        p.map[first + i] = first + i;
+      }
+    }
+    const int before = cta_scan(both, sums, tid, all);
+    int ah = holes + (before & 0xffff), am = movers + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      if (first + i < p.n_pages) {
+        if (first + i < used) {
+          if (r[i] <= 0) p.dst[ah++] = first + i;
+        } else if (r[i] > 0) {
+          p.src[am++] = first + i;
+        }
+      }
+    }
+    holes += all & 0xffff;
+    movers += all >> 16;
   }
   __syncthreads();
   for (int i = tid; i < movers; i += kPlanThreads) {
@@ -275,6 +329,9 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;
 
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const CopyParams p) {
+  // launched while the plan runs (its CTA leaves the other SMs idle); waits
+  // here until the plan has ended and its list can be seen
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int moves = *p.moves;
   constexpr size_t step = (size_t)kCopyThreads * kCopyVecs * 16;
   const size_t chunks = (p.page_bytes + step - 1) / step;
@@ -349,8 +406,16 @@ cudaError_t kv_plan_launch(int mode, const PageParams& p, cudaStream_t st) {
 }
 
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st) {
-  page_copy_kernel<<<num_sms * 8, kCopyThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)num_sms * 8);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, page_copy_kernel, p);
 }
 
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st) {
