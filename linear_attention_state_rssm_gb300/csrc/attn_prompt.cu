@@ -7,12 +7,13 @@
 //
 // A CTA takes 32 query rows of one key head: a row is a token and one of the G
 // query heads that share the key head, so that short prompts fill rows and the
-// keys of a head are read once for its whole group. KG groups of two warps share the keys out in tiles
+// keys of a head are read once for its whole group. KG groups of one or two warps share the keys out in tiles
 // of 16, each staging its own by 16-byte async copies one tile ahead, and are
 // joined at the end: the FMA units want many warps, and a prompt of a thousand
 // tokens has few rows. (64 rows and one group of four warps: 104 us where this
-// takes PROMPT_F32 us, five prompts of 290 to 957 keys.) Tiles of longer sight
-// come first in the grid. Bound by the FMA units: 4 D operations per pair.
+// takes 50 us, five prompts of 290 to 957 keys.) Tiles of longer sight
+// come first in the grid. Bound by shared memory (85% busy): a 16-byte load feeds
+// 4 multiply-adds for each row and key that a lane holds of the other operand.
 #include "attn_core.cuh"
 #include "attn_tiles.cuh"
 #include "kv_common.cuh"
@@ -23,10 +24,11 @@ namespace {
 
 template <int D>
 struct PromptCfg {
-  static constexpr int RW = 2;                                    // row warps of a group
-  static constexpr int KG = D == 64 ? 8 : D == 128 ? 6 : 3;       // groups: registers, then shared
+  static constexpr int MB = D == 64 ? 2 : 1;                      // sixteens of rows of a warp
+  static constexpr int RW = 2 / MB;                               // row warps of a group
+  static constexpr int KG = D == 64 ? 12 : D == 128 ? 6 : 3;      // groups: registers, then shared
   static constexpr int NT = 32 * RW * KG;                         // memory, hold no more
-  static constexpr int ROWS = 16 * RW;
+  static constexpr int ROWS = 16 * MB * RW;
   static constexpr int KEYS = 16;
   static constexpr int QBYTES = ROWS * D * 4;
   static constexpr int TBYTES = KEYS * D * 4;
@@ -45,7 +47,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::NT, 1)
   extern __shared__ __align__(1024) unsigned char sm[];
   PromptTile tl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int grp = warp / C::RW, wr = 16 * (warp % C::RW);  // keys' group, first row
+  const int grp = warp / C::RW, wr = 16 * C::MB * (warp % C::RW);  // keys' group, first row
   const int gtid = tid % (32 * C::RW);
   const int h = (int)(blockIdx.x % (unsigned)p.HKV);    // heads of a tile side by side
   if (!find_tile(p, C::ROWS, (int)(blockIdx.x / (unsigned)p.HKV), h == 0 && tid < 32, tl)) return;
@@ -88,28 +90,37 @@ __global__ void __launch_bounds__(PromptCfg<D>::NT, 1)
         live ? reinterpret_cast<const uint4*>(q)[u] : make_uint4(0, 0, 0, 0);
   }
 
-  int lim[1][2];
+  int lim[C::MB][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    lim[0][e] = max(0, past + token(min(wr + 8 * e + (lane >> 2), R - 1)) + 1);
+  for (int b = 0; b < C::MB; ++b) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      lim[b][e] = max(0, past + token(min(wr + 16 * b + 8 * e + (lane >> 2), R - 1)) + 1);
   }
   const int fewest = max(0, past + token(min(wr, R - 1)) + 1);
-  const int most = max(0, past + token(min(wr + 15, R - 1)) + 1);
+  const int most = max(0, past + token(min(wr + 16 * C::MB - 1, R - 1)) + 1);
 
-  WarpAttn<T, D, 1, C::ROWS, C::KEYS> w;
+  WarpAttn<T, D, C::MB, C::ROWS, C::KEYS> w;
+  auto sync = [&] {  // the group's warps
+    if constexpr (C::RW == 1) {
+      __syncwarp();
+    } else {
+      named_sync(1 + grp, 32 * C::RW);
+    }
+  };
   w.clear();
   __syncthreads();
   for (int i = 0; (grp + i * C::KG) * C::KEYS < keys; ++i) {
     const int key0 = (grp + i * C::KG) * C::KEYS;
     cp_async_wait<1>();
-    named_sync(1 + grp, 32 * C::RW);
+    sync();
     const unsigned char* ks = kv + (i & 1) * 2 * C::TBYTES;
     if (key0 < most && wr < R) {
-      float x[1][C::KEYS / 8][4];
+      float x[C::MB][C::KEYS / 8][4];
       w.template weights<C::KEYS / 8>(x, qs + wr * 128, ks, key0, lim, fewest, p.c, lane);
       w.template add<C::KEYS / 8>(x, ks + C::TBYTES, key0, lim, fewest, lane);
     }
-    named_sync(1 + grp, 32 * C::RW);
+    sync();
     issue(i + 2);
   }
   cp_async_wait<0>();
@@ -121,25 +132,31 @@ __global__ void __launch_bounds__(PromptCfg<D>::NT, 1)
   const int g = lane >> 2, t = lane & 3;
   if (t == 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      sm_m[grp * C::ROWS + wr + 8 * e + g] = w.m[0][e];
-      sm_l[grp * C::ROWS + wr + 8 * e + g] = w.l[0][e];
+    for (int b = 0; b < C::MB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sm_m[grp * C::ROWS + wr + 16 * b + 8 * e + g] = w.m[b][e];
+        sm_l[grp * C::ROWS + wr + 16 * b + 8 * e + g] = w.l[b][e];
+      }
     }
   }
   __syncthreads();
   float* os = reinterpret_cast<float*>(sm);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int rr = wr + 8 * e + g;
-    float mx = kNegInf;
+  for (int b = 0; b < C::MB; ++b) {
 #pragma unroll
-    for (int k = 0; k < C::KG; ++k) mx = fmaxf(mx, sm_m[k * C::ROWS + rr]);
-    const float f = exp2_fast(w.m[0][e] - (mx == kNegInf ? 0.f : mx));
-    if (rr < R) {
+    for (int e = 0; e < 2; ++e) {
+      const int rr = wr + 16 * b + 8 * e + g;
+      float mx = kNegInf;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(os + (grp * C::ROWS + rr) * C::OP + w.col(i, t)) =
-            make_float2(w.o[0][i][2 * e] * f, w.o[0][i][2 * e + 1] * f);
+      for (int k = 0; k < C::KG; ++k) mx = fmaxf(mx, sm_m[k * C::ROWS + rr]);
+      const float f = exp2_fast(w.m[b][e] - (mx == kNegInf ? 0.f : mx));
+      if (rr < R) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          *reinterpret_cast<float2*>(os + (grp * C::ROWS + rr) * C::OP + w.col(i, t)) =
+              make_float2(w.o[b][i][2 * e] * f, w.o[b][i][2 * e + 1] * f);
+      }
     }
   }
   __syncthreads();
