@@ -291,10 +291,11 @@ struct WarpAttn {
     }
   }
 
-  // o += p v with the keys that a row does not see left out by selection
-  template <int NT>
-  __device__ __forceinline__ void pv_select(const float (&p)[MB][NT][4], const unsigned char* vs,
-                                         int key0, const int (&lim)[MB][2], int lane) {
+  // o += p v with the keys that a row does not see left out by selection;
+  // fetch(key, d): values d, d + 1 of a key of the chunk
+  template <int NT, typename F>
+  __device__ __forceinline__ void pv_select(const float (&p)[MB][NT][4], F fetch, int key0,
+                                            const int (&lim)[MB][2], int lane) {
     const int t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -312,9 +313,8 @@ struct WarpAttn {
           const bool s0 = key0 + key < lim[b][0], s1 = key0 + key < lim[b][1];
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
-            constexpr int E = 16 / (int)sizeof(T);  // col(i, t) is even: two of one unit
-            const T* v = reinterpret_cast<const T*>(vs + key_off(key, col(i, t) / E)) + col(i, t) % E;
-            const float v0 = attn_f32(v[0]), v1 = attn_f32(v[1]);
+            const float2 v = fetch(key, col(i, t));
+            const float v0 = v.x, v1 = v.y;
             if (s0) o[b][i][0] = fmaf(p0, v0, o[b][i][0]), o[b][i][1] = fmaf(p0, v1, o[b][i][1]);
             if (s1) o[b][i][2] = fmaf(p1, v0, o[b][i][2]), o[b][i][3] = fmaf(p1, v1, o[b][i][3]);
           }
@@ -354,6 +354,13 @@ struct WarpAttn {
                                           const unsigned char* ks, int key0,
                                           const int (&lim)[MB][2], int all, float c, int lane) {
     scores<NT>(x, qs, ks, lane);
+    soften<NT>(x, key0, lim, all, c, lane);
+  }
+
+  // x: scores in, weights out
+  template <int NT>
+  __device__ __forceinline__ void soften(float (&x)[MB][NT][4], int key0,
+                                         const int (&lim)[MB][2], int all, float c, int lane) {
     const int t = lane & 3;
     const bool masked = key0 + 8 * NT > all;
 #pragma unroll
@@ -404,7 +411,14 @@ struct WarpAttn {
                                       int key0, const int (&lim)[MB][2], int all, int lane) {
     static_assert(8 * NT % KR == 0, "whole blocks of keys");
     if (key0 + 8 * NT > all && any_unfinite<NT>(vs, lane)) {
-      pv_select<NT>(p, vs, key0, lim, lane);
+      pv_select<NT>(
+          p,
+          [&](int key, int d) {
+            constexpr int E = 16 / (int)sizeof(T);  // d is even: two values of one unit
+            const T* v = reinterpret_cast<const T*>(vs + key_off(key, d / E)) + d % E;
+            return make_float2(attn_f32(v[0]), attn_f32(v[1]));
+          },
+          key0, lim, lane);
     } else {
       pv<NT>(p, vs, lane);
     }

@@ -7,7 +7,8 @@
 //
 // A CTA takes 32 query rows of one key head: a row is a token and one of the G
 // query heads that share the key head, so that short prompts fill rows and the
-// keys of a head are read once for its whole group. KG groups of one or two warps share the keys out in tiles
+// keys of a head are read once for its whole group. KG groups of one or two
+// warps share the keys out in tiles
 // of 16, each staging its own by 16-byte async copies one tile ahead, and are
 // joined at the end: the FMA units want many warps, and a prompt of a thousand
 // tokens has few rows. (64 rows and one group of four warps: 104 us where this

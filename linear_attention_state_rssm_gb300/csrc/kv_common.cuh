@@ -155,5 +155,7 @@ cudaError_t attn_prompt_prepare(int D, int dt);
 cudaError_t attn_prompt_launch(const PromptParams& p, cudaStream_t st);
 cudaError_t attn_prompt_tc_prepare(int D, int dt);  // 16-bit types
 cudaError_t attn_prompt_tc_launch(const PromptParams& p, cudaStream_t st);
+cudaError_t attn_prompt_tc_wide_prepare(int dt);    // and D = 256
+cudaError_t attn_prompt_tc_wide_launch(const PromptParams& p, cudaStream_t st);
 
 }  // namespace rssm
