@@ -553,11 +553,14 @@ typedef struct rssm_rope {
 
 /*
  * One layer's new tokens: q_out = rotated q, and rotated k and v written to the
- * slots' pages at cache positions length[s] + i. Row r's tokens are
+ * slots' pages at cache positions length[s] + i. k_out (may be null), contiguous
+ * [N][HKV][D], 16-byte aligned, takes the rotated keys once more, in a row, as
+ * rssm_attn_prefill reads them. Row r's tokens are
  * [r T, (r + 1) T) of N = B T, or [cu_seqlens[r], cu_seqlens[r+1]) of N.
  * positions is device int32[axes][N]; null: a token's place in its cache on
  * every axis. rope null: no rotation. q and q_out may both be null (keys and
- * values only), and q_out may be q itself where q is contiguous. Two rows may
+ * values only), and q_out may be q itself, and k_out k, where
+ * that is contiguous. Two rows may
  * not write the same slot. A token past its slot's pages sets
  * RSSM_DEVERR_PAGES, one with a position outside [0, max_pos)
  * RSSM_DEVERR_POSITION: that token is skipped.
@@ -568,7 +571,7 @@ rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
                            const rssm_rope *rope, const int32_t *positions,
                            const int32_t *cu_seqlens, const int32_t *slot,
                            int32_t B, int32_t T, int32_t N, void *q_out,
-                           void *stream);
+                           void *k_out, void *stream);
 
 /*
  * Attention of a window of T (1 <= T <= 64) new tokens per row over the

@@ -134,7 +134,7 @@ def load() -> ctypes.CDLL:
         "rssm_kv_release": ([_P, _P, _I, _P], _I),
         "rssm_kv_compact": ([_P, _P], _I),
         "rssm_kv_append": ([_P, _I, _P, _P, _P, _L, _L, _L, ctypes.POINTER(rssm_rope), _P, _P, _P,
-                            _I, _I, _I, _P, _P], _I),
+                            _I, _I, _I, _P, _P, _P], _I),
         "rssm_attn_decode": ([_P, _I, _P, _L, _P, _I, _I, _P, _P, _P], _I),
         "rssm_attn_prefill": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P],
                               _I),
@@ -374,11 +374,11 @@ def rssm_kv_compact(handle, stream=None):
 
 
 def rssm_kv_append(handle, layer, q, k, v, q_stride, k_stride, v_stride, rope, positions,
-                   cu_seqlens, slot, B, T, N, q_out, stream=None):
+                   cu_seqlens, slot, B, T, N, q_out, k_out=None, stream=None):
     _check(load().rssm_kv_append(handle, layer, _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride,
                                  v_stride, None if rope is None else ctypes.byref(rope),
                                  _ptr(positions), _ptr(cu_seqlens), _ptr(slot), B, T, N,
-                                 _ptr(q_out), _stream(stream)), "rssm_kv_append")
+                                 _ptr(q_out), _ptr(k_out), _stream(stream)), "rssm_kv_append")
 
 
 def rssm_attn_decode(handle, layer, q, q_stride, slot, B, T, o, lse, stream=None):

@@ -235,7 +235,7 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
                            const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                            const rssm_rope* rope, const int32_t* positions,
                            const int32_t* cu_seqlens, const int32_t* slot, int32_t B, int32_t T,
-                           int32_t N, void* q_out, void* stream) {
+                           int32_t N, void* q_out, void* k_out, void* stream) {
   const rssm_status st = check_rows(h, slot, B);
   if (st != RSSM_OK) return st;
   const rssm_kv_config& c = h->cfg;
@@ -270,10 +270,12 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
     return RSSM_ERR_INVALID_ARG;
   if (q != nullptr && (!tokens_ok(c, q, q_stride, c.HQ) || !aligned16(q_out)))
     return RSSM_ERR_INVALID_ARG;
+  if (!aligned16(k_out)) return RSSM_ERR_INVALID_ARG;
   p.q = q;
   p.k = k;
   p.v = v;
   p.q_out = q_out;
+  p.k_out = k_out;
   p.kp = static_cast<unsigned char*>(h->buf.k_pages) + (size_t)layer * h->layer_bytes;
   p.vp = static_cast<unsigned char*>(h->buf.v_pages) + (size_t)layer * h->layer_bytes;
   p.cu = cu_seqlens;

@@ -206,6 +206,12 @@ __global__ void __launch_bounds__(kAppendThreads, 7)
                              : reinterpret_cast<uint4*>(p.vp + off + (h - hq - p.HKV) * head_bytes);
           to[val ? 2 * j : v0] = a[k];
           to[val ? 2 * j + 1 : v1] = b[k];
+          if (p.k_out != nullptr && h >= hq && !val) {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(p.k_out) +
+                                                  ((size_t)tok * p.HKV + h - hq) * p.D);
+            out[v0] = a[k];
+            out[v1] = b[k];
+          }
         }
       }
     }

@@ -90,6 +90,7 @@ struct AppendParams {
   const void* k;
   const void* v;
   void* q_out;
+  void* k_out;        // or null
   unsigned char* kp;  // this layer's pages
   unsigned char* vp;
   const float* rope;         // [max_pos][2][P] cosines, sines; null: no rotation

@@ -258,20 +258,24 @@ class KVCache:
 
     # ------------------------------------------------------------ attention
     def rssm_kv_append(self, layer, q, k, v, slot, T=1, q_out=None, rope=None, positions=None,
-                       cu_seqlens=None, stream=None):
-        """Rotate q (into q_out) and k, write k and v to the slots' pages."""
+                       cu_seqlens=None, k_out=None, stream=None):
+        """Rotate q (into q_out) and k, write k and v to the slots' pages (and
+        the rotated k to k_out, for rssm_attn_prefill)."""
         n, ks = self._tokens(k, self.HKV)
         _, vs = self._tokens(v, self.HKV, n)
         qs = self._tokens(q, self.HQ, n)[1] if q is not None else 0
         if q_out is not None:
             self._output(q_out, n)
+        if k_out is not None and (k_out.dtype != self._torch_dtype or not k_out.is_contiguous()
+                                  or k_out.numel() != n * self.HKV * self.D):
+            raise ValueError("k_out: contiguous, the cache's dtype, [tokens, HKV, D]")
         if positions is not None and (rope is None or positions.dtype != torch.int32
                                       or positions.numel() != rope.axes * n
                                       or not positions.is_contiguous()):
             raise ValueError("positions: contiguous int32 [axes, tokens], with a rotary table")
         _lib.rssm_kv_append(self.handle, layer, q, k, v, qs, ks, vs,
                             None if rope is None else rope.struct, positions, cu_seqlens, slot,
-                            slot.numel(), T, n, q_out, stream)
+                            slot.numel(), T, n, q_out, k_out, stream)
 
     def rssm_attn_decode(self, layer, q, slot, T, o, lse=None, stream=None):
         """T new tokens per row over the slot's pages (their keys appended before)."""

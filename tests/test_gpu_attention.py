@@ -305,10 +305,11 @@ def test_append_rotates_and_writes_the_pages(dtype, D, pairs, sections, inter):
     pos = rng.integers(0, most, (axes, 4 * T))
     rope = RotaryTable.from_base(most, pairs, 1e4, sections, inter)
     out = torch.full((4 * T, HQ, D), SENTINEL, dtype=TORCH[dtype], device="cuda")
+    kout = torch.full((4 * T, HKV, D), SENTINEL, dtype=TORCH[dtype], device="cuda")
     before = c.k_pages.clone()
     slots = [2, -1, 0, 3]
     c.rssm_kv_append(1, x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], ints(slots), T, out,
-                     rope=rope, positions=torch.from_numpy(pos).int().cuda())
+                     rope=rope, positions=torch.from_numpy(pos).int().cuda(), k_out=kout)
     assert c.rssm_kv_get_device_error() == 0
     freq = 1e4 ** (-np.arange(pairs) / pairs)
     y = ref.rotate(xd[:, :HQ + HKV], pos.astype(float), freq,
@@ -320,6 +321,7 @@ def test_append_rotates_and_writes_the_pages(dtype, D, pairs, sections, inter):
     off = np.abs(out.double().cpu().numpy()[live] - y[live, :HQ]).max()
     assert off <= 1.5 * u * amp
     assert (out[torch.from_numpy(~live)] == SENTINEL).all()
+    assert (kout[torch.from_numpy(~live)] == SENTINEL).all()
     written = torch.zeros(c.k_pages.shape[1], page, dtype=torch.bool)
     for r, s in enumerate(slots):
         for i in range(T if s >= 0 else 0):
@@ -329,6 +331,7 @@ def test_append_rotates_and_writes_the_pages(dtype, D, pairs, sections, inter):
             k = c.k_pages[1, pg, :, at % page].double().cpu().numpy()
             v = c.v_pages[1, pg, :, at % page].double().cpu().numpy()
             assert np.abs(k - y[r * T + i, HQ:]).max() <= 1.5 * u * amp
+            assert np.array_equal(kout[r * T + i].double().cpu().numpy(), k)
             assert np.array_equal(v, xd[r * T + i, HQ + HKV:])
     same = (c.k_pages[1] == before[1]) | (c.k_pages[1].isnan() & before[1].isnan())
     assert same.transpose(1, 2)[~written].all()
