@@ -18,8 +18,17 @@
 // In a CTA one producer warp walks the stretch ahead of the others, over the
 // ends of rows too: it looks the pages up and has one thread issue one TMA box
 // per 16 keys and one per 16 values into a ring. Each stream (one
-// warp per 16 rows of the block) takes every NG-th chunk of the CTA; streams meet only
-// where a row ends, while the ring fills with the next row's chunks.
+// warp per 16 rows of the block) takes every NG-th chunk of the CTA; streams meet
+// only where a row ends, while the ring fills with the next row's chunks.
+//
+// Measured (GB300, back to back): 56 rows of 1 to 8 k tokens, 16/4 heads of 256:
+// 131 us, 6.3 TB/s (93% of the copy rate); two rows of 110 to 131 k tokens, 32/8
+// heads of 128, fp16: 159 us, 6.2 TB/s; 125 windows of 8 tokens over 0.3 to 3 k
+// tokens, 16/4 heads of 128: 68 us, 4.3 TB/s, held back by the ends of its 2.5
+// stretches a CTA (11 k cycles each, of 128 k) and by steps of two warps to a
+// stream. Steps: private rings of cp.async per warp and whole CTAs to a row 142,
+// 160, 113 us; the gap on the line 93 for the windows; this ring 86; rows of a
+// join loaded side by side and 32 keys a step 68.
 #include "attn_core.cuh"
 #include "attn_tma.h"
 #include "kv_common.cuh"

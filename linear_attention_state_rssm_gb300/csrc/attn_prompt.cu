@@ -8,13 +8,13 @@
 // A CTA takes 32 query rows of one key head: a row is a token and one of the G
 // query heads that share the key head, so that short prompts fill rows and the
 // keys of a head are read once for its whole group. KG groups of one or two
-// warps share the keys out in tiles
-// of 16, each staging its own by 16-byte async copies one tile ahead, and are
-// joined at the end: the FMA units want many warps, and a prompt of a thousand
-// tokens has few rows. (64 rows and one group of four warps: 104 us where this
-// takes 50 us, five prompts of 290 to 957 keys.) Tiles of longer sight
-// come first in the grid. Bound by shared memory (85% busy): a 16-byte load feeds
-// 4 multiply-adds for each row and key that a lane holds of the other operand.
+// warps share the keys out in tiles of 16, each staging its own by 16-byte async
+// copies one tile ahead, and are joined at the end: the FMA units want many
+// warps, and a prompt of a thousand tokens has few rows. (64 rows and one group
+// of four warps: 104 us where this takes 51 us, five prompts of 290 to 957 keys.)
+// Tiles of longer sight come first in the grid. Bound by shared memory (85% busy
+// with prompts of two thousand tokens): a 16-byte load feeds 4 multiply-adds for
+// each row and key that a lane holds of the other operand.
 #include "attn_core.cuh"
 #include "attn_tiles.cuh"
 #include "kv_common.cuh"

@@ -11,11 +11,12 @@
 // the tiles of CTAs that have not begun (cluster launch control): the next
 // tile's queries and keys are loaded, and its first scores computed, while the
 // last one's output is written. Eight prompts of 64 to 4096 tokens, 16/4 heads:
-// 305 us with a CTA per tile, 274 us (1.39 PFLOP/s of causal products, 72% of
-// the library's matrix product rate).
+// 305 us with a CTA per tile, 275 us so, back to back (1.39 PFLOP/s of causal
+// products, 72% of the library's matrix product); 257 us by itself.
 //
 // What bounds it: shared memory. A step's products take 2048 cycles; feeding
-// them reads 192 KB and writes 128 KB there, 2500 cycles at 128 bytes.
+// them reads 192 KB and writes 128 KB there, 2500 cycles at 128 bytes (tensor
+// cores 66% busy). Two CTAs sharing their keys (cta_group::2) would halve that.
 #include "attn_prompt_tc.cuh"
 
 namespace rssm {
