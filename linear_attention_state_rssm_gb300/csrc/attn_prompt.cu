@@ -11,10 +11,11 @@
 // warps share the keys out in tiles of 16, each staging its own by 16-byte async
 // copies one tile ahead, and are joined at the end: the FMA units want many
 // warps, and a prompt of a thousand tokens has few rows. (64 rows and one group
-// of four warps: 104 us where this takes 51 us, five prompts of 290 to 957 keys.)
-// Tiles of longer sight come first in the grid. Bound by shared memory (85% busy
-// with prompts of two thousand tokens): a 16-byte load feeds 4 multiply-adds for
-// each row and key that a lane holds of the other operand.
+// of four warps: 104 us where this takes 51 us, five prompts of 302 to 957 keys.)
+// Tiles of longer sight come first in the grid. Longer prompts (eight, the longest
+// of 2048 tokens: 299 us) issue on 63% of cycles with shared memory 61% busy, no unit
+// full: 12 warps per SM wait out shared loads and reductions (168 registers and
+// 203 KB leave no room for more).
 #include "attn_core.cuh"
 #include "attn_tiles.cuh"
 #include "kv_common.cuh"
