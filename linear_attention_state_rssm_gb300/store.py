@@ -171,8 +171,8 @@ class RotaryTable:
 
     def __init__(self, table, sections=None, interleaved=False):
         if table.dtype != torch.float32 or table.dim() != 3 or table.shape[1] != 2 \
-                or not table.is_contiguous():
-            raise ValueError("table: contiguous fp32 [max_pos, 2, pairs]")
+                or not table.is_cuda or not table.is_contiguous():
+            raise ValueError("table: contiguous fp32 [max_pos, 2, pairs] on the device")
         sections = [table.shape[2]] if sections is None else list(sections)
         if not 1 <= len(sections) <= 3:
             raise ValueError("sections: one to three axes")
@@ -237,20 +237,25 @@ class KVCache:
     # ---------------------------------------------------------------- pages
     def rssm_kv_reserve(self, slot, T=1, cu_seqlens=None, stream=None):
         """Pages for the next T tokens of each row (or for its cu_seqlens)."""
-        _lib.rssm_kv_reserve(self.handle, slot, cu_seqlens, slot.numel(), T, stream)
+        B = self._index(slot)
+        self._index(cu_seqlens, B + 1)
+        _lib.rssm_kv_reserve(self.handle, slot, cu_seqlens, B, T, stream)
 
     def rssm_kv_commit(self, slot, T=1, accept_len=None, cu_seqlens=None, stream=None):
         """length += accepted tokens (the whole window where accept_len is None)."""
-        _lib.rssm_kv_commit(self.handle, slot, accept_len, cu_seqlens, slot.numel(), T, stream)
+        B = self._index(slot)
+        self._index(accept_len, B)
+        self._index(cu_seqlens, B + 1)
+        _lib.rssm_kv_commit(self.handle, slot, accept_len, cu_seqlens, B, T, stream)
 
     def rssm_kv_fork(self, src, dst, deep=False, stream=None):
         """Slot dst[r] continues slot src[r]: full pages shared (deep: copied)."""
-        if src.numel() != dst.numel():
-            raise ValueError("one source per destination")
-        _lib.rssm_kv_fork(self.handle, src, dst, src.numel(), deep, stream)
+        B = self._index(src)
+        self._index(dst, B)
+        _lib.rssm_kv_fork(self.handle, src, dst, B, deep, stream)
 
     def rssm_kv_release(self, slot, stream=None):
-        _lib.rssm_kv_release(self.handle, slot, slot.numel(), stream)
+        _lib.rssm_kv_release(self.handle, slot, self._index(slot), stream)
 
     def rssm_kv_compact(self, stream=None):
         """Pages in use move to the front of the pool."""
@@ -261,25 +266,27 @@ class KVCache:
                        cu_seqlens=None, k_out=None, stream=None):
         """Rotate q (into q_out) and k, write k and v to the slots' pages (and
         the rotated k to k_out, for rssm_attn_prefill)."""
+        B = self._index(slot)
+        self._index(cu_seqlens, B + 1)
         n, ks = self._tokens(k, self.HKV)
         _, vs = self._tokens(v, self.HKV, n)
         qs = self._tokens(q, self.HQ, n)[1] if q is not None else 0
         if q_out is not None:
             self._output(q_out, n)
         if k_out is not None and (k_out.dtype != self._torch_dtype or not k_out.is_contiguous()
-                                  or k_out.numel() != n * self.HKV * self.D):
+                                  or not k_out.is_cuda or k_out.numel() != n * self.HKV * self.D):
             raise ValueError("k_out: contiguous, the cache's dtype, [tokens, HKV, D]")
-        if positions is not None and (rope is None or positions.dtype != torch.int32
-                                      or positions.numel() != rope.axes * n
-                                      or not positions.is_contiguous()):
-            raise ValueError("positions: contiguous int32 [axes, tokens], with a rotary table")
+        if positions is not None:
+            if rope is None:
+                raise ValueError("positions: with a rotary table")
+            self._index(positions, rope.axes * n)
         _lib.rssm_kv_append(self.handle, layer, q, k, v, qs, ks, vs,
                             None if rope is None else rope.struct, positions, cu_seqlens, slot,
-                            slot.numel(), T, n, q_out, k_out, stream)
+                            B, T, n, q_out, k_out, stream)
 
     def rssm_attn_decode(self, layer, q, slot, T, o, lse=None, stream=None):
         """T new tokens per row over the slot's pages (their keys appended before)."""
-        B = slot.numel()
+        B = self._index(slot)
         _, qs = self._tokens(q, self.HQ, B * T)
         self._output(o, B * T, lse)
         _lib.rssm_attn_decode(self.handle, layer, q, qs, slot, B, T, o, lse, stream)
@@ -287,12 +294,15 @@ class KVCache:
     def rssm_attn_prefill(self, q, k, v, cu_seqlens, slot, o, cu_keys=None, lse=None,
                           stream=None):
         """Causal attention over packed prompts (cu_seqlens int32, B + 1)."""
+        B = self._index(cu_seqlens) - 1
+        self._index(slot, B)
+        self._index(cu_keys, B + 1)
         n, qs = self._tokens(q, self.HQ)
         m, ks = self._tokens(k, self.HKV, n if cu_keys is None else None)
         _, vs = self._tokens(v, self.HKV, m)
         self._output(o, n, lse)
-        _lib.rssm_attn_prefill(self.handle, q, k, v, qs, ks, vs, cu_seqlens, cu_keys, slot,
-                               cu_seqlens.numel() - 1, n, m, o, lse, stream)
+        _lib.rssm_attn_prefill(self.handle, q, k, v, qs, ks, vs, cu_seqlens, cu_keys, slot, B, n,
+                               m, o, lse, stream)
 
     def rssm_kv_get_device_error(self, clear=True, stream=None) -> int:
         return _lib.rssm_kv_get_device_error(self.handle, clear, stream)
@@ -309,6 +319,19 @@ class KVCache:
             pass
 
     # ------------------------------------------------------------- helpers
+    @staticmethod
+    def _index(x, n=None):
+        """Entries of an index tensor; the kernels read it as n int32 in a run
+        and cannot see where it ends."""
+        if x is None:
+            return 0
+        m = x.numel()
+        if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous():
+            raise ValueError("index tensors: contiguous int32 on the device")
+        if n is not None and m != n:
+            raise ValueError(f"expected {n} entries, got {m}")
+        return m
+
     def _tokens(self, x, heads, n=None):
         """Tokens and token stride of [n, heads, D] (heads and D contiguous)."""
         D = self.D
@@ -319,13 +342,13 @@ class KVCache:
             m = h = d = -1
         if h != heads or d != D or (n is not None and m != n):
             raise ValueError(f"expected {n or 'N'} x {heads} x {D}, got {tuple(x.shape)}")
-        if x.dtype != self._torch_dtype or s2 != 1 or (s1 != D and heads > 1):
-            raise ValueError("the cache's dtype, with contiguous heads")
+        if x.dtype != self._torch_dtype or not x.is_cuda or s2 != 1 or (s1 != D and heads > 1):
+            raise ValueError("the cache's dtype, on the device, with contiguous heads")
         return m, s0 if m > 1 else heads * D
 
     def _output(self, o, n, lse=None):
         if o.dtype != self._torch_dtype or o.numel() != n * self.HQ * self.D \
-                or not o.is_contiguous():
+                or not o.is_cuda or not o.is_contiguous():
             raise ValueError("outputs: contiguous, the cache's dtype, [tokens, HQ, D]")
         if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * self.HQ
                                 or not lse.is_contiguous()):

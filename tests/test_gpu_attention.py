@@ -5,9 +5,10 @@ Tolerances. The weights p enter the product with v rounded to the input type
 11) and the output is rounded once more, so a value is off by at most
 2 u sum_j p_j |v_j|; fp32 sums of up to a few thousand terms and the base-2
 exponential add below 1e-4 of the same mass. f16 weights under 2^-14 lose up to
-2^-25 each: below 2e-4 of |v| at the lengths used. fp32 products are split in
-tf32 head and tail (2^-21 per operand): scores of D = 256 are off by less than
-2e-5, and the outputs by less than 6e-5 of the mass.
+2^-25 each: below 2e-4 of |v| at the lengths used. fp32 has room for products
+split in two tf32 parts (2^-21 per operand: scores of D = 256 off by less than
+2e-5, outputs by less than 6e-5 of the mass); the kernels' fp32 FMAs stay well
+inside.
 """
 import numpy as np
 import pytest
@@ -488,6 +489,40 @@ def test_pages_refusals():
     c.rssm_kv_fork(ints([0]), ints([3]))
     assert c.rssm_kv_get_device_error() == lib.DEVERR["slot"]
     assert c.length.tolist() == [0, 0, 0] and c.held.tolist() == [2, 0, 0]
+
+
+def test_index_tensors_that_the_kernels_would_misread_are_refused():
+    from linear_attention_state_rssm_gb300.store import RotaryTable
+    c, slot = cache(n_slots=4, HQ=2, HKV=1, D=64, n_pages=8, page_size=16), ints([0, 1])
+    q, o = (torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, cu, rope = q[:, :1], ints([0, 1, 2]), RotaryTable.from_base(64, 32)
+    good = dict(slot=slot, cu=cu, cu_keys=None, accept=None, pos=None, q=q)
+
+    def calls(slot, cu, cu_keys, accept, pos, q):
+        return {"reserve": lambda: c.rssm_kv_reserve(slot, cu_seqlens=cu),
+                "append": lambda: c.rssm_kv_append(0, q, k, k, slot, 1, o, rope, pos, cu),
+                "decode": lambda: c.rssm_attn_decode(0, q, slot, 1, o),
+                "prefill": lambda: c.rssm_attn_prefill(q, k, k, cu, slot, o, cu_keys=cu_keys),
+                "commit": lambda: c.rssm_kv_commit(slot, 1, accept, cu),
+                "fork": lambda: c.rssm_kv_fork(slot, ints([2, 3])),
+                "release": lambda: c.rssm_kv_release(slot)}
+
+    takes_slot = tuple(calls(**good))
+    bad = [(dict(slot=s), takes_slot) for s in (slot.long(), slot.cpu(), ints([0, 9, 1, 9])[::2])]
+    bad += [(dict(slot=ints([0])), ("reserve", "append", "decode", "prefill", "commit", "fork"))]
+    bad += [(dict(cu=x), ("reserve", "append", "prefill", "commit"))
+            for x in (cu[:2], cu.long(), cu.cpu())]
+    bad += [(dict(cu_keys=cu[:2]), ("prefill",)), (dict(accept=ints([1])), ("commit",)),
+            (dict(accept=ints([1, 1]).long()), ("commit",)), (dict(pos=ints([0])), ("append",)),
+            (dict(q=q.cpu()), ("append", "decode", "prefill"))]
+    for change, names in bad:
+        for name in names:
+            with pytest.raises(ValueError):
+                calls(**{**good, **change})[name]()
+    assert c.held.tolist() == [0] * 4
+    for call in calls(**good).values():
+        call()
+    assert c.rssm_kv_get_device_error() == 0
 
 
 # ------------------------------------------------------------------ together

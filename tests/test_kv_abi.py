@@ -116,3 +116,13 @@ def test_reference_pages_by_hand():
     m.compact()
     assert m.refs == [1, 1, 1, 0, 0, 0] and m.table == [[], [1], [0, 2]]
     assert m.data[:3] == [0, 3, 1]
+
+
+def test_index_tensors_off_the_device_are_refused():
+    import torch
+    from linear_attention_state_rssm_gb300.store import KVCache, RotaryTable
+    assert KVCache._index(None, 3) == 0
+    with pytest.raises(ValueError):
+        KVCache._index(torch.zeros(3, dtype=torch.int32), 3)
+    with pytest.raises(ValueError):
+        RotaryTable(torch.zeros(4, 2, 32))
