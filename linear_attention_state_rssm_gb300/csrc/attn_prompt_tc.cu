@@ -126,10 +126,13 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     }
     fence_mbar_init();
     if (ntm > 0) {
-      mbar_expect_tx(qfull, (uint32_t)(C::NS * (D / 64) * p.G * toks * 128));
+      // A stream without a step gets no queries: nothing tells it when they have
+      // landed, and its block stages its output from the start.
+      const int with = (nt[0] > 0) + (nt[1] > 0);
+      mbar_expect_tx(qfull, (uint32_t)(with * (D / 64) * p.G * toks * 128));
 #pragma unroll
       for (int s = 0; s < C::NS; ++s) {
-        for (int d = 0; d < D / 64; ++d)
+        for (int d = 0; d < D / 64 && nt[s] > 0; ++d)
           tma_load4(smem_addr(sm + s * C::QS + d * 16384), &maps.q, 64 * d, 0, h,
                     tl.q0 + i0 + s * toks, qfull);
       }

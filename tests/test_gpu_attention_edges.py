@@ -1,0 +1,49 @@
+"""The full-attention layers' operators where their parts meet: streams of a tile
+without work, waits that run out, sums of page plans near their limits, rows
+with refused offsets. Tolerances are those of test_gpu_attention.py."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attention import SENTINEL, TORCH, cache, draw, ints, rng_of, run_prompt
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from linear_attention_state_rssm_gb300 import build
+    build.build()
+
+
+# ------------------------------------------- a stream of a tile without a key
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("HQ,HKV,lq,lk", [
+    (2, 2, 256, 100),      # 128 tokens to a stream: the first sees nothing, the second does
+    (3, 1, 84, 40),        # 42 tokens
+    (64, 1, 4, 1),         # two tokens
+    (4, 2, 300, 3)])       # tiles of which both, one and no stream sees nothing
+def test_prompt_stream_without_any_key(dtype, D, HQ, HKV, lq, lk):
+    """Rows that see no key are 0 and -inf whichever part of a tile they fill, every time."""
+    o, lse = run_prompt(dtype, HQ, HKV, D, [lq], [lk], 51)
+    none = lq - lk
+    assert (o[:none] == 0).all() and torch.isneginf(lse[:none]).all()
+    # many tiles at once, many times: a load of queries that lands late would show in these rows
+    B = 40
+    rng = rng_of(52, D)
+    q, k, v = (draw(rng, (B * n, h, D), dtype)[0] for n, h in ((lq, HQ), (lk, HKV), (lk, HKV)))
+    c = cache(n_slots=B, HQ=HQ, HKV=HKV, D=D, page_size=16, dtype=dtype)
+    cu, cuk = ints(range(0, B * lq + 1, lq)), ints(range(0, B * lk + 1, lk))
+    first = None
+    for _ in range(20):
+        o = torch.full_like(q, SENTINEL)
+        lse = torch.full((B * lq, HQ), SENTINEL, device="cuda")
+        c.rssm_attn_prefill(q, k, v, cu, None, o, cu_keys=cuk, lse=lse)
+        assert (o.view(B, lq, HQ, D)[:, :none] == 0).all()
+        assert torch.isneginf(lse.view(B, lq, HQ)[:, :none]).all()
+        first = o if first is None else first
+        assert torch.equal(o, first)
+    assert c.rssm_kv_get_device_error() == 0
