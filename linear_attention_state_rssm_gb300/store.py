@@ -351,5 +351,5 @@ class KVCache:
                 or not o.is_cuda or not o.is_contiguous():
             raise ValueError("outputs: contiguous, the cache's dtype, [tokens, HQ, D]")
         if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * self.HQ
-                                or not lse.is_contiguous()):
-            raise ValueError("lse: contiguous fp32 [tokens, HQ]")
+                                or not lse.is_cuda or not lse.is_contiguous()):
+            raise ValueError("lse: contiguous fp32 [tokens, HQ] on the device")

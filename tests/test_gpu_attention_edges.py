@@ -47,3 +47,14 @@ def test_prompt_stream_without_any_key(dtype, D, HQ, HKV, lq, lk):
         first = o if first is None else first
         assert torch.equal(o, first)
     assert c.rssm_kv_get_device_error() == 0
+
+
+# ------------------------------------------------------------ host-side tensors
+def test_lse_in_host_memory_is_refused():
+    c = cache(n_slots=2, HQ=2, HKV=1, D=64, n_pages=2, page_size=16)
+    q, o = (torch.zeros((2, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, slot, lse = q[:, :1], ints([0, 1]), torch.zeros(2, 2)
+    with pytest.raises(ValueError):
+        c.rssm_attn_decode(0, q, slot, 1, o, lse=lse)
+    with pytest.raises(ValueError):
+        c.rssm_attn_prefill(q, k, k, ints([0, 1, 2]), slot, o, lse=lse)
