@@ -581,7 +581,8 @@ rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
  * q is [B T][HQ][D]. A slot may be named by several rows. A row whose window
  * is not within its pages sets RSSM_DEVERR_PAGES and is skipped; a table entry
  * outside the pool sets it too and leaves that row's output undefined (nothing
- * outside the pool is read).
+ * outside the pool is read). Where a wait runs out (RSSM_DEVERR_TIMEOUT) some
+ * of the outputs are left as they are; what is stored is right.
  */
 rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
                              int64_t q_stride, const int32_t *slot, int32_t B,
@@ -607,6 +608,17 @@ rssm_status rssm_attn_prefill(rssm_kv_handle *h, const void *q, const void *k,
 /* As rssm_get_device_error, for a cache's error word. */
 rssm_status rssm_kv_get_device_error(rssm_kv_handle *h, uint32_t *out,
                                      int32_t clear, void *stream);
+
+/*
+ * Test and debugging hook of the bounded waits, as rssm_debug_withhold: in
+ * later launches of rssm_attn_decode place `unit` (modulo their number) of the
+ * ring into which CTA `cta` of the launch copies keys and values by turns is
+ * promised, for its first copy, 16 bytes more than the copy brings. So every
+ * wait on it runs out after the usual 0.5 s; the copies themselves all land.
+ * cta -1: off, as after rssm_kv_alloc. Host state only. Never on in production
+ * calls.
+ */
+rssm_status rssm_kv_debug_withhold(rssm_kv_handle *h, int32_t cta, int32_t unit);
 
 const char *rssm_status_string(rssm_status s);
 

@@ -32,7 +32,7 @@ SYMBOLS = ("rssm_required_bytes", "rssm_alloc", "rssm_free", "rssm_decode", "rss
            "rssm_kv_required_bytes", "rssm_kv_alloc", "rssm_kv_free", "rssm_kv_reserve",
            "rssm_kv_commit", "rssm_kv_fork", "rssm_kv_release", "rssm_kv_compact",
            "rssm_kv_append", "rssm_attn_decode", "rssm_attn_prefill",
-           "rssm_kv_get_device_error")
+           "rssm_kv_get_device_error", "rssm_kv_debug_withhold")
 
 
 class RssmError(RuntimeError):
@@ -139,6 +139,7 @@ def load() -> ctypes.CDLL:
         "rssm_attn_prefill": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P],
                               _I),
         "rssm_kv_get_device_error": ([_P, ctypes.POINTER(ctypes.c_uint32), _I, _P], _I),
+        "rssm_kv_debug_withhold": ([_P, _I, _I], _I),
         "rssm_status_string": ([_I], ctypes.c_char_p),
         "rssm_version": ([], _I),
     }
@@ -400,3 +401,7 @@ def rssm_kv_get_device_error(handle, clear=True, stream=None) -> int:
     if st not in (RSSM_OK, 4):
         raise RssmError(st, "rssm_kv_get_device_error")
     return int(word.value)
+
+
+def rssm_kv_debug_withhold(handle, cta, unit=0):
+    _check(load().rssm_kv_debug_withhold(handle, int(cta), int(unit)), "rssm_kv_debug_withhold")

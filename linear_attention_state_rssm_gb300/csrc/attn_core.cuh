@@ -119,6 +119,13 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
+// Test hook of the bounded waits: the barrier's phase waits for `bytes` more
+// than its copies bring, so every wait on it runs out.
+__device__ __forceinline__ void mbar_promise(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
+}
 // Byte offset of 16-byte unit u of row r in a block of ROWS rows.
 template <int ROWS>
 __device__ __forceinline__ uint32_t unit_off(int r, int u) {

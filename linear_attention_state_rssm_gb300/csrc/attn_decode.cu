@@ -185,6 +185,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
     for (int i = 0; i < 2; ++i) mbar_init(&qfull[i], 33), mbar_init(&qempty[i], NW);
     *issued = 0;
     for (int i = 0; i < 4; ++i) flag[i] = 0;
+    if (p.hook_cta == (int)blockIdx.x) mbar_promise(&full[p.hook_unit % C::NU], 16);
     fence_mbar_init();
   }
   // ---- the line's length and its longest row, and the row that holds this
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
     // ---- producer
     Seg sg;
     int n = 0, ns = 0;  // chunks and segments issued
+    int stop = 0x7fffffff;  // the unit that was not sent for, once a wait ran out (lane 0)
     while (!dead) {
       sg.more = line.next(p, sg);
       // the segment's description and its query rows (zeros after the last),
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
               const int u = 2 * n + kv, at_u = u % C::NU;
               if (!dead && u >= C::NU &&
                   !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1)))
-                dead = true;
+                dead = true, stop = u;
               if (!dead) {
                 mbar_expect_tx(&full[at_u], C::UNIT);
 #pragma unroll
@@ -345,12 +347,18 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
         dead = __any_sync(kFull, dead);
       }
     }
-    // every copy has landed before the CTA leaves
+    // Every copy has landed before the CTA leaves. Once a wait ran out the copies
+    // on their way get one more limit between them (a slot's earlier units were
+    // read, or it would not have been filled again).
     if (lane == 0) {
-      for (int u = max(0, 2 * n - C::NU); u < 2 * n && !dead; ++u)
-        dead = !mbar_wait_bounded(&full[u % C::NU], (uint32_t)((u / C::NU) & 1));
-      if (dead) atomicOr(p.err, DEVERR_TIMEOUT);
+      bool late = false;
+      const int sent = min(2 * n, stop);
+      for (int u = max(0, sent - C::NU); u < sent; ++u)
+        late |= !mbar_wait_bounded(&full[u % C::NU], (uint32_t)((u / C::NU) & 1),
+                                   late ? 0 : kWaitLimitNs);
+      if (dead || late) atomicOr(p.err, DEVERR_TIMEOUT);
     }
+    if (dead) cp_async_wait_all();  // the queries'
     return;
   }
 
@@ -403,11 +411,13 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
       dead = !landed(u);
       w.template weights<C::CH / 8>(x, qw, ring + uk * C::UNIT, key0, lim, fewest, p.c, lane);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[uk]);
+      // A unit that was not seen to land is not given back: the producer would
+      // fill a slot, and arm a barrier, whose last copy is still on its way.
+      if (lane == 0 && !dead) mbar_arrive(&empty[uk]);
       dead |= !landed(u + 1);
       w.template add<C::CH / 8>(x, ring + uv * C::UNIT, key0, lim, fewest, lane);
       dead = __any_sync(kFull, dead);
-      if (lane == 0) mbar_arrive(&empty[uv]);
+      if (lane == 0 && !dead) mbar_arrive(&empty[uv]);
     }
     n0 += nc;
     w.finish();
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
         if (!whole) {
           part[C::ROWS * D + rr] = mx;
           part[C::ROWS * (D + 1) + rr] = sum;
-        } else if (p.lse != nullptr && !dead) {
+        } else if (p.lse != nullptr && (NG > 1 ? flag[0] == 0 : !dead)) {
           p.lse[out_row(rr)] = lse_of(mx, sum);
         }
       }

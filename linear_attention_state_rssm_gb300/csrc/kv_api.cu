@@ -15,6 +15,7 @@ struct rssm_kv_handle {
   int shift;            // log2(page_size)
   size_t layer_bytes;   // one layer's keys (or values)
   size_t page_bytes;    // one page of one layer's keys (or values)
+  int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   alignas(64) unsigned char maps[kKvMapBytes];  // the pool's tensor maps
 };
 
@@ -141,6 +142,7 @@ rssm_status rssm_kv_alloc(const rssm_kv_config* cfg, const rssm_kv_buffers* buf,
   while ((1 << h->shift) < cfg->page_size) ++h->shift;
   h->page_bytes = page_bytes(*cfg);
   h->layer_bytes = (size_t)cfg->n_pages * h->page_bytes;
+  h->hook_cta = h->hook_unit = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess)
@@ -338,6 +340,8 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   p.shift = h->shift;
   const int rows = attn_decode_block_rows(c.D, c.dtype, T * p.G);
   p.nmb = (T * p.G + rows - 1) / rows;
+  p.hook_cta = h->hook_cta;
+  p.hook_unit = h->hook_unit;
   p.c = (float)((double)c.scale * 1.4426950408889634);
   return from_cuda(
       attn_decode_launch(p, h->maps, c.D, c.dtype, h->num_sms,
@@ -383,6 +387,13 @@ rssm_status rssm_attn_prefill(rssm_kv_handle* h, const void* q, const void* k, c
   p.dt = c.dtype;
   p.c = (float)((double)c.scale * 1.4426950408889634);
   return from_cuda(attn_prompt_launch(p, static_cast<cudaStream_t>(stream)));
+}
+
+rssm_status rssm_kv_debug_withhold(rssm_kv_handle* h, int32_t cta, int32_t unit) {
+  if (h == nullptr || cta < -1 || (cta >= 0 && unit < 0)) return RSSM_ERR_INVALID_ARG;
+  h->hook_cta = cta;
+  h->hook_unit = cta < 0 ? -1 : unit;
+  return RSSM_OK;
 }
 
 rssm_status rssm_kv_get_device_error(rssm_kv_handle* h, uint32_t* out, int32_t clear,

@@ -122,6 +122,7 @@ struct DecodeParams {
   long long page0;  // the layer's first page among all layers'
   int B, T, HQ, HKV, G, n_slots, n_pages, max_pages, shift;
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
+  int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   float c;      // scale * log2(e)
 };
 

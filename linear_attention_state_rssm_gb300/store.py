@@ -307,6 +307,11 @@ class KVCache:
     def rssm_kv_get_device_error(self, clear=True, stream=None) -> int:
         return _lib.rssm_kv_get_device_error(self.handle, clear, stream)
 
+    def rssm_kv_debug_withhold(self, cta, unit=0):
+        """Test hook of the bounded waits (include/rssm.h): later launches of this
+        cache short-change a unit of CTA ``cta`` (-1: off)."""
+        _lib.rssm_kv_debug_withhold(self.handle, cta, unit)
+
     def close(self):
         if getattr(self, "handle", None):
             _lib.rssm_kv_free(self.handle)

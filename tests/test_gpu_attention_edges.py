@@ -1,11 +1,13 @@
 """The full-attention layers' operators where their parts meet: streams of a tile
 without work, waits that run out, sums of page plans near their limits, rows
 with refused offsets. Tolerances are those of test_gpu_attention.py."""
-import numpy as np
+import time
+
 import pytest
 import torch
 
-from test_gpu_attention import SENTINEL, TORCH, cache, draw, ints, rng_of, run_prompt
+from linear_attention_state_rssm_gb300._lib import DEVERR
+from test_gpu_attention import SENTINEL, cache, draw, filled, ints, rng_of, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +60,53 @@ def test_lse_in_host_memory_is_refused():
         c.rssm_attn_decode(0, q, slot, 1, o, lse=lse)
     with pytest.raises(ValueError):
         c.rssm_attn_prefill(q, k, k, ints([0, 1, 2]), slot, o, lse=lse)
+
+
+# ---------------------------------------------------------- waits that run out
+def timed(call):
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    call()
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 < 30.0
+
+
+@pytest.mark.parametrize("dtype,D,HQ,T", [("bf16", 128, 4, 1), ("f16", 64, 4, 1),
+                                          ("bf16", 256, 4, 1), ("f32", 64, 2, 1),
+                                          ("bf16", 128, 4, 8), ("bf16", 128, 1, 64),
+                                          ("f16", 256, 1, 48)])
+@pytest.mark.parametrize("unit", [0, 1, 3, 8])
+def test_decode_wait_that_runs_out_leaves_the_row_alone(dtype, D, HQ, T, unit):
+    """Three rows of one length, a CTA each. One copy of the second is promised more than it
+    brings: the call returns, says so, leaves that row as it is, and the others and the next
+    call are what they are without (every copy has landed: nothing faults)."""
+    c, _ = filled(rng_of(61, D), [400 - T] * 3, T, HQ, 1, D, dtype, 16)
+    q, slot = draw(rng_of(62), (3 * T, HQ, D), dtype)[0], ints([0, 1, 2])
+
+    def decode():
+        o = torch.full_like(q, SENTINEL)
+        lse = torch.full((3 * T, HQ), SENTINEL, device="cuda")
+        timed(lambda: c.rssm_attn_decode(1, q, slot, T, o, lse=lse))
+        return o.view(3, T, HQ, D), lse.view(3, T, HQ)
+
+    clean = decode()
+    assert c.rssm_kv_get_device_error() == 0
+    c.rssm_kv_debug_withhold(1, unit)
+    late = decode()
+    assert c.rssm_kv_get_device_error() == DEVERR["timeout"]
+    c.rssm_kv_debug_withhold(-1)
+    for got, want in zip(late, clean):
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+        assert (got[1] == SENTINEL).all()
+    for got, want in zip(decode(), clean):
+        assert torch.equal(got, want)
+    assert c.rssm_kv_get_device_error() == 0
+
+
+def test_arguments_of_the_waits_hook_are_checked():
+    from linear_attention_state_rssm_gb300 import RssmError
+    c = cache(n_slots=1, HQ=1, HKV=1, D=64, page_size=16)
+    for bad in ((-2, 0), (0, -1)):
+        with pytest.raises(RssmError):
+            c.rssm_kv_debug_withhold(*bad)
+    c.rssm_kv_debug_withhold(-1)
