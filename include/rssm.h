@@ -582,7 +582,8 @@ rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
  * is not within its pages sets RSSM_DEVERR_PAGES and is skipped; a table entry
  * outside the pool sets it too and leaves that row's output undefined (nothing
  * outside the pool is read). Where a wait runs out (RSSM_DEVERR_TIMEOUT) some
- * of the outputs are left as they are; what is stored is right.
+ * of the outputs are left as they are; what is stored is right, and later
+ * calls are not touched by it.
  */
 rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
                              int64_t q_stride, const int32_t *slot, int32_t B,

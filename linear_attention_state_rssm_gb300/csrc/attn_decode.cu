@@ -41,6 +41,7 @@ constexpr int kBox = 16;        // keys of a TMA box: within one page (pages of 
 constexpr int kGapKeys = 256;   // what beginning and ending a row costs, as keys
 constexpr int kLeastKeys = 512; // keys that a CTA takes at least (of longer rows)
 constexpr int kRowParts = 96;   // parts of the longest row, about: one CTA joins them
+constexpr int kLostPart = 1 << 16;  // in a row's arrivals, beside their number: a part that is not there
 
 template <typename T, int D, int MW>
 struct DecCfg {
@@ -151,6 +152,31 @@ struct Line {
   }
 };
 
+// Counts a CTA's part of a split row in (one thread). Every part is counted,
+// there or not, so the last one clears the count for the next call whatever
+// happened, and joins the row (true) only if none is missing.
+__device__ __forceinline__ bool count_part(int32_t* count, long long item0, int chunks,
+                                           long long share, bool lost) {
+  const int cta0 = (int)(item0 / share);
+  const int parts = (int)((item0 + chunks - 1) / share) - cta0 + 1;
+  const int add = lost ? kLostPart + 1 : 1;
+  const int n = atomicAdd(count + cta0, add) + add;
+  if ((n & (kLostPart - 1)) != parts) return false;
+  count[cta0] = 0;
+  return n < kLostPart;
+}
+
+// Counts in what a CTA that gave up in its ns-th segment leaves undone.
+template <int CH>
+__device__ __noinline__ void give_up(const DecodeParams& p, Line<CH> line, int ns,
+                                     long long share) {
+  Seg g;
+  for (int i = 0; line.next(p, g); ++i) {
+    if (i >= ns && (g.c0 > 0 || g.c1 < g.chunks))
+      count_part(p.count, g.item0, g.chunks, share, true);
+  }
+}
+
 struct KvMaps {
   CUtensorMap k, v;
 };
@@ -178,12 +204,16 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
   Seg* segs = reinterpret_cast<Seg*>(scan + 3 * (NW + 1) + 3); // [2]
   volatile int* issued = reinterpret_cast<volatile int*>(segs + 2);  // units on their way
   int* flag = const_cast<int*>(issued) + 1;  // [4] no output; joins; a wait ran out (by turns)
+  // the unit that was not sent for because a wait ran out (in a register it would
+  // cost the producer's loop 1.5% of 56 rows of 1 to 8 k tokens)
+  volatile int* stop = issued + 5;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], 1), mbar_init(&empty[u], MW);
     for (int i = 0; i < 2; ++i) mbar_init(&qfull[i], 33), mbar_init(&qempty[i], NW);
     *issued = 0;
+    *stop = -1;
     for (int i = 0; i < 4; ++i) flag[i] = 0;
     if (p.hook_cta == (int)blockIdx.x) mbar_promise(&full[p.hook_unit % C::NU], 16);
     fence_mbar_init();
@@ -261,12 +291,15 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
   line.row0 = found[1];
 
   const long long begin = line.pos;
+  // for a CTA that gives up; the sums that stood there have been read
+  Line<C::CH>* from_start = reinterpret_cast<Line<C::CH>*>(scan);
+  static_assert(sizeof(Line<C::CH>) <= 3 * 8 * (NW + 1), "behind the barriers");
+  if (tid == 0) *from_start = line;
   bool dead = false;  // a bounded wait ran out
   if (warp == NW) {
     // ---- producer
     Seg sg;
     int n = 0, ns = 0;  // chunks and segments issued
-    int stop = 0x7fffffff;  // the unit that was not sent for, once a wait ran out (lane 0)
     while (!dead) {
       sg.more = line.next(p, sg);
       // the segment's description and its query rows (zeros after the last),
@@ -330,7 +363,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
               const int u = 2 * n + kv, at_u = u % C::NU;
               if (!dead && u >= C::NU &&
                   !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1)))
-                dead = true, stop = u;
+                dead = true, *stop = u;
               if (!dead) {
                 mbar_expect_tx(&full[at_u], C::UNIT);
 #pragma unroll
@@ -352,7 +385,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
     // read, or it would not have been filled again).
     if (lane == 0) {
       bool late = false;
-      const int sent = min(2 * n, stop);
+      const int sent = *stop >= 0 ? *stop : 2 * n;
       for (int u = max(0, sent - C::NU); u < sent; ++u)
         late |= !mbar_wait_bounded(&full[u % C::NU], (uint32_t)((u / C::NU) & 1),
                                    late ? 0 : kWaitLimitNs);
@@ -376,7 +409,11 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
     if (dead) flag[2 + half] = 1;
     named_sync(1, C::CT);
     const Seg sg = segs[half];
-    if (flag[2 + half] != 0 || !sg.more) break;
+    if (flag[2 + half] != 0) {
+      if (tid == 0) give_up(p, *from_start, ns, share);
+      break;
+    }
+    if (!sg.more) break;
     const int base = sg.mb * C::ROWS;                  // first of the block's T G rows
     const int R = min(C::ROWS, p.T * p.G - base);      // rows in use
     // how many keys the lane's rows see
@@ -535,9 +572,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
       named_sync(1, C::CT);
       if (tid == 0) {
         __threadfence();  // the CTA's part, and after the count the others'
-        const int n = atomicAdd(p.count + cta0, 1);
-        if (n == parts - 1) p.count[cta0] = 0;  // free for the next call
-        flag[1] = n == parts - 1;
+        flag[1] = count_part(p.count, sg.item0, sg.chunks, share, flag[0] != 0);
         __threadfence();
       }
       named_sync(1, C::CT);
@@ -576,12 +611,11 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
             if (sub == 0 && rr < R) {
               row_m[rr] = mx == kNegInf ? 0.f : mx;
               row_l[rr] = 1.f / sum;
-              if (p.lse != nullptr && flag[0] == 0) p.lse[out_row(rr)] = lse_of(mx, sum);
+              if (p.lse != nullptr) p.lse[out_row(rr)] = lse_of(mx, sum);
             }
           }
         }
         named_sync(1, C::CT);
-        const bool ok = flag[0] == 0;
         // kJoin values of four a thread at a time, so that a part's loads go out
         // together: the loop over the parts is one trip to L2 each
         constexpr int kJoin = C::ROWS >= 32 ? 8 : 4;
@@ -617,7 +651,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW>::NT, DecCfg<T, D, MW>::CPS)
 #pragma unroll
           for (int j = 0; j < kJoin; ++j) {
             const int i = i0 + j * C::CT;
-            if (i < R * (D / 4) && ok) {
+            if (i < R * (D / 4)) {
               const int rr = i / (D / 4), d = 4 * (i % (D / 4));
               const float r = row_l[rr];
               T* o = static_cast<T*>(p.o) + out_row(rr) * D + d;

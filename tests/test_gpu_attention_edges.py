@@ -103,6 +103,43 @@ def test_decode_wait_that_runs_out_leaves_the_row_alone(dtype, D, HQ, T, unit):
     assert c.rssm_kv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,D,HQ,HKV,T", [("bf16", 128, 4, 1, 1), ("f16", 64, 8, 2, 5),
+                                              ("bf16", 256, 6, 2, 9), ("f32", 128, 4, 1, 1)])
+@pytest.mark.parametrize("cta", [0, 1, 7, 39])  # 39: the end of a row and the begin of the next
+@pytest.mark.parametrize("unit", [0, 2])
+def test_decode_wait_that_runs_out_in_a_split_row(dtype, D, HQ, HKV, T, cta, unit):
+    """Rows cut over many CTAs, of which one loses a copy: each row and key head is either
+    complete or as it was, arrivals are back at zero, and the next call is right."""
+    lens = [30011, 700, 12345, 3]
+    c, _ = filled(rng_of(63, D), lens, T, HQ, HKV, D, dtype, 64)
+    q, slot = draw(rng_of(64), (4 * T, HQ, D), dtype)[0], ints([0, 1, 2, 3])
+    G = HQ // HKV
+
+    def decode():
+        o = torch.full_like(q, SENTINEL)
+        lse = torch.full((4 * T, HQ), SENTINEL, device="cuda")
+        timed(lambda: c.rssm_attn_decode(1, q, slot, T, o, lse=lse))
+        # one block of T G query rows per row and key head (of 16 or more rows: in one piece)
+        return (o.view(4, T, HKV, G, D).transpose(1, 2).flatten(2),
+                lse.view(4, T, HKV, G).transpose(1, 2).flatten(2))
+
+    clean = decode()
+    assert c.rssm_kv_get_device_error() == 0
+    c.rssm_kv_debug_withhold(cta, unit)
+    late = decode()
+    assert c.rssm_kv_get_device_error() == DEVERR["timeout"]
+    c.rssm_kv_debug_withhold(-1)
+    kept = [(got == SENTINEL).all(-1) for got in late]
+    right = [(got == want).all(-1) for got, want in zip(late, clean)]
+    assert torch.equal(kept[0], kept[1])
+    assert kept[0].any() and torch.equal(right[0], ~kept[0]) and torch.equal(right[1], ~kept[1])
+    assert (c.work[:4 * 456] == 0).all()            # the arrival counters of every CTA
+    for _ in range(2):
+        for got, want in zip(decode(), clean):
+            assert torch.equal(got, want)
+    assert c.rssm_kv_get_device_error() == 0
+
+
 def test_arguments_of_the_waits_hook_are_checked():
     from linear_attention_state_rssm_gb300 import RssmError
     c = cache(n_slots=1, HQ=1, HKV=1, D=64, page_size=16)
