@@ -597,7 +597,9 @@ rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
  * keys of earlier chunks come before the chunk's own; a query that sees none
  * (Lk < Lq) gives o = 0 and lse = -inf. The cache is not read. slot (may be
  * null) skips rows with a null slot. Offsets that decrease or leave [0, N] or
- * [0, M] set RSSM_DEVERR_SEQLEN and skip the sequence.
+ * [0, M] set RSSM_DEVERR_SEQLEN and skip the sequence. Where a wait runs out
+ * (RSSM_DEVERR_TIMEOUT) some of the outputs are left as they are; what is
+ * stored is right.
  */
 rssm_status rssm_attn_prefill(rssm_kv_handle *h, const void *q, const void *k,
                               const void *v, int64_t q_stride,
@@ -611,13 +613,14 @@ rssm_status rssm_kv_get_device_error(rssm_kv_handle *h, uint32_t *out,
                                      int32_t clear, void *stream);
 
 /*
- * Test and debugging hook of the bounded waits, as rssm_debug_withhold: in
- * later launches of rssm_attn_decode place `unit` (modulo their number) of the
- * ring into which CTA `cta` of the launch copies keys and values by turns is
- * promised, for its first copy, 16 bytes more than the copy brings. So every
- * wait on it runs out after the usual 0.5 s; the copies themselves all land.
- * cta -1: off, as after rssm_kv_alloc. Host state only. Never on in production
- * calls.
+ * Test and debugging hook of the bounded waits, as rssm_debug_withhold. CTA
+ * `cta` of a launch copies keys and values by turns into the places of a ring;
+ * in later launches of rssm_attn_decode and, for heads of 64 and 128 in 16-bit
+ * types, rssm_attn_prefill, the first copy into place `unit` (modulo their
+ * number; prompts have one more for the queries) is promised 16 bytes more than
+ * it brings. So every wait on it runs out after the usual 0.5 s; the copies
+ * themselves all land. cta -1: off, as after rssm_kv_alloc. Host state only.
+ * Never on in production calls.
  */
 rssm_status rssm_kv_debug_withhold(rssm_kv_handle *h, int32_t cta, int32_t unit);
 

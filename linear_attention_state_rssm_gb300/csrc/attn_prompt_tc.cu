@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
   uint64_t* pfull = sfull + 2;                                 // [2][2] half the weights are
   uint64_t* odone = pfull + 4;                                 // [2] a step's P V is done
   uint64_t* tail = odone + 2;                                  // the last values have landed
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(tail + 1);
+  uint64_t* drained = tail + 1;                                // no product is in flight
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  // A softmax warp whose wait ran out goes on without waiting, ahead of the
+  // others' phases, so no warp stores what it finds after that.
+  volatile uint32_t* gave_up = tslot + 1;
   PromptTile tl;
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   if (tid < 3)
@@ -107,8 +111,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     uint64_t* bar = other != nullptr ? other : &full[u];  // completed by the loads
     if (issued >= C::NU)
       tc_wait(&empty[u], (uint32_t)((issued / C::NU - 1) & 1), dead);
-    ++issued;
     if (dead) return;
+    ++issued;
     mbar_expect_tx(bar, C::UNIT);
     for (int d = 0; d < D / 64; ++d)
       tma_load3(smem_addr(sm + C::RING + u * C::UNIT + d * 16384), map, 64 * d, h,
@@ -118,12 +122,15 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], 1), mbar_init(&empty[u], 1);
     mbar_init(qfull, 1);
     mbar_init(tail, 1);
+    mbar_init(drained, 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sfull[b], 1);
       mbar_init(&pfull[2 * b], 128);
       mbar_init(&pfull[2 * b + 1], 128);
       mbar_init(&odone[b], 1);
     }
+    *gave_up = 0;
+    if (p.hook_cta == (int)blockIdx.x) promise_more<C::NU>(full, qfull, p.hook_unit);
     fence_mbar_init();
     if (ntm > 0) {
       // A stream without a step gets no queries: nothing tells it when they have
@@ -164,12 +171,17 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     if (ntm > 0 && valid < 128 && !dead) {
       const int u = (issued - 1) % C::NU;
       tc_wait(tail, 0, dead);
-      zero_rows<D>(sm + C::RING + u * C::UNIT, valid, lane);
-      if (lane == 0) mbar_arrive(&full[u]);
+      dead = __any_sync(kFull, dead);
+      if (!dead) {
+        zero_rows<D>(sm + C::RING + u * C::UNIT, valid, lane);
+        if (lane == 0) mbar_arrive(&full[u]);
+      }
     }
-    // every copy has landed before the CTA leaves
+    // Every copy has landed before the CTA leaves. Once a wait ran out the copies
+    // on their way get one more limit between them.
     if (lane == 0) {
       bool late = false;
+      if (ntm > 0) tc_wait(qfull, 0, late);
       for (int k = max(0, issued - C::NU); k < issued; ++k)
         tc_wait(&full[k % C::NU], (uint32_t)((k / C::NU) & 1), late);
       dead |= late;
@@ -237,8 +249,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       }
       if (__any_sync(kFull, dead)) {  // products in flight end before their memory is given back
         bool late = false;
-        mma16_commit(el, qfull);
-        tc_wait(qfull, 1, late);
+        mma16_commit(el, drained);
+        tc_wait(drained, 0, late);
       }
     }
     __syncwarp();
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     const float c = p.c;
     const int n_steps = nt[s];
     for (int j = 0; j < n_steps; ++j) {
-      tc_wait(&sfull[s], (uint32_t)(j & 1), dead);
+      tc_wait(&sfull[s], (uint32_t)(j & 1), dead, gave_up);
       dead = __any_sync(kFull, dead);
       tc_fence_after();
       const uint32_t ts = tb + lane_at + s * 128;
@@ -295,7 +307,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
             un2(l2[i], a, b);
             l2[i] = f2(a * f, b * f);
           }
-          tc_wait(&odone[s], (uint32_t)((j - 1) & 1), dead);
+          tc_wait(&odone[s], (uint32_t)((j - 1) & 1), dead, gave_up);
           dead = __any_sync(kFull, dead);
           tc_fence_after();
           const uint32_t to_o = tb + lane_at + C::O0 + s * D;
@@ -347,8 +359,8 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
     const size_t orow = (size_t)(tl.q0 + tok0 + rr / p.G) * p.HQ + h * p.G + rr % p.G;
     bool bad = false;
     if (n_steps > 0) {
-      tc_wait(&odone[s], (uint32_t)((n_steps - 1) & 1), dead);
-      dead = __any_sync(kFull, dead);
+      tc_wait(&odone[s], (uint32_t)((n_steps - 1) & 1), dead, gave_up);
+      dead = __any_sync(kFull, dead || *gave_up != 0);
       tc_fence_after();
     }
     const bool mine = row < R && !dead;

@@ -95,15 +95,26 @@ __device__ __noinline__ void again(const PromptParams& p, const PromptTile& tl, 
 // A wait that gives up after the usual limit; after the first that did, none
 // of the thread's later waits waits. The hardware parks the warp meanwhile: a
 // warp that polls takes issue slots from the softmax warp beside it.
-__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& dead) {
+// `told` (may be null) becomes non-zero when it gives up.
+__device__ __forceinline__ void tc_wait(uint64_t* bar, uint32_t parity, bool& dead,
+                                        volatile uint32_t* told = nullptr) {
   if (dead || mbar_try_wait(bar, parity)) return;
   const unsigned long long t0 = global_ns();
   while (!mbar_try_wait_hint(bar, parity, 20000)) {
     if (global_ns() - t0 > kWaitLimitNs) {
       dead = true;
+      if (told != nullptr) *told = 1;
       return;
     }
   }
+}
+
+// Test hook: the first copy into place `unit` of the ring, or of the queries
+// (the place behind it), is promised more than it brings.
+template <int NU>
+__device__ __forceinline__ void promise_more(uint64_t* full, uint64_t* qfull, int unit) {
+  const int place = unit % (NU + 1);
+  mbar_promise(place < NU ? full + place : qfull, 16);
 }
 
 inline bool encode(CUtensorMap* map, int dt, int rank, const void* base, const cuuint64_t* dims,

@@ -385,6 +385,8 @@ rssm_status rssm_attn_prefill(rssm_kv_handle* h, const void* q, const void* k, c
   p.D = c.D;
   p.n_slots = c.n_slots;
   p.dt = c.dtype;
+  p.hook_cta = h->hook_cta;
+  p.hook_unit = h->hook_unit;
   p.c = (float)((double)c.scale * 1.4426950408889634);
   return from_cuda(attn_prompt_launch(p, static_cast<cudaStream_t>(stream)));
 }

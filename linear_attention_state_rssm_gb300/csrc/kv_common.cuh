@@ -138,6 +138,7 @@ struct PromptParams {
   uint32_t* err;
   long long qs, ks, vs;
   int B, N, M, HQ, HKV, G, D, n_slots, dt;
+  int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   float c;
 };
 

@@ -140,6 +140,41 @@ def test_decode_wait_that_runs_out_in_a_split_row(dtype, D, HQ, HKV, T, cta, uni
     assert c.rssm_kv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,D,HQ,HKV", [("bf16", 64, 4, 4), ("f16", 64, 6, 2),
+                                            ("bf16", 128, 4, 4), ("f16", 128, 40, 2)])
+@pytest.mark.parametrize("unit", [0, 1, 2, "queries"])
+def test_prompt_wait_that_runs_out_leaves_rows_alone(dtype, D, HQ, HKV, unit):
+    """One CTA's keys, values or queries are promised more than they bring: each row and head
+    is either complete or as it was, and the next call is right."""
+    late_prompt(dtype, D, HQ, HKV, unit, {64: 8, 128: 5}[D])
+
+
+def late_prompt(dtype, D, HQ, HKV, unit, places):
+    cu = ints([0, 400, 430, 900])
+    q, k, v = (draw(rng_of(65, D), (900, h, D), dtype)[0] for h in (HQ, HKV, HKV))
+    c = cache(n_slots=3, HQ=HQ, HKV=HKV, D=D, page_size=16, dtype=dtype)
+
+    def prompt():
+        o = torch.full_like(q, SENTINEL)
+        lse = torch.full((900, HQ), SENTINEL, device="cuda")
+        timed(lambda: c.rssm_attn_prefill(q, k, v, cu, None, o, lse=lse))
+        return o, lse[..., None]
+
+    clean = prompt()
+    assert c.rssm_kv_get_device_error() == 0
+    c.rssm_kv_debug_withhold(0, places if unit == "queries" else unit)
+    late = prompt()
+    assert c.rssm_kv_get_device_error() == DEVERR["timeout"]
+    c.rssm_kv_debug_withhold(-1)
+    kept = [(got == SENTINEL).all(-1) for got in late]
+    assert kept[0].any() and not kept[0].all() and torch.equal(kept[0], kept[1])
+    for got, want, left in zip(late, clean, kept):
+        assert torch.equal((got == want).all(-1), ~left)
+    for got, want in zip(prompt(), clean):
+        assert torch.equal(got, want)
+    assert c.rssm_kv_get_device_error() == 0
+
+
 def test_arguments_of_the_waits_hook_are_checked():
     from linear_attention_state_rssm_gb300 import RssmError
     c = cache(n_slots=1, HQ=1, HKV=1, D=64, page_size=16)
