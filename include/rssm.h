@@ -615,8 +615,8 @@ rssm_status rssm_kv_get_device_error(rssm_kv_handle *h, uint32_t *out,
 /*
  * Test and debugging hook of the bounded waits, as rssm_debug_withhold. CTA
  * `cta` of a launch copies keys and values by turns into the places of a ring;
- * in later launches of rssm_attn_decode and, for heads of 64 and 128 in 16-bit
- * types, rssm_attn_prefill, the first copy into place `unit` (modulo their
+ * in later launches of rssm_attn_decode and, for 16-bit types,
+ * rssm_attn_prefill, the first copy into place `unit` (modulo their
  * number; prompts have one more for the queries) is promised 16 bytes more than
  * it brings. So every wait on it runs out after the usual 0.5 s; the copies
  * themselves all land. cta -1: off, as after rssm_kv_alloc. Host state only.

@@ -92,10 +92,12 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
   uint64_t* tempty = tfull + 2;                                // [2] every role has it
   uint64_t* sent = tempty + 2;                                 // a tile's loads are all on their way
   uint64_t* answered = sent + 1;                               // a CTA was asked for
+  uint64_t* drained = answered + 1;                            // no product is in flight
   uint4* answer = reinterpret_cast<uint4*>(sm + C::BARS + 272);
   TcTile* tiles = reinterpret_cast<TcTile*>(sm + C::BARS + 288);  // [2]
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + C::BARS + 288 + 2 * sizeof(TcTile));
-  static_assert((2 * C::NU + 17) * 8 <= 272 && 288 + 2 * sizeof(TcTile) + 4 <= 512, "barriers");
+  volatile uint32_t* gave_up = tslot + 1;  // as in attn_prompt_tc.cu
+  static_assert((2 * C::NU + 18) * 8 <= 272 && 288 + 2 * sizeof(TcTile) + 8 <= 512, "barriers");
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int toks = 128 / p.G;  // tokens of a stream
   constexpr int W0 = 4;  // first of the warps with roles
@@ -117,6 +119,9 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
     mbar_init(odone, 1);
     mbar_init(sent, 1);
     mbar_init(answered, 1);
+    mbar_init(drained, 1);
+    *gave_up = 0;
+    if (p.hook_cta == (int)blockIdx.x) promise_more<C::NU>(full, qfull, p.hook_unit);
     fence_mbar_init();
   }
   if (warp == W0 + 1) tmem_alloc512(tslot);
@@ -289,8 +294,8 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
     }
     if (dead) {  // products in flight end before their memory is given back
       bool late = false;
-      mma16_commit(el, answered);
-      tc_wait(answered, 0, late);
+      mma16_commit(el, drained);
+      tc_wait(drained, 0, late);
     }
     __syncwarp();
   } else if (warp == W0 + 2) {
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
       for (int j = 0; j < n_steps; ++j) {
         const uint32_t at = done + (uint32_t)j;
         const int buf = at & 1;
-        tc_wait(&sfull[buf], (at >> 1) & 1, dead);
+        tc_wait(&sfull[buf], (at >> 1) & 1, dead, gave_up);
         dead = __any_sync(kFull, dead);
         tc_fence_after();
         const uint32_t ts = tb + lane_at + buf * 128;
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
               un2(l2[i], a, b);
               l2[i] = f2(a * f, b * f);
             }
-            tc_wait(odone, (at - 1) & 1, dead);
+            tc_wait(odone, (at - 1) & 1, dead, gave_up);
             dead = __any_sync(kFull, dead);
             tc_fence_after();
             const uint32_t to_o = tb + lane_at + C::O0;
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
             // A parity tells a phase only from its neighbours, so every phase
             // of odone is seen before the next can end: the scores of step j
             // do not wait for P V of step j - 1.
-            if (q == 1 && j > 0) tc_wait(odone, (at - 1) & 1, dead);
+            if (q == 1 && j > 0) tc_wait(odone, (at - 1) & 1, dead, gave_up);
             tc_fence_before();
             mbar_arrive(&pfull[2 * buf + (q >> 1)]);
           }
@@ -440,8 +445,8 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
       const size_t orow = (size_t)(tl.q0 + tok0 + rr / p.G) * p.HQ + tt.h * p.G + rr % p.G;
       bool bad = false;
       if (n_steps > 0) {
-        tc_wait(odone, (done - 1) & 1, dead);
-        dead = __any_sync(kFull, dead);
+        tc_wait(odone, (done - 1) & 1, dead, gave_up);
+        dead = __any_sync(kFull, dead || *gave_up != 0);
         tc_fence_after();
       }
       T* to[4];  // the lane's sixteen bytes in the rows of its four lanes

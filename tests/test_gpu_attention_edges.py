@@ -141,12 +141,13 @@ def test_decode_wait_that_runs_out_in_a_split_row(dtype, D, HQ, HKV, T, cta, uni
 
 
 @pytest.mark.parametrize("dtype,D,HQ,HKV", [("bf16", 64, 4, 4), ("f16", 64, 6, 2),
-                                            ("bf16", 128, 4, 4), ("f16", 128, 40, 2)])
+                                            ("bf16", 128, 4, 4), ("f16", 128, 40, 2),
+                                            ("bf16", 256, 4, 4), ("f16", 256, 96, 32)])
 @pytest.mark.parametrize("unit", [0, 1, 2, "queries"])
 def test_prompt_wait_that_runs_out_leaves_rows_alone(dtype, D, HQ, HKV, unit):
     """One CTA's keys, values or queries are promised more than they bring: each row and head
     is either complete or as it was, and the next call is right."""
-    late_prompt(dtype, D, HQ, HKV, unit, {64: 8, 128: 5}[D])
+    late_prompt(dtype, D, HQ, HKV, unit, {64: 8, 128: 5, 256: 5}[D])
 
 
 def late_prompt(dtype, D, HQ, HKV, unit, places):
