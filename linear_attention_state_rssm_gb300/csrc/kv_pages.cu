@@ -19,6 +19,9 @@ namespace rssm {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+// Where the sum of a call's needs stops: more pages than any pool has (2^28), and
+// with a block's rows behind it (1024 of at most 2^20 pages) still below 2^31.
+constexpr int kPlenty = 1 << 29;
 
 // Sum of one value per thread over the CTA before this thread (exclusive),
 // and the total.
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_reserve_kernel(const PagePa
     int n;
     const int at = total + cta_scan(need, sums, tid, n);
     if (r < p.B) p.rows[r] = at;
-    total = min(total + n, 1 << 30);
+    total = min(total + n, kPlenty);
   }
   if (tid == 0) p.rows[p.B] = total;
   __syncthreads();
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_fork_kernel(const PageParam
     int n;
     const int at = total + cta_scan(f.need, sums, tid, n);
     if (b + tid < p.B) p.rows[b + tid] = at;
-    total = min(total + n, 1 << 30);
+    total = min(total + n, kPlenty);
   }
   if (tid == 0) p.rows[p.B] = total;
   __syncthreads();

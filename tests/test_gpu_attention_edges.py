@@ -183,3 +183,29 @@ def test_arguments_of_the_waits_hook_are_checked():
         with pytest.raises(RssmError):
             c.rssm_kv_debug_withhold(*bad)
     c.rssm_kv_debug_withhold(-1)
+
+
+# --------------------------------------------------------- sums of page plans
+def test_page_plans_whose_needs_are_past_two_to_the_thirty():
+    """2048 rows that want 2^20 pages each, of a pool with five free ones: every row is
+    refused and nothing else changes."""
+    n, pages = 2048, 1 << 20
+    c = cache(n_slots=n + 1, HQ=1, HKV=1, D=64, n_pages=pages + 5, page_size=16,
+              max_pages=pages, dtype="f16")
+    c.table[0] = torch.arange(pages, dtype=torch.int32, device="cuda")
+    c.refs[:pages] = 1
+    c.held[0], c.length[0] = pages, 16 * pages
+    refs = c.refs.clone()
+    rest = ints(range(1, n + 1))
+    c.rssm_kv_fork(torch.zeros_like(rest), rest, deep=True)
+    assert c.rssm_kv_get_device_error() == DEVERR["pages"]
+    assert torch.equal(c.refs, refs) and not c.held[1:].any() and not c.length[1:].any()
+    c.length[1:] = 16 * pages - 1
+    c.rssm_kv_reserve(rest, 1)
+    assert c.rssm_kv_get_device_error() == DEVERR["pages"]
+    assert torch.equal(c.refs, refs) and not c.held[1:].any()
+    assert (c.table[1:] == -1).all()
+    c.length[1:] = 0
+    c.rssm_kv_reserve(rest[:6], 1)                  # five rows get the five pages
+    assert c.rssm_kv_get_device_error() == DEVERR["pages"]
+    assert c.held[1:].tolist() == [1] * 5 + [0] * (n - 5)
