@@ -563,7 +563,8 @@ typedef struct rssm_rope {
  * that is contiguous. Two rows may
  * not write the same slot. A token past its slot's pages sets
  * RSSM_DEVERR_PAGES, one with a position outside [0, max_pos)
- * RSSM_DEVERR_POSITION: that token is skipped.
+ * RSSM_DEVERR_POSITION: that token is skipped. Offsets that decrease or leave
+ * [0, N] set RSSM_DEVERR_SEQLEN and skip the row.
  */
 rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
                            const void *k, const void *v, int64_t q_stride,

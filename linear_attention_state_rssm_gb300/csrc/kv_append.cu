@@ -70,8 +70,10 @@ __device__ __forceinline__ TokenPlace place_of(const AppendParams& p, int tok, i
       if (p.cu[mid] <= tok) lo = mid; else hi = mid;
     }
     r = lo;
-    i = tok - p.cu[r];
-    if (i < 0 || tok >= p.cu[r + 1]) return t;  // outside every window
+    const int first = p.cu[r], end = p.cu[r + 1];
+    // outside every window, or in one that is refused
+    if (first < 0 || tok < first || tok >= end || end > p.N) return t;
+    i = tok - first;
   }
   const int s = p.slot[r];
   if (s < 0) return t;

@@ -209,3 +209,24 @@ def test_page_plans_whose_needs_are_past_two_to_the_thirty():
     c.rssm_kv_reserve(rest[:6], 1)                  # five rows get the five pages
     assert c.rssm_kv_get_device_error() == DEVERR["pages"]
     assert c.held[1:].tolist() == [1] * 5 + [0] * (n - 5)
+
+
+# --------------------------------------------------- rows with refused offsets
+@pytest.mark.parametrize("cu,live", [([0, 4, 9], [0]), ([-2, 4, 6], [1]), ([0, 4, 2], [0])])
+def test_append_skips_rows_whose_offsets_are_refused(cu, live):
+    c, _ = filled(rng_of(71), [0, 0], 16, 2, 1, 64, "f32", 16)
+    q, k, v = (draw(rng_of(72), (6, h, 64), "f32")[0] for h in (2, 1, 1))
+    out, kout = torch.full_like(q, SENTINEL), torch.full_like(k, SENTINEL)
+    pages = [int(c.table[s, 0]) for s in range(2)]
+    before = c.k_pages.clone()
+    c.rssm_kv_append(0, q, k, v, ints([0, 1]), q_out=out, cu_seqlens=ints(cu), k_out=kout)
+    assert c.rssm_kv_get_device_error() == DEVERR["seqlen"]
+    for r in range(2):
+        a, b = max(cu[r], 0), min(cu[r + 1], 6)
+        if r in live:
+            assert torch.equal(out[a:b], q[a:b]) and torch.equal(kout[a:b], k[a:b])
+            assert torch.equal(c.k_pages[0, pages[r], 0, :b - a], k[a:b, 0])
+        else:
+            assert torch.equal(c.k_pages[0, pages[r]].isnan(), before[0, pages[r]].isnan())
+            if b > a:
+                assert (out[a:b] == SENTINEL).all() and (kout[a:b] == SENTINEL).all()
