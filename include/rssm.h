@@ -598,7 +598,9 @@ rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
  * keys of earlier chunks come before the chunk's own; a query that sees none
  * (Lk < Lq) gives o = 0 and lse = -inf. The cache is not read. slot (may be
  * null) skips rows with a null slot. Offsets that decrease or leave [0, N] or
- * [0, M] set RSSM_DEVERR_SEQLEN and skip the sequence. Where a wait runs out
+ * [0, M] set RSSM_DEVERR_SEQLEN and skip the sequence. Sequences must not share
+ * query tokens: where later offsets go back, outputs are undefined, and
+ * RSSM_DEVERR_SEQLEN says so if some were not computed. Where a wait runs out
  * (RSSM_DEVERR_TIMEOUT) some of the outputs are left as they are; what is
  * stored is right.
  */

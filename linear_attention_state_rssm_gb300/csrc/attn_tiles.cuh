@@ -72,6 +72,9 @@ __device__ __forceinline__ bool find_tile(const PromptParams& p, int rows, int i
     }
     before += __shfl_sync(kFull, incl, 31);
   }
+  // the launch has room for every tile unless sequences share query tokens
+  if (tell && index == 0 && lane == 0 && before > (int)(gridDim.x / (unsigned)p.HKV))
+    atomicOr(p.err, DEVERR_SEQLEN);
   return found;
 }
 

@@ -230,3 +230,16 @@ def test_append_skips_rows_whose_offsets_are_refused(cu, live):
             assert torch.equal(c.k_pages[0, pages[r]].isnan(), before[0, pages[r]].isnan())
             if b > a:
                 assert (out[a:b] == SENTINEL).all() and (kout[a:b] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f16", 128), ("bf16", 256), ("f32", 64)])
+def test_prompt_reports_tiles_that_it_has_no_room_for(dtype, D):
+    """Offsets that go back at a null row, so that two sequences share tokens: more tiles than
+    N tokens in order can make are not dropped silently."""
+    q, k, v = (draw(rng_of(73), (1300, h, D), dtype)[0] for h in (1, 1, 1))
+    c = cache(n_slots=4, HQ=1, HKV=1, D=D, page_size=16, dtype=dtype)
+    o = torch.empty_like(q)
+    c.rssm_attn_prefill(q, k, v, ints([0, 1000, 1, 1000, 1300]), ints([0, -1, 2, 3]), o)
+    assert c.rssm_kv_get_device_error() == DEVERR["seqlen"]
+    c.rssm_attn_prefill(q, k, v, ints([0, 1000, 1000, 1000, 1300]), ints([0, -1, 2, 3]), o)
+    assert c.rssm_kv_get_device_error() == 0
