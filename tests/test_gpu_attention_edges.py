@@ -1,13 +1,16 @@
 """The full-attention layers' operators where their parts meet: streams of a tile
 without work, waits that run out, sums of page plans near their limits, rows
-with refused offsets. Tolerances are those of test_gpu_attention.py."""
+with refused offsets. Tolerances are those of test_gpu_attention.py unless a
+test derives its own."""
 import time
 
+import numpy as np
 import pytest
 import torch
 
 from linear_attention_state_rssm_gb300._lib import DEVERR
-from test_gpu_attention import SENTINEL, cache, draw, filled, ints, rng_of, run_prompt
+from oracle import attention as ref
+from test_gpu_attention import REL, SENTINEL, cache, draw, filled, ints, rng_of, run_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +246,73 @@ def test_prompt_reports_tiles_that_it_has_no_room_for(dtype, D):
     assert c.rssm_kv_get_device_error() == DEVERR["seqlen"]
     c.rssm_attn_prefill(q, k, v, ints([0, 1000, 1000, 1000, 1300]), ints([0, -1, 2, 3]), o)
     assert c.rssm_kv_get_device_error() == 0
+
+
+# ------------------------------------------------------------ closer tolerances
+def test_decode_leaves_every_arrival_counter_at_zero():
+    """Three CTAs per SM (16-bit heads of 64) and rows that all of them share."""
+    c, _ = filled(rng_of(81), [4000] * 24, 1, 4, 4, 64, "bf16", 64)
+    q = draw(rng_of(82), (24, 4, 64), "bf16")[0]
+    o, first = torch.empty_like(q), None
+    for _ in range(3):
+        c.rssm_attn_decode(1, q, ints(range(24)), 1, o)
+        assert (c.work[:4 * 456] == 0).all()
+        first = o.clone() if first is None else first
+        assert torch.equal(o, first)
+    assert c.rssm_kv_get_device_error() == 0
+
+
+# fp32 sums of D products in a row: partial sums of size 1.7 sqrt(k) round by 2^-24 of
+# themselves each, about 1.1e-5 (D = 256) of standard deviation, times scale 1/16 = 7e-7;
+# six of those, and the rounding of x c (2^-24 of at most 15), leave the exponent within
+# 5e-6. Weights and their sum are off by that each: 1e-5 of the mass, and the sum over the
+# keys and the base-2 exponential (2 ulp) add 2e-6.
+CLOSE32 = 1.2e-5
+
+
+def close32(got, want, mass):
+    off = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(off <= CLOSE32 * mass + 1e-8), (off / mass).max()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_fp32_attention_keeps_fp32_accuracy(D):
+    rng = rng_of(83, D)
+    lq, lk = [300, 1, 77], [900, 700, 77]
+    cu, cuk = np.cumsum([0] + lq), np.cumsum([0] + lk)
+    (q, qd), (k, kd), (v, vd) = (draw(rng, (n, h, D), "f32", 1.3)
+                                 for n, h in ((cu[-1], 4), (cuk[-1], 2), (cuk[-1], 2)))
+    c = cache(n_slots=3, HQ=4, HKV=2, D=D, page_size=16, dtype="f32")
+    o = torch.empty_like(q)
+    c.rssm_attn_prefill(q, k, v, ints(cu), None, o, cu_keys=ints(cuk))
+    want, _, mass = ref.prompt(qd, kd, vd, cu, cuk, c.scale)
+    close32(o, want, mass)
+    lens, T = [0, 1500, 4001, 63], 3
+    c, tokens = filled(rng, lens, T, 4, 2, D, "f32", 32)
+    q, qd = draw(rng, (4 * T, 4, D), "f32", 1.2)
+    o = torch.empty_like(q)
+    c.rssm_attn_decode(1, q, ints(range(4)), T, o)
+    want, _, mass = ref.window(qd, tokens, lens, T, c.scale)
+    close32(o, want, mass)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_prompt_rows_before_a_poisoned_token(dtype, D, bad):
+    """Token 600 of 700 and its neighbours' ends are poisoned. Rows of tiles that end before
+    its keys are bitwise what they are without; the rows right before it, computed again,
+    are within their own mass of rounding."""
+    rng = rng_of(84, D)
+    (q, qd), (k, kd), (v, vd) = (draw(rng, (740, h, D), dtype) for h in (2, 1, 1))
+    cu = [0, 700, 740]
+    c = cache(n_slots=2, HQ=2, HKV=1, D=D, page_size=16, dtype=dtype)
+    want, _, mass = ref.prompt(qd, kd, vd, cu, cu, c.scale)
+    clean, dirty = torch.empty_like(q), torch.empty_like(q)
+    c.rssm_attn_prefill(q, k, v, ints(cu), None, clean)
+    k[600], v[600] = bad, bad
+    c.rssm_attn_prefill(q, k, v, ints(cu), None, dirty)
+    assert torch.equal(dirty[:512], clean[:512]) and torch.equal(dirty[700:], clean[700:])
+    off = np.abs(dirty[512:600].double().cpu().numpy() - want[512:600])
+    assert np.all(off <= REL[dtype] * mass[512:600] + 1e-7)
+    assert not torch.isfinite(dirty[600:700].float()).any()
