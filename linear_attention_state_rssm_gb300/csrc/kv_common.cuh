@@ -15,9 +15,10 @@ enum : uint32_t {
 
 constexpr int kMaxSms = 152;        // SMs that a decode launch uses at most
 constexpr int kMaxParts = 3 * kMaxSms;  // its CTAs: parts a row can be cut into
-// fp32 values of two parts per CTA: outputs, running maxima and sums of up to
-// 64 rows (two CTAs per SM for D = 256, three for smaller heads)
-constexpr size_t kPartFloats = (size_t)2 * 2 * kMaxSms * 64 * (256 + 4);
+// fp32 values of two parts per CTA: outputs, running maxima and sums. Heads of
+// 128 have the most: two CTAs per SM and 64 rows (D = 256: one CTA and 48 rows;
+// D = 64: three CTAs). 20 MB, whatever the cache's D.
+constexpr size_t kPartFloats = (size_t)2 * 2 * kMaxSms * 64 * (128 + 2);
 constexpr int kMaxRopeAxes = 3;
 
 // Regions of the caller's work buffer (bytes); `count` is zero between calls.
