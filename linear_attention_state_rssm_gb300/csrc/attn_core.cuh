@@ -6,12 +6,13 @@
 //     m'   = max(m, max_j x_ij);  a = 2^(m - m');  p_ij = 2^(x_ij - m')
 //     l    = a l + sum_j p_ij;    o = a o + sum_j p_ij v_j;     output o / l
 //
-// Products run on the warp-level tensor cores: m16n8k16 for 16-bit types,
-// m16n8k8 tf32 with operands split in head and tail for fp32 (fp32 accuracy). The fragments of x are those of p's operand: a row's values never
-// leave the registers of its four lanes. l adds the weights in fp32 as they
-// are; their product with v takes them rounded to the input type, because that
-// is what the tensor cores read (relative error 2^-9 for bf16, independent from
-// weight to weight, below the rounding of the output).
+// Products of 16-bit types run on the warp-level tensor cores (m16n8k16), those
+// of fp32 on the FMA units. The fragments of x are those of p's operand: a row's
+// values never leave the registers of its four lanes. l adds the weights in fp32
+// as they are; their product with v takes them rounded to the input type,
+// because that is what the tensor cores read (relative error 2^-8 at most for
+// bf16 and 2^-11 for fp16, independent from weight to weight, as the rounding of
+// the output); fp32 rounds nothing.
 //
 // Blocks in shared memory are cut in columns of 128 bytes: row r of a column is
 // 128 bytes after row r - 1, and within it 16-byte unit u lies at unit

@@ -12,7 +12,8 @@
 // copies one tile ahead, and are joined at the end: the FMA units want many
 // warps, and a prompt of a thousand tokens has few rows. (64 rows and one group
 // of four warps: 104 us where this takes 51 us, five prompts of 302 to 957 keys.)
-// Tiles of longer sight come first in the grid. Longer prompts (eight, the longest
+// A sequence's tiles of longer sight come first in the grid, sequences as given.
+// Longer prompts (eight, the longest
 // of 2048 tokens: 299 us) issue on 63% of cycles with shared memory 61% busy, no unit
 // full: 12 warps per SM wait out shared loads and reductions (168 registers and
 // 203 KB leave no room for more).

@@ -15,13 +15,13 @@
 // warpgroup per stream does the softmax, one thread per row, so that row sums
 // need no exchange, and tensor memory finds the maxima on the way out. The two
 // streams take turns on the tensor cores: while one's weights are computed the
-// other's products run. Weights are handed over in halves of a step. Tiles of
-// longer sight come first in the grid.
+// other's products run. Weights are handed over in halves of a step. A
+// sequence's tiles of longer sight come first in the grid, sequences as given.
 //
-// The maximum that the weights are relative to is only moved when a row's true
-// maximum is more than 2^8 above it (weights stay below 2^8, exact in range for
-// both types); moving it costs a pass over O in tensor memory and is rare
-// after the first steps.
+// The softmax does not depend on what its weights are relative to, as long as
+// they stay in range. So that reference is only moved when a row's true maximum
+// would get a weight above 2^8 (well within both types); moving it costs a pass
+// over O in tensor memory and is rare after the first steps.
 //
 // Products with masked keys are 0 * v, which is not 0 where v is infinite or
 // NaN. Values behind the sequence's last key are zeroed in shared memory; a row
