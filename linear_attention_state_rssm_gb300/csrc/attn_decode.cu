@@ -22,9 +22,9 @@
 // only where a row ends, while the ring fills with the next row's chunks.
 //
 // Measured (GB300, back to back): 56 rows of 1 to 8 k tokens, 16/4 heads of 256:
-// 131 us, 6.3 TB/s (93% of the copy rate); two rows of 109 to 131 k tokens, 32/8
-// heads of 128, fp16: 159 us, 6.2 TB/s; 125 windows of 8 tokens over 0.3 to 3 k
-// tokens, 16/4 heads of 128: 68 us, 4.3 TB/s, held back by the ends of its 2.5
+// 133 us, 6.2 TB/s (92% of the copy rate); two rows of 109 to 131 k tokens, 32/8
+// heads of 128, fp16: 157 us, 6.3 TB/s; 125 windows of 8 tokens over 0.3 to 3 k
+// tokens, 16/4 heads of 128: 67 us, 4.4 TB/s, held back by the ends of its 2.5
 // stretches a CTA (11 k cycles each, of 128 k) and by steps of two warps to a
 // stream. Steps: private rings of cp.async per warp and whole CTAs to a row 142,
 // 160, 113 us; the gap on the line 93 for the windows; this ring 86; rows of a

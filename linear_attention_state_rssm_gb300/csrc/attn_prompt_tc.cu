@@ -29,12 +29,12 @@
 // selection where a value it must not see is to blame (attn_prompt_tc.cuh).
 //
 // What bounds it: for heads of 128 the tensor cores, which the two streams keep
-// 80% busy. 14336 tokens, 16/4 heads of 128: 454 us by itself, 1.85 PFLOP/s of
-// causal products (97% of the library's matrix product, burst); 490 to 510 us
-// back to back, 1.65 to 1.72 (96 to 100% of its sustained rate). Heads of 64: 387
-// us; tensor cores and exponentials are each 46% busy, so neither binds: a
-// stream's round of scores, maximum, weights and products does. What it took, back to back:
-// issue by a converged warp 655 -> 531 us, coalesced output and earlier first
+// 80% busy. 14336 tokens, 16/4 heads of 128: 454 to 463 us by itself, 1.82 to
+// 1.85 PFLOP/s of causal products (95 to 97% of the library's matrix product,
+// burst); 495 to 512 us back to back, 1.64 to 1.70 (96 to 99% of its sustained
+// rate). Heads of 64: 387 us; tensor cores and exponentials are each 46% busy, so
+// neither binds: a stream's round of scores, maximum, weights and products does.
+// What it took, back to back: issue by a converged warp 655 -> 531 us, coalesced output and earlier first
 // loads 523, maxima by tensor memory 502. Staying on the SM for further tiles, as
 // the wide form does, lost 2% here (and 13% of short ragged prompts, gaining 4% of
 // long ones): what the longer-lived state costs every step is more than a tile's
