@@ -316,3 +316,82 @@ def test_prompt_rows_before_a_poisoned_token(dtype, D, bad):
     off = np.abs(dirty[512:600].double().cpu().numpy() - want[512:600])
     assert np.all(off <= REL[dtype] * mass[512:600] + 1e-7)
     assert not torch.isfinite(dirty[600:700].float()).any()
+
+
+# --------------------------------------------------- large pools, other streams
+def test_pages_past_32_bit_offsets():
+    """Pools of 13 G values (26 GB) each: append, decode, fork and compaction at their far end
+    give what a small pool gives."""
+    HQ, HKV, D, page, T, n = 8, 4, 128, 64, 3, 200
+    pages = 400_000
+    lens = [n, 64]
+    results = []
+    for total, ids in ((16, [5, 9, 7, 2, 11, 12]),
+                       (pages, [pages - 1, pages - 9, pages - 2, 131072, pages - 3, pages - 5])):
+        rng = rng_of(91)
+        c = cache(n_layers=1, n_slots=3, HQ=HQ, HKV=HKV, D=D, n_pages=total, page_size=page,
+                  max_pages=8, dtype="bf16")
+        c.table[0, :4], c.table[1, :2] = ints(ids[:4]), ints(ids[4:])
+        c.held[:2], c.refs[ids] = ints([4, 2]), 1
+        cu = ints([0, n, n + 64])
+        k, v = (draw(rng, (n + 64, HKV, D), "bf16")[0] for _ in range(2))
+        c.rssm_kv_append(0, None, k, v, ints([0, 1]), cu_seqlens=cu)
+        c.rssm_kv_commit(ints([0, 1]), cu_seqlens=cu)
+        out = []
+
+        def decode(slot):
+            B = slot.numel()
+            q, k, v = (draw(rng, (B * T, h, D), "bf16")[0] for h in (HQ, HKV, HKV))
+            c.rssm_kv_reserve(slot, T)
+            c.rssm_kv_append(0, None, k, v, slot, T)
+            o = torch.empty_like(q)
+            c.rssm_attn_decode(0, q, slot, T, o)
+            out.append(o)
+
+        decode(ints([0, 1]))
+        c.rssm_kv_fork(ints([0]), ints([2]), deep=True)
+        decode(ints([2, 0]))
+        c.rssm_kv_compact()
+        decode(ints([1, 2, 0]))
+        assert c.rssm_kv_get_device_error() == 0
+        assert sorted(c.refs.nonzero().flatten().tolist()) == list(range(int((c.refs > 0).sum())))
+        results.append(out)
+        del c
+        torch.cuda.empty_cache()
+    for got, want in zip(*results):
+        assert torch.equal(got, want)
+
+
+def test_page_calls_in_a_graph_on_another_stream():
+    from linear_attention_state_rssm_gb300.store import KVCache
+    a, b = (KVCache(2, 6, 2, 1, 64, n_pages=40, page_size=16, max_pages=8, dtype="f32")
+            for _ in range(2))
+    for c in (a, b):
+        c.k_pages.copy_(torch.arange(c.k_pages.numel(), device="cuda").view_as(c.k_pages))
+        c.v_pages.copy_(c.k_pages).neg_()
+    slots, n = ints([0, 1, 2]), ints([40, 3, 100])
+    src, dst, gone = ints([0, 2]), ints([3, 4]), ints([1, 2])
+
+    def calls(c):
+        c.rssm_kv_reserve(slots, 110)
+        c.rssm_kv_commit(slots, 110, accept_len=n)
+        c.rssm_kv_fork(src, dst)
+        c.rssm_kv_release(gone)
+        c.rssm_kv_compact()
+        c.rssm_kv_fork(dst, ints_5, deep=True)
+        c.rssm_kv_release(slots)
+        c.rssm_kv_compact()
+
+    ints_5 = ints([5, 1])
+    calls(a)
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        calls(b)
+    with torch.cuda.stream(st):
+        graph.replay()
+    st.synchronize()
+    for name in ("table", "held", "length", "refs", "k_pages", "v_pages"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+    assert a.rssm_kv_get_device_error() == b.rssm_kv_get_device_error() == 0
+    assert a.held.tolist()[3:] == [3, 7, 3]
