@@ -534,6 +534,27 @@ rssm_status rssm_kv_release(rssm_kv_handle *h, const int32_t *slot, int32_t B,
  */
 rssm_status rssm_kv_compact(rssm_kv_handle *h, void *stream);
 
+/*
+ * A cache whose pages are quantised as they are written. k_pages and v_pages
+ * hold e4m3 values (one byte, the layout as above), and each token of each head
+ * has a power of two for its keys and one for its values,
+ *     scales : [n_layers][n_pages][HKV][page_size][2] bytes (keys', values'),
+ * e + 127 for 2^e: with a = max |x_i| over the finite x_i of the head, e is the
+ * least whole number with a <= 448 2^e, kept within [-64, 63]. The page holds
+ * e4m3(x_i 2^-e), rounded to nearest even; infinities and NaN are held as NaN,
+ * values past 448 2^63 saturate. dtype (BF16 or F16; F32 is
+ * RSSM_ERR_UNSUPPORTED) is that of inputs and outputs: keys are rounded once,
+ * from fp32, after norm and rotation. Every call on the handle works on such a
+ * cache: rssm_kv_append quantises, rssm_attn_decode and rssm_kv_gather read it
+ * back, pages are copied with their scales. scales is 16-byte aligned, set to 0
+ * by the caller before the first call, and borrowed as the other buffers are.
+ */
+rssm_status rssm_kv_quant_required_bytes(const rssm_kv_config *cfg,
+                                         rssm_kv_sizes *out, size_t *scales);
+rssm_status rssm_kv_quant_alloc(const rssm_kv_config *cfg,
+                                const rssm_kv_buffers *buf, void *scales,
+                                rssm_kv_handle **out);
+
 /* Rotary positions: pair i < pairs of a head turns dimensions i and i + pairs
  * by the angle position * frequency_i, read from `table`, device
  * fp32[max_pos][2][pairs] (cosines, then sines), 16-byte aligned. Positions have `axes` axes
@@ -573,6 +594,50 @@ rssm_status rssm_kv_append(rssm_kv_handle *h, int32_t layer, const void *q,
                            const int32_t *cu_seqlens, const int32_t *slot,
                            int32_t B, int32_t T, int32_t N, void *q_out,
                            void *k_out, void *stream);
+
+/* Norms of queries and keys, head by head: y_i = x_i w_i / sqrt(mean_i x_i^2 +
+ * eps), i < D, in fp32 and before the rotation. q_weight, k_weight: device
+ * fp32[D], 16-byte aligned; null: those heads are left as they are. eps is
+ * positive and finite. */
+typedef struct rssm_head_norm {
+  const float *q_weight;
+  const float *k_weight;
+  float eps;
+} rssm_head_norm;
+
+/*
+ * rssm_kv_append with norms of q and k in the same pass (norm null: none), and
+ * with v_out (may be null, contiguous [N][HKV][D], 16-byte aligned; may be v
+ * itself where that is contiguous), which takes the values in a row as k_out
+ * takes the keys. Both take what the pages hold: from quantised pages the
+ * values that the codes stand for, rounded to dtype, so that the attention of a
+ * prompt over k_out and v_out sees what later tokens will see.
+ */
+rssm_status rssm_kv_append_norm(rssm_kv_handle *h, int32_t layer, const void *q,
+                                const void *k, const void *v, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride,
+                                const rssm_head_norm *norm,
+                                const rssm_rope *rope, const int32_t *positions,
+                                const int32_t *cu_seqlens, const int32_t *slot,
+                                int32_t B, int32_t T, int32_t N, void *q_out,
+                                void *k_out, void *v_out, void *stream);
+
+/*
+ * One layer's cached keys and values in a row: k_out and v_out, contiguous
+ * [N][HKV][D] in dtype, 16-byte aligned, either may be null (both: nothing is
+ * done), take tokens [first[r], first[r] + T_r) of slot[r] (first: device
+ * int32[B], null: 0) at [cu_seqlens[r], cu_seqlens[r+1]), or with cu_seqlens
+ * null at [r T, (r + 1) T) of N = B T. Quantised pages give the values that their codes stand for,
+ * rounded to dtype. That is the part of a prompt's keys that the cache holds
+ * already, as rssm_attn_prefill reads it. A slot may be named by several rows.
+ * A token that its slot's pages do not hold, or before the first one, sets
+ * RSSM_DEVERR_PAGES: it is skipped, its outputs left as they are. Offsets that
+ * decrease or leave [0, N] set RSSM_DEVERR_SEQLEN and skip the row.
+ */
+rssm_status rssm_kv_gather(rssm_kv_handle *h, int32_t layer,
+                           const int32_t *slot, const int32_t *first,
+                           const int32_t *cu_seqlens, int32_t B, int32_t T,
+                           int32_t N, void *k_out, void *v_out, void *stream);
 
 /*
  * Attention of a window of T (1 <= T <= 64) new tokens per row over the

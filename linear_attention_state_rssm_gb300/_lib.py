@@ -32,6 +32,8 @@ SYMBOLS = ("rssm_required_bytes", "rssm_alloc", "rssm_free", "rssm_decode", "rss
            "rssm_kv_required_bytes", "rssm_kv_alloc", "rssm_kv_free", "rssm_kv_reserve",
            "rssm_kv_commit", "rssm_kv_fork", "rssm_kv_release", "rssm_kv_compact",
            "rssm_kv_append", "rssm_attn_decode", "rssm_attn_prefill",
+           "rssm_kv_quant_required_bytes", "rssm_kv_quant_alloc", "rssm_kv_append_norm",
+           "rssm_kv_gather",
            "rssm_kv_get_device_error", "rssm_kv_debug_withhold")
 
 
@@ -86,6 +88,11 @@ class rssm_rope(ctypes.Structure):
                 ("sections", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32)]
 
 
+class rssm_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _L = ctypes.c_int64
@@ -135,6 +142,15 @@ def load() -> ctypes.CDLL:
         "rssm_kv_compact": ([_P, _P], _I),
         "rssm_kv_append": ([_P, _I, _P, _P, _P, _L, _L, _L, ctypes.POINTER(rssm_rope), _P, _P, _P,
                             _I, _I, _I, _P, _P, _P], _I),
+        "rssm_kv_quant_required_bytes": ([ctypes.POINTER(rssm_kv_config),
+                                          ctypes.POINTER(rssm_kv_sizes),
+                                          ctypes.POINTER(ctypes.c_size_t)], _I),
+        "rssm_kv_quant_alloc": ([ctypes.POINTER(rssm_kv_config),
+                                 ctypes.POINTER(rssm_kv_buffers), _P, ctypes.POINTER(_P)], _I),
+        "rssm_kv_append_norm": ([_P, _I, _P, _P, _P, _L, _L, _L, ctypes.POINTER(rssm_head_norm),
+                                 ctypes.POINTER(rssm_rope), _P, _P, _P, _I, _I, _I, _P, _P, _P,
+                                 _P], _I),
+        "rssm_kv_gather": ([_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P], _I),
         "rssm_attn_decode": ([_P, _I, _P, _L, _P, _I, _I, _P, _P, _P], _I),
         "rssm_attn_prefill": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P],
                               _I),
@@ -380,6 +396,39 @@ def rssm_kv_append(handle, layer, q, k, v, q_stride, k_stride, v_stride, rope, p
                                  v_stride, None if rope is None else ctypes.byref(rope),
                                  _ptr(positions), _ptr(cu_seqlens), _ptr(slot), B, T, N,
                                  _ptr(q_out), _ptr(k_out), _stream(stream)), "rssm_kv_append")
+
+
+def rssm_kv_quant_required_bytes(cfg: rssm_kv_config):
+    """Sizes of a cache with quantised pages, and of its scales."""
+    out, scales = rssm_kv_sizes(), ctypes.c_size_t(0)
+    _check(load().rssm_kv_quant_required_bytes(ctypes.byref(cfg), ctypes.byref(out),
+                                               ctypes.byref(scales)),
+           "rssm_kv_quant_required_bytes")
+    return out, scales.value
+
+
+def rssm_kv_quant_alloc(cfg: rssm_kv_config, bufs: rssm_kv_buffers, scales) -> int:
+    h = _P()
+    _check(load().rssm_kv_quant_alloc(ctypes.byref(cfg), ctypes.byref(bufs), _ptr(scales),
+                                      ctypes.byref(h)), "rssm_kv_quant_alloc")
+    return h.value
+
+
+def rssm_kv_append_norm(handle, layer, q, k, v, q_stride, k_stride, v_stride, norm, rope,
+                        positions, cu_seqlens, slot, B, T, N, q_out, k_out=None, v_out=None,
+                        stream=None):
+    _check(load().rssm_kv_append_norm(handle, layer, _ptr(q), _ptr(k), _ptr(v), q_stride,
+                                      k_stride, v_stride,
+                                      None if norm is None else ctypes.byref(norm),
+                                      None if rope is None else ctypes.byref(rope),
+                                      _ptr(positions), _ptr(cu_seqlens), _ptr(slot), B, T, N,
+                                      _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(stream)),
+           "rssm_kv_append_norm")
+
+
+def rssm_kv_gather(handle, layer, slot, first, cu_seqlens, B, T, N, k_out, v_out, stream=None):
+    _check(load().rssm_kv_gather(handle, layer, _ptr(slot), _ptr(first), _ptr(cu_seqlens), B, T,
+                                 N, _ptr(k_out), _ptr(v_out), _stream(stream)), "rssm_kv_gather")
 
 
 def rssm_attn_decode(handle, layer, q, q_stride, slot, B, T, o, lse, stream=None):

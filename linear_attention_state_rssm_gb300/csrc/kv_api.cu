@@ -15,6 +15,7 @@ struct rssm_kv_handle {
   int shift;            // log2(page_size)
   size_t layer_bytes;   // one layer's keys (or values)
   size_t page_bytes;    // one page of one layer's keys (or values)
+  unsigned char* scales;  // e4m3 pages: [pool row][2] powers of two (else null)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   alignas(64) unsigned char maps[kKvMapBytes];  // the pool's tensor maps
 };
@@ -50,8 +51,62 @@ rssm_status check_config(const rssm_kv_config* c) {
   return RSSM_OK;
 }
 
-size_t page_bytes(const rssm_kv_config& c) {
-  return (size_t)c.HKV * c.page_size * c.D * dtype_bytes(c.dtype);
+size_t page_bytes(const rssm_kv_config& c, bool quant) {
+  return (size_t)c.HKV * c.page_size * c.D * (quant ? 1 : dtype_bytes(c.dtype));
+}
+size_t scale_page_bytes(const rssm_kv_config& c) { return (size_t)2 * c.HKV * c.page_size; }
+
+rssm_status check_quant_config(const rssm_kv_config* c) {
+  const rssm_status st = check_config(c);
+  if (st != RSSM_OK) return st;
+  return c->dtype == RSSM_F32 ? RSSM_ERR_UNSUPPORTED : RSSM_OK;
+}
+
+void fill_sizes(const rssm_kv_config& c, bool quant, rssm_kv_sizes* out) {
+  out->k_pages = out->v_pages = (size_t)c.n_layers * c.n_pages * page_bytes(c, quant);
+  out->table = (size_t)c.n_slots * c.max_pages * 4;
+  out->held = out->length = (size_t)c.n_slots * 4;
+  out->refs = (size_t)c.n_pages * 4;
+  out->work = KvWork(c.n_pages).total;
+  out->err_word = 4;
+}
+
+// `scales` null: pages of the cache's dtype
+rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, void* scales,
+                        rssm_kv_handle** out) {
+  if (!buf->k_pages || !buf->v_pages || !buf->table || !buf->held || !buf->length || !buf->refs ||
+      !buf->work || !buf->err_word)
+    return RSSM_ERR_INVALID_ARG;
+  if (!aligned16(buf->k_pages) || !aligned16(buf->v_pages) || !aligned16(buf->work) ||
+      !aligned4(buf->table) || !aligned4(buf->held) || !aligned4(buf->length) ||
+      !aligned4(buf->refs) || !aligned4(buf->err_word) || !aligned16(scales))
+    return RSSM_ERR_INVALID_ARG;
+  rssm_kv_handle* h = new (std::nothrow) rssm_kv_handle;
+  if (h == nullptr) return RSSM_ERR_CUDA;
+  h->cfg = *cfg;
+  h->buf = *buf;
+  h->shift = 0;
+  while ((1 << h->shift) < cfg->page_size) ++h->shift;
+  h->scales = static_cast<unsigned char*>(scales);
+  h->page_bytes = page_bytes(*cfg, scales != nullptr);
+  h->layer_bytes = (size_t)cfg->n_pages * h->page_bytes;
+  h->hook_cta = h->hook_unit = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype);
+  if (e == cudaSuccess) e = attn_prompt_prepare(cfg->D, cfg->dtype);
+  if (e == cudaSuccess && scales == nullptr)
+    e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
+                         (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
+                         cfg->D, cfg->dtype);
+  if (e != cudaSuccess) {
+    delete h;
+    return RSSM_ERR_CUDA;
+  }
+  *out = h;
+  return RSSM_OK;
 }
 
 rssm_status check_rows(const rssm_kv_handle* h, const int32_t* slot, int32_t B) {
@@ -92,6 +147,9 @@ rssm_status copy_pages(const rssm_kv_handle* h, const PageParams& p, bool remap,
   CopyParams c{};
   c.k = static_cast<unsigned char*>(h->buf.k_pages);
   c.v = static_cast<unsigned char*>(h->buf.v_pages);
+  c.scales = h->scales;
+  c.scale_page_bytes = scale_page_bytes(h->cfg);
+  c.scale_layer_bytes = (size_t)h->cfg.n_pages * c.scale_page_bytes;
   c.moves = p.moves;
   c.src = p.src;
   c.dst = p.dst;
@@ -113,12 +171,7 @@ rssm_status rssm_kv_required_bytes(const rssm_kv_config* cfg, rssm_kv_sizes* out
   const rssm_status st = check_config(cfg);
   if (st != RSSM_OK) return st;
   if (out == nullptr) return RSSM_ERR_INVALID_ARG;
-  out->k_pages = out->v_pages = (size_t)cfg->n_layers * cfg->n_pages * page_bytes(*cfg);
-  out->table = (size_t)cfg->n_slots * cfg->max_pages * 4;
-  out->held = out->length = (size_t)cfg->n_slots * 4;
-  out->refs = (size_t)cfg->n_pages * 4;
-  out->work = KvWork(cfg->n_pages).total;
-  out->err_word = 4;
+  fill_sizes(*cfg, false, out);
   return RSSM_OK;
 }
 
@@ -127,38 +180,25 @@ rssm_status rssm_kv_alloc(const rssm_kv_config* cfg, const rssm_kv_buffers* buf,
   const rssm_status st = check_config(cfg);
   if (st != RSSM_OK) return st;
   if (buf == nullptr || out == nullptr) return RSSM_ERR_INVALID_ARG;
-  if (!buf->k_pages || !buf->v_pages || !buf->table || !buf->held || !buf->length || !buf->refs ||
-      !buf->work || !buf->err_word)
-    return RSSM_ERR_INVALID_ARG;
-  if (!aligned16(buf->k_pages) || !aligned16(buf->v_pages) || !aligned16(buf->work) ||
-      !aligned4(buf->table) || !aligned4(buf->held) || !aligned4(buf->length) ||
-      !aligned4(buf->refs) || !aligned4(buf->err_word))
-    return RSSM_ERR_INVALID_ARG;
-  rssm_kv_handle* h = new (std::nothrow) rssm_kv_handle;
-  if (h == nullptr) return RSSM_ERR_CUDA;
-  h->cfg = *cfg;
-  h->buf = *buf;
-  h->shift = 0;
-  while ((1 << h->shift) < cfg->page_size) ++h->shift;
-  h->page_bytes = page_bytes(*cfg);
-  h->layer_bytes = (size_t)cfg->n_pages * h->page_bytes;
-  h->hook_cta = h->hook_unit = -1;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype);
-  if (e == cudaSuccess) e = attn_prompt_prepare(cfg->D, cfg->dtype);
-  if (e == cudaSuccess)
-    e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
-                         (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
-                         cfg->D, cfg->dtype);
-  if (e != cudaSuccess) {
-    delete h;
-    return RSSM_ERR_CUDA;
-  }
-  *out = h;
+  return make_handle(cfg, buf, nullptr, out);
+}
+
+rssm_status rssm_kv_quant_required_bytes(const rssm_kv_config* cfg, rssm_kv_sizes* out,
+                                         size_t* scales) {
+  const rssm_status st = check_quant_config(cfg);
+  if (st != RSSM_OK) return st;
+  if (out == nullptr || scales == nullptr) return RSSM_ERR_INVALID_ARG;
+  fill_sizes(*cfg, true, out);
+  *scales = (size_t)cfg->n_layers * cfg->n_pages * scale_page_bytes(*cfg);
   return RSSM_OK;
+}
+
+rssm_status rssm_kv_quant_alloc(const rssm_kv_config* cfg, const rssm_kv_buffers* buf,
+                                void* scales, rssm_kv_handle** out) {
+  const rssm_status st = check_quant_config(cfg);
+  if (st != RSSM_OK) return st;
+  if (buf == nullptr || scales == nullptr || out == nullptr) return RSSM_ERR_INVALID_ARG;
+  return make_handle(cfg, buf, scales, out);
 }
 
 void rssm_kv_free(rssm_kv_handle* h) { delete h; }
@@ -238,6 +278,17 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
                            const rssm_rope* rope, const int32_t* positions,
                            const int32_t* cu_seqlens, const int32_t* slot, int32_t B, int32_t T,
                            int32_t N, void* q_out, void* k_out, void* stream) {
+  return rssm_kv_append_norm(h, layer, q, k, v, q_stride, k_stride, v_stride, nullptr, rope,
+                             positions, cu_seqlens, slot, B, T, N, q_out, k_out, nullptr, stream);
+}
+
+rssm_status rssm_kv_append_norm(rssm_kv_handle* h, int32_t layer, const void* q, const void* k,
+                                const void* v, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, const rssm_head_norm* norm,
+                                const rssm_rope* rope, const int32_t* positions,
+                                const int32_t* cu_seqlens, const int32_t* slot, int32_t B,
+                                int32_t T, int32_t N, void* q_out, void* k_out, void* v_out,
+                                void* stream) {
   const rssm_status st = check_rows(h, slot, B);
   if (st != RSSM_OK) return st;
   const rssm_kv_config& c = h->cfg;
@@ -267,19 +318,30 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
     p.max_pos = rope->max_pos;
     p.interleaved = rope->interleaved != 0;
   }
+  if (norm != nullptr) {
+    if (!aligned16(norm->q_weight) || !aligned16(norm->k_weight) || !std::isfinite(norm->eps) ||
+        !(norm->eps > 0.f))
+      return RSSM_ERR_INVALID_ARG;
+    p.q_weight = norm->q_weight;
+    p.k_weight = norm->k_weight;
+    p.eps = norm->eps;
+  }
   if (B == 0 || N == 0) return RSSM_OK;
   if (!tokens_ok(c, k, k_stride, c.HKV) || !tokens_ok(c, v, v_stride, c.HKV))
     return RSSM_ERR_INVALID_ARG;
   if (q != nullptr && (!tokens_ok(c, q, q_stride, c.HQ) || !aligned16(q_out)))
     return RSSM_ERR_INVALID_ARG;
-  if (!aligned16(k_out)) return RSSM_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return RSSM_ERR_INVALID_ARG;
   p.q = q;
   p.k = k;
   p.v = v;
   p.q_out = q_out;
   p.k_out = k_out;
+  p.v_out = v_out;
   p.kp = static_cast<unsigned char*>(h->buf.k_pages) + (size_t)layer * h->layer_bytes;
   p.vp = static_cast<unsigned char*>(h->buf.v_pages) + (size_t)layer * h->layer_bytes;
+  if (h->scales != nullptr)
+    p.scales = h->scales + (size_t)layer * c.n_pages * scale_page_bytes(c);
   p.cu = cu_seqlens;
   p.slot = slot;
   p.table = h->buf.table;
@@ -303,6 +365,44 @@ rssm_status rssm_kv_append(rssm_kv_handle* h, int32_t layer, const void* q, cons
   return from_cuda(kv_append_launch(p, static_cast<cudaStream_t>(stream)));
 }
 
+rssm_status rssm_kv_gather(rssm_kv_handle* h, int32_t layer, const int32_t* slot,
+                           const int32_t* first, const int32_t* cu_seqlens, int32_t B, int32_t T,
+                           int32_t N, void* k_out, void* v_out, void* stream) {
+  const rssm_status st = check_rows(h, slot, B);
+  if (st != RSSM_OK) return st;
+  const rssm_kv_config& c = h->cfg;
+  if (layer < 0 || layer >= c.n_layers) return RSSM_ERR_INVALID_ARG;
+  if (N < 0 || !aligned4(cu_seqlens) || !aligned4(first)) return RSSM_ERR_INVALID_ARG;
+  if (cu_seqlens == nullptr && (T < 1 || T > kMaxWindow || (int64_t)B * T != N))
+    return RSSM_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return RSSM_ERR_INVALID_ARG;
+  if (B == 0 || N == 0 || (k_out == nullptr && v_out == nullptr)) return RSSM_OK;
+  GatherParams p{};
+  p.kp = static_cast<unsigned char*>(h->buf.k_pages) + (size_t)layer * h->layer_bytes;
+  p.vp = static_cast<unsigned char*>(h->buf.v_pages) + (size_t)layer * h->layer_bytes;
+  if (h->scales != nullptr)
+    p.scales = h->scales + (size_t)layer * c.n_pages * scale_page_bytes(c);
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.cu = cu_seqlens;
+  p.first = first;
+  p.slot = slot;
+  p.table = h->buf.table;
+  p.held = h->buf.held;
+  p.err = h->buf.err_word;
+  p.B = B;
+  p.T = T;
+  p.N = N;
+  p.HKV = c.HKV;
+  p.D = c.D;
+  p.n_slots = c.n_slots;
+  p.n_pages = c.n_pages;
+  p.max_pages = c.max_pages;
+  p.shift = h->shift;
+  p.dt = c.dtype;
+  return from_cuda(kv_gather_launch(p, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
 rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, int64_t q_stride,
                              const int32_t* slot, int32_t B, int32_t T, void* o, float* lse,
                              void* stream) {
@@ -311,6 +411,7 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   const rssm_kv_config& c = h->cfg;
   if (layer < 0 || layer >= c.n_layers || T < 1) return RSSM_ERR_INVALID_ARG;
   if (T > 64) return RSSM_ERR_UNSUPPORTED;
+  if (h->scales != nullptr) return RSSM_ERR_UNSUPPORTED;
   if (B == 0) return RSSM_OK;
   if (!tokens_ok(c, q, q_stride, c.HQ) || o == nullptr || !aligned16(o) || !aligned4(lse))
     return RSSM_ERR_INVALID_ARG;

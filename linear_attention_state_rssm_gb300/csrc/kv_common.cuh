@@ -1,7 +1,8 @@
 // Parameters and launches of the full-attention layers' operators: the paged
-// key-value cache (kv_pages.cu), the rotary append (kv_append.cu), attention of
-// new tokens over the pages (attn_decode.cu) and of whole prompts
-// (attn_prompt.cu, attn_prompt_tc.cu). Internal to librssm.
+// key-value cache (kv_pages.cu), the rotary append (kv_append.cu), pages read
+// back in a row (kv_gather.cu), attention of new tokens over the pages
+// (attn_decode.cu) and of whole prompts (attn_prompt.cu, attn_prompt_tc.cu).
+// Internal to librssm.
 #pragma once
 
 #include "rssm_common.cuh"
@@ -67,12 +68,14 @@ struct PageParams {
 struct CopyParams {
   unsigned char* k;
   unsigned char* v;
+  unsigned char* scales;  // e4m3 pages (else null)
   const int32_t* moves;
   const int32_t* src;
   const int32_t* dst;
   const int32_t* map;     // compaction: renames the tables' pages (else null)
   int32_t* table;
   size_t page_bytes, layer_bytes, table_size;
+  size_t scale_page_bytes, scale_layer_bytes;
   int n_layers, n_pages;
 };
 
@@ -92,8 +95,13 @@ struct AppendParams {
   const void* v;
   void* q_out;
   void* k_out;        // or null
+  void* v_out;        // or null
   unsigned char* kp;  // this layer's pages
   unsigned char* vp;
+  unsigned char* scales;  // this layer's, of e4m3 pages (else null)
+  const float* q_weight;  // [D] norms of q and k, or null
+  const float* k_weight;
+  float eps;
   const float* rope;         // [max_pos][2][P] cosines, sines; null: no rotation
   const int32_t* positions;  // [axes][N]; null: the token's place in its cache
   const int32_t* cu;
@@ -105,6 +113,22 @@ struct AppendParams {
   long long qs, ks, vs;  // token strides, elements
   int B, T, N, HQ, HKV, D, P, axes, max_pos, interleaved;
   int sec[kMaxRopeAxes];
+  int n_slots, n_pages, max_pages, shift, dt;
+};
+
+struct GatherParams {
+  const unsigned char* kp;  // this layer's pages
+  const unsigned char* vp;
+  const unsigned char* scales;  // this layer's, of e4m3 pages (else null)
+  void* k_out;              // [N][HKV][D], or null
+  void* v_out;
+  const int32_t* cu;        // or null: T tokens a row
+  const int32_t* first;     // [B] cache position of each row's first token; null: 0
+  const int32_t* slot;
+  const int32_t* table;
+  const int32_t* held;
+  uint32_t* err;
+  int B, T, N, HKV, D;
   int n_slots, n_pages, max_pages, shift, dt;
 };
 
@@ -147,6 +171,7 @@ cudaError_t kv_plan_launch(int mode, const PageParams& p, cudaStream_t st);
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
+cudaError_t kv_gather_launch(const GatherParams& p, int num_sms, cudaStream_t st);
 cudaError_t attn_decode_prepare(int D, int dt);
 // tensor maps of the pool (kKvMapBytes, 64-byte aligned) and the launch with them
 constexpr int kKvMapBytes = 256;

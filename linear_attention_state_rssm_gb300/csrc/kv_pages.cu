@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_compact_kernel(const PagePa
   if (tid == 0) *p.moves = movers;
 }
 
-// Copies of whole pages, every layer's keys and values, 16 KB of a page per
-// CTA step; with a map, the tables take the pages' new places too.
+// Copies of whole pages, every layer's keys and values (and scales), 16 KB of a
+// page per CTA step; with a map, the tables take the pages' new places too.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVecs = 4;
 
@@ -340,14 +340,17 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const CopyParam
   const int moves = *p.moves;
   constexpr size_t step = (size_t)kCopyThreads * kCopyVecs * 16;
   const size_t chunks = (p.page_bytes + step - 1) / step;
-  const size_t units = (size_t)moves * chunks * p.n_layers * 2;
+  const int kinds = p.scales != nullptr ? 3 : 2;  // keys, values, scales of quantised pages
+  const size_t units = (size_t)moves * chunks * p.n_layers * kinds;
   for (size_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const size_t mv = u / (chunks * p.n_layers * 2), rest = u % (chunks * p.n_layers * 2);
-    const size_t lay = rest / (chunks * 2), which = rest / chunks % 2, chunk = rest % chunks;
-    unsigned char* base = (which ? p.v : p.k) + lay * p.layer_bytes;
-    const uint4* s = reinterpret_cast<const uint4*>(base + p.src[mv] * p.page_bytes);
-    uint4* d = reinterpret_cast<uint4*>(base + p.dst[mv] * p.page_bytes);
-    const size_t at = chunk * step / 16 + threadIdx.x, end = p.page_bytes / 16;
+    const size_t mv = u / (chunks * p.n_layers * kinds), rest = u % (chunks * p.n_layers * kinds);
+    const size_t lay = rest / (chunks * kinds), which = rest / chunks % kinds, chunk = rest % chunks;
+    const size_t bytes = which == 2 ? p.scale_page_bytes : p.page_bytes;
+    unsigned char* base = (which == 0 ? p.k : which == 1 ? p.v : p.scales) +
+                          lay * (which == 2 ? p.scale_layer_bytes : p.layer_bytes);
+    const uint4* s = reinterpret_cast<const uint4*>(base + p.src[mv] * bytes);
+    uint4* d = reinterpret_cast<uint4*>(base + p.dst[mv] * bytes);
+    const size_t at = chunk * step / 16 + threadIdx.x, end = bytes / 16;
     uint4 v[kCopyVecs];
 #pragma unroll
     for (int i = 0; i < kCopyVecs; ++i) {

@@ -192,11 +192,33 @@ class RotaryTable:
                    interleaved)
 
 
+class HeadNorm:
+    """Weights of the norms of queries and keys for KVCache.rssm_kv_append: fp32
+    [D] each (None: those heads are left as they are). Kept, not copied."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps=1e-6):
+        sizes = set()
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
+            if w.dtype != torch.float32 or w.dim() != 1 or not w.is_cuda or not w.is_contiguous():
+                raise ValueError("weights: contiguous fp32 [D] on the device")
+            sizes.add(w.shape[0])
+        if len(sizes) > 1:
+            raise ValueError("weights: one head size")
+        self.D = sizes.pop() if sizes else None
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self.struct = _lib.rssm_head_norm(*(None if w is None else w.data_ptr()
+                                            for w in (q_weight, k_weight)), float(eps))
+
+
 class KVCache:
     """Paged keys and values of the full-attention layers, ``n_slots`` requests.
 
     Buffers (row-major):
-      k_pages, v_pages [n_layers, n_pages, HKV, page_size, D]  dtype
+      k_pages, v_pages [n_layers, n_pages, HKV, page_size, D]  dtype, or e4m3 with
+      page_scales      [n_layers, n_pages, HKV, page_size, 2] uint8 (page_dtype "e4m3":
+                       quantised as they are written; else None)
       table            [n_slots, max_pages] int32 (-1: no page)
       held, length     [n_slots] int32: pages held, committed tokens
       refs             [n_pages] int32: tables that name the page
@@ -208,20 +230,32 @@ class KVCache:
     """
 
     def __init__(self, n_layers=1, n_slots=1, HQ=1, HKV=1, D=128, n_pages=1, page_size=64,
-                 max_pages=None, dtype="bf16", scale=None, device="cuda"):
+                 max_pages=None, dtype="bf16", scale=None, device="cuda", page_dtype=None):
+        if page_dtype not in (None, dtype, "e4m3"):
+            raise ValueError('page_dtype: None (dtype) or "e4m3"')
+        quant = page_dtype == "e4m3"
         max_pages = n_pages if max_pages is None else max_pages
         self.cfg = _lib.make_kv_config(n_layers, n_slots, HQ, HKV, D, n_pages, page_size,
                                        max_pages, dtype, scale)
         self.n_layers, self.n_slots, self.HQ, self.HKV, self.D = n_layers, n_slots, HQ, HKV, D
         self.n_pages, self.page_size, self.max_pages = n_pages, page_size, max_pages
         self.dtype, self.scale = dtype, self.cfg.scale
+        self.page_dtype = "e4m3" if quant else dtype
         self._torch_dtype = _TORCH[dtype]
         self.device = torch.device(device)
-        sizes = _lib.rssm_kv_required_bytes(self.cfg)  # validates the configuration
-        dev, t = self.device, _TORCH[dtype]
+        if quant:  # validates the configuration
+            sizes, _ = _lib.rssm_kv_quant_required_bytes(self.cfg)
+        else:
+            sizes = _lib.rssm_kv_required_bytes(self.cfg)
+        dev, t = self.device, torch.uint8 if quant else _TORCH[dtype]
         shape = (n_layers, n_pages, HKV, page_size, D)
         self.k_pages = torch.zeros(shape, dtype=t, device=dev)
         self.v_pages = torch.zeros(shape, dtype=t, device=dev)
+        self.page_scales = None
+        if quant:
+            self.k_pages = self.k_pages.view(torch.float8_e4m3fn)
+            self.v_pages = self.v_pages.view(torch.float8_e4m3fn)
+            self.page_scales = torch.zeros(shape[:4] + (2,), dtype=torch.uint8, device=dev)
         self.table = torch.full((n_slots, max_pages), -1, dtype=torch.int32, device=dev)
         self.held = torch.zeros(n_slots, dtype=torch.int32, device=dev)
         self.length = torch.zeros(n_slots, dtype=torch.int32, device=dev)
@@ -232,7 +266,8 @@ class KVCache:
             self.k_pages, self.v_pages, self.table, self.held, self.length, self.refs,
             self.work, self.err_word)))
         with torch.cuda.device(dev):
-            self.handle = _lib.rssm_kv_alloc(self.cfg, bufs)
+            self.handle = _lib.rssm_kv_quant_alloc(self.cfg, bufs, self.page_scales) if quant \
+                else _lib.rssm_kv_alloc(self.cfg, bufs)
 
     # ---------------------------------------------------------------- pages
     def rssm_kv_reserve(self, slot, T=1, cu_seqlens=None, stream=None):
@@ -263,9 +298,10 @@ class KVCache:
 
     # ------------------------------------------------------------ attention
     def rssm_kv_append(self, layer, q, k, v, slot, T=1, q_out=None, rope=None, positions=None,
-                       cu_seqlens=None, k_out=None, stream=None):
-        """Rotate q (into q_out) and k, write k and v to the slots' pages (and
-        the rotated k to k_out, for rssm_attn_prefill)."""
+                       cu_seqlens=None, k_out=None, stream=None, norm=None, v_out=None):
+        """Norms (a HeadNorm) and rotation of q (into q_out) and k, k and v to the
+        slots' pages (and, as the pages hold them, to k_out and v_out for
+        rssm_attn_prefill)."""
         B = self._index(slot)
         self._index(cu_seqlens, B + 1)
         n, ks = self._tokens(k, self.HKV)
@@ -273,16 +309,35 @@ class KVCache:
         qs = self._tokens(q, self.HQ, n)[1] if q is not None else 0
         if q_out is not None:
             self._output(q_out, n)
-        if k_out is not None and (k_out.dtype != self._torch_dtype or not k_out.is_contiguous()
-                                  or not k_out.is_cuda or k_out.numel() != n * self.HKV * self.D):
-            raise ValueError("k_out: contiguous, the cache's dtype, [tokens, HKV, D]")
+        if k_out is not None:
+            self._row("k_out", k_out, n)
+        if v_out is not None:
+            self._row("v_out", v_out, n)
+        if norm is not None and norm.D not in (None, self.D):
+            raise ValueError(f"norm: weights of {self.D} values")
         if positions is not None:
             if rope is None:
                 raise ValueError("positions: with a rotary table")
             self._index(positions, rope.axes * n)
-        _lib.rssm_kv_append(self.handle, layer, q, k, v, qs, ks, vs,
-                            None if rope is None else rope.struct, positions, cu_seqlens, slot,
-                            B, T, n, q_out, k_out, stream)
+        _lib.rssm_kv_append_norm(self.handle, layer, q, k, v, qs, ks, vs,
+                                 None if norm is None else norm.struct,
+                                 None if rope is None else rope.struct, positions, cu_seqlens,
+                                 slot, B, T, n, q_out, k_out, v_out, stream)
+
+    def rssm_kv_gather(self, layer, slot, k_out, v_out, T=1, cu_seqlens=None, first=None,
+                       stream=None):
+        """Cached tokens [first[r], first[r] + T_r) of each row's slot in a row
+        (k_out or v_out may be None)."""
+        B = self._index(slot)
+        self._index(cu_seqlens, B + 1)
+        self._index(first, B)
+        n = B * T if cu_seqlens is None else None
+        for name, x in (("k_out", k_out), ("v_out", v_out)):
+            if x is not None:
+                n = x.shape[0] if n is None else n
+                self._row(name, x, n)
+        _lib.rssm_kv_gather(self.handle, layer, slot, first, cu_seqlens, B, T, n or 0, k_out,
+                            v_out, stream)
 
     def rssm_attn_decode(self, layer, q, slot, T, o, lse=None, stream=None):
         """T new tokens per row over the slot's pages (their keys appended before)."""
@@ -350,6 +405,11 @@ class KVCache:
         if x.dtype != self._torch_dtype or not x.is_cuda or s2 != 1 or (s1 != D and heads > 1):
             raise ValueError("the cache's dtype, on the device, with contiguous heads")
         return m, s0 if m > 1 else heads * D
+
+    def _row(self, name, x, n):
+        if x.dtype != self._torch_dtype or not x.is_contiguous() or not x.is_cuda \
+                or x.numel() != n * self.HKV * self.D:
+            raise ValueError(f"{name}: contiguous, the cache's dtype, [tokens, HKV, D]")
 
     def _output(self, o, n, lse=None):
         if o.dtype != self._torch_dtype or o.numel() != n * self.HQ * self.D \

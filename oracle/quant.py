@@ -1,0 +1,62 @@
+"""fp64 reference of quantised pages and of the norms of queries and keys. Test
+infrastructure; shares no code with the CUDA path."""
+import math
+
+import numpy as np
+
+
+def e4m3_values():
+    """The 256 values: sign, four bits of exponent (bias 7), three of mantissa;
+    the largest pattern of either sign is NaN."""
+    out = np.empty(256)
+    for b in range(256):
+        e, m = b >> 3 & 15, b & 7
+        x = math.nan if b & 127 == 127 else \
+            (m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10))
+        out[b] = -x if b & 128 else x
+    return out
+
+
+VALUES = e4m3_values()
+_UP = VALUES[:127]  # 0 .. 448
+
+
+def exponent(a):
+    """Least e with a <= 448 2^e, kept within [-64, 63]."""
+    e = -64
+    while e < 63 and a > 448 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def quantise(x):
+    """x [..., D] -> codes (uint8) and e + 127 (uint8) of each head."""
+    x = np.asarray(x, np.float64)
+    flat = x.reshape(-1, x.shape[-1])
+    codes = np.empty(flat.shape, np.uint8)
+    scale = np.empty(flat.shape[0], np.uint8)
+    for r, row in enumerate(flat):
+        fin = np.abs(row[np.isfinite(row)])
+        e = exponent(fin.max(initial=0.0))
+        scale[r] = e + 127
+        y = np.minimum(np.abs(np.where(np.isfinite(row), row, 0.0)) * 2.0 ** -e, 448.0)
+        hi = np.clip(np.searchsorted(_UP, y), 0, 126)  # nearest of two neighbours, ties to even
+        lo = np.maximum(hi - 1, 0)
+        up = _UP[hi] - y
+        down = y - _UP[lo]
+        c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
+        c |= np.where(np.signbit(row), 128, 0).astype(np.uint8)
+        codes[r] = np.where(np.isfinite(row), c, 127)
+    return codes.reshape(x.shape), scale.reshape(x.shape[:-1])
+
+
+def value(codes, scale):
+    """What codes [..., D] with their bytes [...] stand for."""
+    return VALUES[codes] * 2.0 ** (scale.astype(np.float64) - 127)[..., None]
+
+
+def norm(x, w, eps):
+    """x [..., D] by the root of its mean square, times w (None: x itself)."""
+    if w is None:
+        return np.asarray(x, np.float64)
+    return x * w / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
