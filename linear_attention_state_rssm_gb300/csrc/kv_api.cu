@@ -95,12 +95,12 @@ rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, v
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype);
+  if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype, scales != nullptr);
   if (e == cudaSuccess) e = attn_prompt_prepare(cfg->D, cfg->dtype);
-  if (e == cudaSuccess && scales == nullptr)
+  if (e == cudaSuccess)
     e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
                          (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
-                         cfg->D, cfg->dtype);
+                         cfg->D, cfg->dtype, scales != nullptr);
   if (e != cudaSuccess) {
     delete h;
     return RSSM_ERR_CUDA;
@@ -411,7 +411,6 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   const rssm_kv_config& c = h->cfg;
   if (layer < 0 || layer >= c.n_layers || T < 1) return RSSM_ERR_INVALID_ARG;
   if (T > 64) return RSSM_ERR_UNSUPPORTED;
-  if (h->scales != nullptr) return RSSM_ERR_UNSUPPORTED;
   if (B == 0) return RSSM_OK;
   if (!tokens_ok(c, q, q_stride, c.HQ) || o == nullptr || !aligned16(o) || !aligned4(lse))
     return RSSM_ERR_INVALID_ARG;
@@ -419,6 +418,7 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   char* work = static_cast<char*>(h->buf.work);
   DecodeParams p{};
   p.q = q;
+  p.scales = h->scales;
   p.slot = slot;
   p.table = h->buf.table;
   p.held = h->buf.held;

@@ -132,8 +132,65 @@ struct GatherParams {
   int n_slots, n_pages, max_pages, shift, dt;
 };
 
+// What rows of a batch share (kv_share.cuh), in the caller's buffer: the groups,
+// and what the first of the two launches leaves for the second.
+struct ShareView {
+  int32_t* of;          // [2] B and T of the plan
+  int32_t* groups;      // [1] their number
+  int32_t* lost;        // [1] a wait ran out: the prefixes' outputs are not all there
+  int32_t* prefix;      // [B] keys of each row's shared prefix (0: none)
+  int32_t* lead;        // [B] row whose table the group's keys are read by
+  int32_t* order;       // [B] rows, group by group, each group's lead first
+  int32_t* begin;       // [B + 1] first place of a group in order
+  int32_t* group_keys;  // [B] keys of a group's prefix
+  int32_t* scratch;     // [2 B] of the plan
+  float2* ml;           // [B T][HQ] running maxima and sums of the prefixes
+  float* o;             // [B T][HQ][D] and outputs
+  __host__ __device__ static size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+  // the view of a buffer (null: only its size)
+  __host__ __device__ static size_t lay(void* base, int B, int T, int HQ, int D, ShareView* v) {
+    char* at = static_cast<char*>(base);
+    size_t n = 0;
+    auto take = [&](size_t bytes) {
+      const size_t from = n;
+      n += up(bytes);
+      return at + from;
+    };
+    const size_t b = (size_t)B * 4, rows = (size_t)B * T * HQ;
+    ShareView s{};
+    char* head = take(16);
+    char* prefix = take(b);
+    char* lead = take(b);
+    char* order = take(b);
+    char* begin = take(b + 4);
+    char* keys = take(b);
+    char* scratch = take(2 * b);
+    char* ml = take(rows * 8);
+    char* o = take(rows * (size_t)D * 4);
+    if (v != nullptr) {
+      s.of = reinterpret_cast<int32_t*>(head);
+      s.groups = s.of + 2;
+      s.lost = s.of + 3;
+      s.prefix = reinterpret_cast<int32_t*>(prefix);
+      s.lead = reinterpret_cast<int32_t*>(lead);
+      s.order = reinterpret_cast<int32_t*>(order);
+      s.begin = reinterpret_cast<int32_t*>(begin);
+      s.group_keys = reinterpret_cast<int32_t*>(keys);
+      s.scratch = reinterpret_cast<int32_t*>(scratch);
+      s.ml = reinterpret_cast<float2*>(ml);
+      s.o = reinterpret_cast<float*>(o);
+      *v = s;
+    }
+    return n;
+  }
+};
+__device__ __forceinline__ bool share_is_of(const ShareView& s, int B, int T) {
+  return s.of[0] == B && s.of[1] == T;
+}
+
 struct DecodeParams {
   const void* q;
+  const unsigned char* scales;  // all layers', of e4m3 pages (else null)
   const int32_t* slot;
   const int32_t* table;
   const int32_t* held;
@@ -149,6 +206,7 @@ struct DecodeParams {
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   float c;      // scale * log2(e)
+  ShareView share;
 };
 
 struct PromptParams {
@@ -172,11 +230,14 @@ cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
 cudaError_t kv_gather_launch(const GatherParams& p, int num_sms, cudaStream_t st);
-cudaError_t attn_decode_prepare(int D, int dt);
+cudaError_t attn_decode_prepare(int D, int dt, bool quant);
 // tensor maps of the pool (kKvMapBytes, 64-byte aligned) and the launch with them
 constexpr int kKvMapBytes = 256;
 cudaError_t attn_decode_maps(void* maps, const void* k, const void* v, long long rows, int D,
-                             int dt);
+                             int dt, bool quant);
+// kernels of quantised pages, mw warps to a stream; p null: prepares them all
+cudaError_t attn_decode_quant(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                              int sms, cudaStream_t st);
 cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st);
 int attn_decode_block_rows(int D, int dt, int rows);  // rows of a block for T G rows

@@ -32,22 +32,17 @@ def exponent(a):
 def quantise(x):
     """x [..., D] -> codes (uint8) and e + 127 (uint8) of each head."""
     x = np.asarray(x, np.float64)
-    flat = x.reshape(-1, x.shape[-1])
-    codes = np.empty(flat.shape, np.uint8)
-    scale = np.empty(flat.shape[0], np.uint8)
-    for r, row in enumerate(flat):
-        fin = np.abs(row[np.isfinite(row)])
-        e = exponent(fin.max(initial=0.0))
-        scale[r] = e + 127
-        y = np.minimum(np.abs(np.where(np.isfinite(row), row, 0.0)) * 2.0 ** -e, 448.0)
-        hi = np.clip(np.searchsorted(_UP, y), 0, 126)  # nearest of two neighbours, ties to even
-        lo = np.maximum(hi - 1, 0)
-        up = _UP[hi] - y
-        down = y - _UP[lo]
-        c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi).astype(np.uint8)
-        c |= np.where(np.signbit(row), 128, 0).astype(np.uint8)
-        codes[r] = np.where(np.isfinite(row), c, 127)
-    return codes.reshape(x.shape), scale.reshape(x.shape[:-1])
+    fine = np.isfinite(x)
+    mag = np.abs(np.where(fine, x, 0.0))
+    border = 448 * 2.0 ** np.arange(-64, 63)  # e is the number of borders passed, less 64
+    e = np.searchsorted(border, mag.max(-1), side="left") - 64
+    y = np.minimum(mag * 2.0 ** -e.astype(np.float64)[..., None], 448.0)
+    hi = np.clip(np.searchsorted(_UP, y), 0, 126)  # nearest of two neighbours, ties to even
+    lo = np.maximum(hi - 1, 0)
+    up, down = _UP[hi] - y, y - _UP[lo]
+    c = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    c = np.where(np.signbit(x), c | 128, c)
+    return np.where(fine, c, 127).astype(np.uint8), (e + 127).astype(np.uint8)
 
 
 def value(codes, scale):

@@ -23,6 +23,7 @@ def test_rounding_is_to_nearest_even_and_by_at_most_half_a_step():
     codes, scale = quant.quantise(x)
     y = quant.value(codes, scale)
     e = scale.astype(int) - 127
+    assert [quant.exponent(a) for a in np.abs(x).max(-1)] == e.tolist()
     step = np.maximum(2.0 ** -4 * np.abs(x), 2.0 ** -10 * 2.0 ** e[:, None])
     assert np.all(np.abs(y - x) <= step)
     # against the type's own conversion
