@@ -656,6 +656,38 @@ rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
                              int32_t T, void *o, float *lse, void *stream);
 
 /*
+ * Attention of new tokens for a batch whose slots share the pages of a prefix (a
+ * fork's full pages), each prefix read once for all its rows. rssm_kv_share
+ * finds the groups from the tables, once for a step's layers: rows whose tables
+ * begin with the same page, as many pages as all of them begin with and have
+ * committed whole. It writes them to `share`, a device buffer of the caller's of
+ * rssm_kv_share_bytes(B, T) bytes, 16-byte aligned, which also takes what the
+ * attention holds between its two launches: a buffer serves one call at a time.
+ * The rows may be in any order; rows that share nothing are served as by
+ * rssm_attn_decode, whose arguments, contract and results these are (sums in
+ * another order).
+ *
+ * The plan is of B, T and the rows' slots. It stays true while the slots grow,
+ * and through rssm_kv_compact; it has to be made anew where a row has another
+ * slot, and where a slot was released or forked into; rows whose slot has become
+ * null are left out. A row whose table does not begin with its group's pages any more, or whose slot has become shorter
+ * than its prefix, sets RSSM_DEVERR_PAGES and is skipped, and so is every row
+ * where B or T are not the plan's. Rows with a null slot, or one that is
+ * refused, are left out by rssm_kv_share, which sets no error bits. Where a wait
+ * runs out over a prefix (RSSM_DEVERR_TIMEOUT), the rows of groups are skipped
+ * until rssm_kv_share is called again.
+ */
+rssm_status rssm_kv_share_bytes(const rssm_kv_config *cfg, int32_t B, int32_t T,
+                                size_t *out);
+rssm_status rssm_kv_share(rssm_kv_handle *h, const int32_t *slot, int32_t B,
+                          int32_t T, void *share, void *stream);
+rssm_status rssm_attn_decode_shared(rssm_kv_handle *h, int32_t layer,
+                                    const void *q, int64_t q_stride,
+                                    const int32_t *slot, int32_t B, int32_t T,
+                                    void *share, void *o, float *lse,
+                                    void *stream);
+
+/*
  * Causal attention over prompts, packed: sequence r's query tokens are
  * [cu_seqlens[r], cu_seqlens[r+1]) of N, its keys and values
  * [cu_keys[r], cu_keys[r+1]) of M (cu_keys null: those of the query tokens,

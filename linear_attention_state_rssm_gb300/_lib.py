@@ -33,7 +33,7 @@ SYMBOLS = ("rssm_required_bytes", "rssm_alloc", "rssm_free", "rssm_decode", "rss
            "rssm_kv_commit", "rssm_kv_fork", "rssm_kv_release", "rssm_kv_compact",
            "rssm_kv_append", "rssm_attn_decode", "rssm_attn_prefill",
            "rssm_kv_quant_required_bytes", "rssm_kv_quant_alloc", "rssm_kv_append_norm",
-           "rssm_kv_gather",
+           "rssm_kv_gather", "rssm_kv_share_bytes", "rssm_kv_share", "rssm_attn_decode_shared",
            "rssm_kv_get_device_error", "rssm_kv_debug_withhold")
 
 
@@ -151,6 +151,10 @@ def load() -> ctypes.CDLL:
                                  ctypes.POINTER(rssm_rope), _P, _P, _P, _I, _I, _I, _P, _P, _P,
                                  _P], _I),
         "rssm_kv_gather": ([_P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P], _I),
+        "rssm_kv_share_bytes": ([ctypes.POINTER(rssm_kv_config), _I, _I,
+                                 ctypes.POINTER(ctypes.c_size_t)], _I),
+        "rssm_kv_share": ([_P, _P, _I, _I, _P, _P], _I),
+        "rssm_attn_decode_shared": ([_P, _I, _P, _L, _P, _I, _I, _P, _P, _P, _P], _I),
         "rssm_attn_decode": ([_P, _I, _P, _L, _P, _I, _I, _P, _P, _P], _I),
         "rssm_attn_prefill": ([_P, _P, _P, _P, _L, _L, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P],
                               _I),
@@ -434,6 +438,24 @@ def rssm_kv_gather(handle, layer, slot, first, cu_seqlens, B, T, N, k_out, v_out
 def rssm_attn_decode(handle, layer, q, q_stride, slot, B, T, o, lse, stream=None):
     _check(load().rssm_attn_decode(handle, layer, _ptr(q), q_stride, _ptr(slot), B, T, _ptr(o),
                                    _ptr(lse), _stream(stream)), "rssm_attn_decode")
+
+
+def rssm_kv_share_bytes(cfg: rssm_kv_config, B, T) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().rssm_kv_share_bytes(ctypes.byref(cfg), B, T, ctypes.byref(out)),
+           "rssm_kv_share_bytes")
+    return out.value
+
+
+def rssm_kv_share(handle, slot, B, T, share, stream=None):
+    _check(load().rssm_kv_share(handle, _ptr(slot), B, T, _ptr(share), _stream(stream)),
+           "rssm_kv_share")
+
+
+def rssm_attn_decode_shared(handle, layer, q, q_stride, slot, B, T, share, o, lse, stream=None):
+    _check(load().rssm_attn_decode_shared(handle, layer, _ptr(q), q_stride, _ptr(slot), B, T,
+                                          _ptr(share), _ptr(o), _ptr(lse), _stream(stream)),
+           "rssm_attn_decode_shared")
 
 
 def rssm_attn_prefill(handle, q, k, v, q_stride, k_stride, v_stride, cu_seqlens, cu_keys, slot,

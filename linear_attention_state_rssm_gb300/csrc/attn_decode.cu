@@ -65,4 +65,29 @@ cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, i
                              : plain(&p, maps, D, dt, mw, sms, st);
 }
 
+// Shared prefixes: a stream of one warp where all the batch's query rows of a key
+// head are sixteen at most, else of as many as there are.
+cudaError_t attn_shared_prepare(int D, int dt, bool quant) {
+  const cudaError_t e = quant ? attn_shared_prefix_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
+                              : attn_shared_prefix(nullptr, nullptr, D, dt, 0, 0, nullptr);
+  if (e != cudaSuccess) return e;
+  return quant ? attn_shared_own_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
+               : attn_shared_own(nullptr, nullptr, D, dt, 0, 0, nullptr);
+}
+
+cudaError_t attn_shared_launch(DecodeParams p, const void* maps, int D, int dt, int num_sms,
+                               cudaStream_t st) {
+  const int sms = num_sms < kMaxSms ? num_sms : kMaxSms;
+  const bool quant = p.scales != nullptr;
+  const int most = dt == DT_F32 ? 1 : D == 256 ? 3 : 4;
+  const int all = (long long)p.B * p.T * p.G <= 16 ? 1 : most;
+  const int own = p.T * p.G <= 16 ? 1 : most;
+  const cudaError_t e = quant ? attn_shared_prefix_quant(&p, maps, D, dt, all, sms, st)
+                              : attn_shared_prefix(&p, maps, D, dt, all, sms, st);
+  if (e != cudaSuccess) return e;
+  p.nmb = (p.T * p.G + 16 * own - 1) / (16 * own);
+  return quant ? attn_shared_own_quant(&p, maps, D, dt, own, sms, st)
+               : attn_shared_own(&p, maps, D, dt, own, sms, st);
+}
+
 }  // namespace rssm

@@ -91,6 +91,16 @@ struct DecCfg {
   static_assert(CPS * kMaxSms * 2 * PART <= kPartFloats, "work buffer");
 };
 
+// Slot whose table stands for those of all of a group's members: the first that
+// is still in use; -1 where none is.
+__device__ __forceinline__ int lead_slot(const DecodeParams& p, int group) {
+  for (int i = p.share.begin[group]; i < p.share.begin[group + 1]; ++i) {
+    const int s = p.slot[p.share.order[i]];
+    if (s >= 0 && s < p.n_slots) return s;
+  }
+  return -1;
+}
+
 // keys of row r (committed and new), 0 for a null or refused row; for PREFIX the
 // shared keys of group r. start: the first key that the row reads here.
 template <int MODE>
@@ -98,8 +108,10 @@ __device__ __forceinline__ int row_keys(const DecodeParams& p, int r, bool tell,
                                         int& start) {
   start = 0;
   if constexpr (MODE == DEC_PREFIX) {
-    s = r;
+    s = -1;
     if (!share_is_of(p.share, p.B, p.T) || r >= *p.share.groups) return 0;
+    s = lead_slot(p, r);
+    if (s < 0) return 0;
     const int keys = p.share.group_keys[r], most = p.max_pages << p.shift;
     return keys < most ? keys : most;
   } else {
@@ -250,21 +262,12 @@ __device__ __forceinline__ long long query_token(const DecodeParams& p, int r, i
   }
 }
 
-// Slot of a group's first member, whose table stands for all of theirs. A null
-// or bad slot (the call's slots are not the plan's) is replaced by slot 0: OWN
-// compares the tables and skips the rows that are not served by it.
-__device__ __forceinline__ int lead_slot(const DecodeParams& p, int r) {
-  const int s = p.slot[p.share.order[p.share.begin[r]]];
-  return s < 0 || s >= p.n_slots ? 0 : s;
-}
-
 // Whether the row's pages up to its prefix's end are those that the group's keys
 // were read from (the plan may be older than the tables), and were read.
 template <int THREADS>
 __device__ __forceinline__ bool prefix_holds(const DecodeParams& p, const Seg& sg, int tid) {
   bool same = *p.share.lost == 0;
-  const int lead = p.slot[p.share.lead[sg.row]];
-  if (lead < 0 || lead >= p.n_slots) return false;
+  const int lead = lead_slot(p, p.share.group[sg.row]);
   const int32_t* a = p.table + (size_t)sg.slot * p.max_pages;
   const int32_t* b = p.table + (size_t)lead * p.max_pages;
   const int n = sg.start >> p.shift;
@@ -449,9 +452,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
       cp_async_arrive(&qfull[half]);
       ++ns;
       if (!sg.more) break;
-      int slot = sg.slot;
-      if constexpr (MODE == DEC_PREFIX) slot = lead_slot(p, sg.row);
-      const int32_t* tab = p.table + (size_t)slot * p.max_pages;
+      const int32_t* tab = p.table + (size_t)sg.slot * p.max_pages;
       // the boxes of the segment's chunks, 32 looked up at a time
       constexpr int BPC = C::CH / kBox;  // boxes of a chunk
       const int b_end = min(sg.c1 * BPC, (sg.keys - sg.start + kBox - 1) / kBox);

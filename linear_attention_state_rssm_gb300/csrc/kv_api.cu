@@ -96,6 +96,7 @@ rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, v
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = attn_decode_prepare(cfg->D, cfg->dtype, scales != nullptr);
+  if (e == cudaSuccess) e = attn_shared_prepare(cfg->D, cfg->dtype, scales != nullptr);
   if (e == cudaSuccess) e = attn_prompt_prepare(cfg->D, cfg->dtype);
   if (e == cudaSuccess)
     e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
@@ -161,6 +162,41 @@ rssm_status copy_pages(const rssm_kv_handle* h, const PageParams& p, bool remap,
   c.n_layers = h->cfg.n_layers;
   c.n_pages = h->cfg.n_pages;
   return from_cuda(kv_copy_launch(c, h->num_sms, st));
+}
+
+// Parameters of attention over the pages but for its blocks of rows.
+DecodeParams decode_params(const rssm_kv_handle* h, int32_t layer, const void* q, int64_t q_stride,
+                           const int32_t* slot, int32_t B, int32_t T, void* o, float* lse) {
+  const rssm_kv_config& c = h->cfg;
+  const KvWork w(c.n_pages);
+  char* work = static_cast<char*>(h->buf.work);
+  DecodeParams p{};
+  p.q = q;
+  p.scales = h->scales;
+  p.slot = slot;
+  p.table = h->buf.table;
+  p.held = h->buf.held;
+  p.length = h->buf.length;
+  p.o = o;
+  p.lse = lse;
+  p.page0 = (long long)layer * c.n_pages;
+  p.part = reinterpret_cast<float*>(work + w.part);
+  p.count = reinterpret_cast<int32_t*>(work + w.count);
+  p.err = h->buf.err_word;
+  p.qs = q_stride;
+  p.B = B;
+  p.T = T;
+  p.HQ = c.HQ;
+  p.HKV = c.HKV;
+  p.G = c.HQ / c.HKV;
+  p.n_slots = c.n_slots;
+  p.n_pages = c.n_pages;
+  p.max_pages = c.max_pages;
+  p.shift = h->shift;
+  p.hook_cta = h->hook_cta;
+  p.hook_unit = h->hook_unit;
+  p.c = (float)((double)c.scale * 1.4426950408889634);
+  return p;
 }
 
 }  // namespace
@@ -414,39 +450,54 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   if (B == 0) return RSSM_OK;
   if (!tokens_ok(c, q, q_stride, c.HQ) || o == nullptr || !aligned16(o) || !aligned4(lse))
     return RSSM_ERR_INVALID_ARG;
-  const KvWork w(c.n_pages);
-  char* work = static_cast<char*>(h->buf.work);
-  DecodeParams p{};
-  p.q = q;
-  p.scales = h->scales;
-  p.slot = slot;
-  p.table = h->buf.table;
-  p.held = h->buf.held;
-  p.length = h->buf.length;
-  p.o = o;
-  p.lse = lse;
-  p.page0 = (long long)layer * c.n_pages;
-  p.part = reinterpret_cast<float*>(work + w.part);
-  p.count = reinterpret_cast<int32_t*>(work + w.count);
-  p.err = h->buf.err_word;
-  p.qs = q_stride;
-  p.B = B;
-  p.T = T;
-  p.HQ = c.HQ;
-  p.HKV = c.HKV;
-  p.G = c.HQ / c.HKV;
-  p.n_slots = c.n_slots;
-  p.n_pages = c.n_pages;
-  p.max_pages = c.max_pages;
-  p.shift = h->shift;
+  DecodeParams p = decode_params(h, layer, q, q_stride, slot, B, T, o, lse);
   const int rows = attn_decode_block_rows(c.D, c.dtype, T * p.G);
   p.nmb = (T * p.G + rows - 1) / rows;
-  p.hook_cta = h->hook_cta;
-  p.hook_unit = h->hook_unit;
-  p.c = (float)((double)c.scale * 1.4426950408889634);
   return from_cuda(
-      attn_decode_launch(p, h->maps, c.D, c.dtype, h->num_sms,
-                                     static_cast<cudaStream_t>(stream)));
+      attn_decode_launch(p, h->maps, c.D, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+rssm_status rssm_kv_share_bytes(const rssm_kv_config* cfg, int32_t B, int32_t T, size_t* out) {
+  const rssm_status st = check_config(cfg);
+  if (st != RSSM_OK) return st;
+  if (out == nullptr || B < 0 || B > kMaxRows || T < 1) return RSSM_ERR_INVALID_ARG;
+  if (T > 64) return RSSM_ERR_UNSUPPORTED;
+  *out = ShareView::lay(nullptr, B, T, cfg->HQ, cfg->D, nullptr);
+  return RSSM_OK;
+}
+
+rssm_status rssm_kv_share(rssm_kv_handle* h, const int32_t* slot, int32_t B, int32_t T,
+                          void* share, void* stream) {
+  const rssm_status st = check_rows(h, slot, B);
+  if (st != RSSM_OK) return st;
+  if (T < 1 || share == nullptr || !aligned16(share)) return RSSM_ERR_INVALID_ARG;
+  if (T > 64) return RSSM_ERR_UNSUPPORTED;
+  if (B == 0) return RSSM_OK;
+  PageParams p = page_params(h);
+  p.slot = slot;
+  p.B = B;
+  p.T = T;
+  ShareView v;
+  ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.D, &v);
+  return from_cuda(kv_share_launch(v, p, static_cast<cudaStream_t>(stream)));
+}
+
+rssm_status rssm_attn_decode_shared(rssm_kv_handle* h, int32_t layer, const void* q,
+                                    int64_t q_stride, const int32_t* slot, int32_t B, int32_t T,
+                                    void* share, void* o, float* lse, void* stream) {
+  const rssm_status st = check_rows(h, slot, B);
+  if (st != RSSM_OK) return st;
+  const rssm_kv_config& c = h->cfg;
+  if (layer < 0 || layer >= c.n_layers || T < 1) return RSSM_ERR_INVALID_ARG;
+  if (T > 64) return RSSM_ERR_UNSUPPORTED;
+  if (B == 0) return RSSM_OK;
+  if (!tokens_ok(c, q, q_stride, c.HQ) || o == nullptr || !aligned16(o) || !aligned4(lse) ||
+      share == nullptr || !aligned16(share))
+    return RSSM_ERR_INVALID_ARG;
+  DecodeParams p = decode_params(h, layer, q, q_stride, slot, B, T, o, lse);
+  ShareView::lay(share, B, T, c.HQ, c.D, &p.share);
+  return from_cuda(
+      attn_shared_launch(p, h->maps, c.D, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 rssm_status rssm_attn_prefill(rssm_kv_handle* h, const void* q, const void* k, const void* v,

@@ -139,8 +139,8 @@ struct ShareView {
   int32_t* groups;      // [1] their number
   int32_t* lost;        // [1] a wait ran out: the prefixes' outputs are not all there
   int32_t* prefix;      // [B] keys of each row's shared prefix (0: none)
-  int32_t* lead;        // [B] row whose table the group's keys are read by
-  int32_t* order;       // [B] rows, group by group, each group's lead first
+  int32_t* group;       // [B] each row's group (where it has a prefix)
+  int32_t* order;       // [B] rows, group by group
   int32_t* begin;       // [B + 1] first place of a group in order
   int32_t* group_keys;  // [B] keys of a group's prefix
   int32_t* scratch;     // [2 B] of the plan
@@ -160,7 +160,7 @@ struct ShareView {
     ShareView s{};
     char* head = take(16);
     char* prefix = take(b);
-    char* lead = take(b);
+    char* group = take(b);
     char* order = take(b);
     char* begin = take(b + 4);
     char* keys = take(b);
@@ -172,7 +172,7 @@ struct ShareView {
       s.groups = s.of + 2;
       s.lost = s.of + 3;
       s.prefix = reinterpret_cast<int32_t*>(prefix);
-      s.lead = reinterpret_cast<int32_t*>(lead);
+      s.group = reinterpret_cast<int32_t*>(group);
       s.order = reinterpret_cast<int32_t*>(order);
       s.begin = reinterpret_cast<int32_t*>(begin);
       s.group_keys = reinterpret_cast<int32_t*>(keys);
@@ -226,6 +226,7 @@ struct PromptParams {
 };
 
 cudaError_t kv_plan_launch(int mode, const PageParams& p, cudaStream_t st);
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, cudaStream_t st);
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
@@ -241,6 +242,18 @@ cudaError_t attn_decode_quant(const DecodeParams* p, const void* maps, int D, in
 cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st);
 int attn_decode_block_rows(int D, int dt, int rows);  // rows of a block for T G rows
+// the two launches of attention over shared prefixes, and their preparation
+cudaError_t attn_shared_prepare(int D, int dt, bool quant);
+cudaError_t attn_shared_launch(DecodeParams p, const void* maps, int D, int dt, int num_sms,
+                               cudaStream_t st);
+cudaError_t attn_shared_prefix(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                               int sms, cudaStream_t st);
+cudaError_t attn_shared_prefix_quant(const DecodeParams* p, const void* maps, int D, int dt,
+                                     int mw, int sms, cudaStream_t st);
+cudaError_t attn_shared_own(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                            int sms, cudaStream_t st);
+cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                                  int sms, cudaStream_t st);
 cudaError_t attn_prompt_prepare(int D, int dt);
 cudaError_t attn_prompt_launch(const PromptParams& p, cudaStream_t st);
 cudaError_t attn_prompt_tc_prepare(int D, int dt);  // 16-bit types

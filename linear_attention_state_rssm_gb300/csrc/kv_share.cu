@@ -1,0 +1,198 @@
+// Prefixes that rows of a batch share: the plan of a step, made from the page
+// tables once for all layers, and the attention that reads each prefix once for
+// all its rows.
+//
+// A fork leaves a prompt's full pages named by several tables. Rows whose tables
+// begin with the same page form a group; its prefix is as many pages as all of
+// them begin with, among those that every one has committed whole, so all of it
+// is seen by all of the group's query tokens. The softmax of a row is then taken
+// in two parts of its keys, which meet in the running maximum, sum and output
+// (attn_decode.cuh): what the second launch begins with is what the first left.
+//
+// The plan says which rows and how many keys, not which pages: pages may move
+// (all tables follow) and slots grow. Where a table no longer begins with its
+// group's pages the attention sees that, and skips the row.
+#include <climits>
+
+#include "kv_common.cuh"
+
+namespace rssm {
+
+namespace {
+
+constexpr int kShareThreads = 1024;
+
+struct PlanShareParams {
+  ShareView v;
+  const int32_t* slot;
+  const int32_t* table;
+  const int32_t* held;
+  const int32_t* length;
+  int32_t* map;  // [n_pages] of the cache's work buffer
+  int B, T, n_slots, n_pages, max_pages, shift, least;
+};
+
+__device__ __forceinline__ int scan_of(int x, int* sums, int tid, int& total) {
+  const int warp = tid >> 5, lane = tid & 31;
+  int incl = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kFull, incl, d);
+    if (lane >= d) incl += y;
+  }
+  __syncthreads();  // the last call's sums have been read
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int s = sums[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(kFull, s, d);
+    if (lane >= d) s += y;
+  }
+  total = __shfl_sync(kFull, s, 31);
+  return incl - x + (warp > 0 ? __shfl_sync(kFull, s, warp - 1) : 0);
+}
+
+// One CTA. Groups are numbered in the order of their first rows, so that the
+// same tables give the same stretches, and sums, in the attention. Counters are
+// read past the L1 cache, which atomics do not write.
+__global__ void __launch_bounds__(kShareThreads)
+    plan_share_kernel(const __grid_constant__ PlanShareParams p) {
+  __shared__ int sums[32];
+  const int tid = threadIdx.x;
+  int32_t* full = p.v.order;                // whole committed pages, until phase 3
+  int32_t* count = p.v.scratch;             // of a lead: members; then its group
+  int32_t* common = p.v.scratch + p.B;      // of a lead: pages; then the next place
+  if (tid == 0) {
+    p.v.of[0] = p.B;
+    p.v.of[1] = p.T;
+    *p.v.lost = 0;
+  }
+  // ---- 1: each row's whole pages, and the first row that begins with its page
+  auto first_page = [&](int r) {
+    const int s = p.slot[r];
+    if (s < 0 || s >= p.n_slots || full[r] < 1) return -1;
+    const int page = p.table[(size_t)s * p.max_pages];
+    return page >= 0 && page < p.n_pages ? page : -1;
+  };
+  for (int r = tid; r < p.B; r += kShareThreads) {
+    const int s = p.slot[r];
+    int n = 0;
+    if (s >= 0 && s < p.n_slots) {
+      const int len = p.length[s], held = p.held[s];
+      if (len >= 0 && held >= 0 && held <= p.max_pages &&
+          (long long)len + p.T <= ((long long)held << p.shift))
+        n = len >> p.shift;
+    }
+    full[r] = n;
+    count[r] = 0;
+    common[r] = INT_MAX;
+    p.v.prefix[r] = 0;
+    const int page = first_page(r);
+    if (page >= 0) p.map[page] = INT_MAX;
+  }
+  __syncthreads();
+  for (int r = tid; r < p.B; r += kShareThreads) {
+    const int page = first_page(r);
+    if (page >= 0) atomicMin(p.map + page, r);
+  }
+  __syncthreads();
+  // ---- 2: pages in common with the lead, a warp to a row
+  for (int r = tid >> 5; r < p.B; r += kShareThreads / 32) {
+    const int lane = tid & 31, page = first_page(r);
+    const int lead = page >= 0 ? __ldcg(p.map + page) : r;
+    int same = full[r];
+    if (lead != r) {
+      const int n = min(same, full[lead]);
+      const int32_t* a = p.table + (size_t)p.slot[r] * p.max_pages;
+      const int32_t* b = p.table + (size_t)p.slot[lead] * p.max_pages;
+      same = n;
+      for (int i0 = 0; i0 < n; i0 += 128) {
+        bool eq[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = i0 + 32 * k + lane;
+          eq[k] = i >= n || a[i] == b[i];
+        }
+        int at = n;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const unsigned off = __ballot_sync(kFull, !eq[k]);
+          if (off) at = i0 + 32 * k + __ffs(off) - 1;
+        }
+        if (at < n) {
+          same = at;
+          break;
+        }
+      }
+    }
+    if (lane == 0) {
+      p.v.group[r] = lead;  // until phase 4
+      if (page >= 0) {
+        atomicMin(common + lead, same);
+        atomicAdd(count + lead, 1);
+      }
+    }
+  }
+  __syncthreads();
+  // ---- 3: the groups
+  int groups = 0, rows = 0;
+  for (int r0 = 0; r0 < p.B; r0 += kShareThreads) {
+    const int r = r0 + tid;
+    const int n = r < p.B ? __ldcg(count + r) : 0;
+    const int pages = r < p.B ? __ldcg(common + r) : 0;
+    const bool on = n >= 2 && ((long long)pages << p.shift) >= p.least;
+    int all_groups, all_rows;
+    const int g = groups + scan_of(on, sums, tid, all_groups);
+    const int at = rows + scan_of(on ? n : 0, sums, tid, all_rows);
+    if (r < p.B) {
+      if (on) {
+        p.v.begin[g] = at;
+        p.v.group_keys[g] = pages << p.shift;
+        p.v.order[at] = r;
+        common[r] = at + 1;
+        count[r] = g;
+      } else {
+        count[r] = -1;
+      }
+    }
+    groups += all_groups;
+    rows += all_rows;
+  }
+  if (tid == 0) {
+    *p.v.groups = groups;
+    p.v.begin[groups] = rows;
+  }
+  __syncthreads();
+  // ---- 4: their members
+  for (int r = tid; r < p.B; r += kShareThreads) {
+    const int lead = p.v.group[r], g = count[lead];
+    if (g < 0) continue;
+    if (lead != r) p.v.order[atomicAdd(common + lead, 1)] = r;
+    p.v.prefix[r] = p.v.group_keys[g];
+    p.v.group[r] = g;
+  }
+}
+
+}  // namespace
+
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, cudaStream_t st) {
+  PlanShareParams s{};
+  s.v = v;
+  s.slot = p.slot;
+  s.table = p.table;
+  s.held = p.held;
+  s.length = p.length;
+  s.map = p.map;
+  s.B = p.B;
+  s.T = p.T;
+  s.n_slots = p.n_slots;
+  s.n_pages = p.n_pages;
+  s.max_pages = p.max_pages;
+  s.shift = p.shift;
+  s.least = 1;
+  plan_share_kernel<<<1, kShareThreads, 0, st>>>(s);
+  return cudaGetLastError();
+}
+
+}  // namespace rssm

@@ -212,6 +212,15 @@ class HeadNorm:
                                             for w in (q_weight, k_weight)), float(eps))
 
 
+class Share:
+    """A plan of shared prefixes and the attention's room for it (KVCache.new_share)."""
+
+    def __init__(self, cache, B, T):
+        self.cache, self.B, self.T = cache, B, T
+        self.buffer = torch.zeros(_lib.rssm_kv_share_bytes(cache.cfg, B, T), dtype=torch.uint8,
+                                  device=cache.device)
+
+
 class KVCache:
     """Paged keys and values of the full-attention layers, ``n_slots`` requests.
 
@@ -346,6 +355,26 @@ class KVCache:
         self._output(o, B * T, lse)
         _lib.rssm_attn_decode(self.handle, layer, q, qs, slot, B, T, o, lse, stream)
 
+    def new_share(self, B, T=1):
+        """Room for rssm_kv_share's plan of B rows of T tokens; one for each call
+        that may be on its way at a time."""
+        return Share(self, B, T)
+
+    def rssm_kv_share(self, slot, T, share, stream=None):
+        """Which rows share a prefix's pages, into share (once for a step's layers)."""
+        B = self._index(slot)
+        self._shared(share, B, T)
+        _lib.rssm_kv_share(self.handle, slot, B, T, share.buffer, stream)
+
+    def rssm_attn_decode_shared(self, layer, q, slot, T, share, o, lse=None, stream=None):
+        """As rssm_attn_decode, prefixes that rows share read once (rssm_kv_share's plan)."""
+        B = self._index(slot)
+        self._shared(share, B, T)
+        _, qs = self._tokens(q, self.HQ, B * T)
+        self._output(o, B * T, lse)
+        _lib.rssm_attn_decode_shared(self.handle, layer, q, qs, slot, B, T, share.buffer, o, lse,
+                                     stream)
+
     def rssm_attn_prefill(self, q, k, v, cu_seqlens, slot, o, cu_keys=None, lse=None,
                           stream=None):
         """Causal attention over packed prompts (cu_seqlens int32, B + 1)."""
@@ -379,6 +408,10 @@ class KVCache:
             pass
 
     # ------------------------------------------------------------- helpers
+    def _shared(self, share, B, T):
+        if share.cache is not self or share.B != B or share.T != T:
+            raise ValueError(f"share: of this cache, {B} rows and {T} tokens")
+
     @staticmethod
     def _index(x, n=None):
         """Entries of an index tensor; the kernels read it as n int32 in a run

@@ -84,3 +84,30 @@ def test_rows_that_the_kernels_cannot_write_are_refused(kw):
     KVCache._row(kv, "v_out", like((4, 2, 64)), 4)
     with pytest.raises(ValueError):
         KVCache._row(kv, "v_out", like(**{"shape": (4, 2, 64), **kw}), 4)
+
+
+def test_share_buffers(lib):
+    cfg = config()
+    n = _lib.rssm_kv_share_bytes(cfg, 64, 2)
+    out = 64 * 2 * 16 * (128 + 2) * 4
+    assert out <= n <= out + 8 * 64 * 4 + 9 * 256
+    assert _lib.rssm_kv_share_bytes(cfg, 0, 1) >= 16
+    for B, T, status in ((-1, 1, 1), (65536, 1, 1), (4, 0, 1), (4, 65, 2)):
+        with pytest.raises(_lib.RssmError) as e:
+            _lib.rssm_kv_share_bytes(cfg, B, T)
+        assert e.value.status == status
+    for call in (lambda: _lib.rssm_kv_share(None, None, 1, 1, 0x1000, stream=0),
+                 lambda: _lib.rssm_attn_decode_shared(None, 0, None, 0, None, 1, 1, 0x1000, None,
+                                                      None, stream=0)):
+        with pytest.raises(_lib.RssmError) as e:
+            call()
+        assert e.value.status == 1
+
+
+def test_plans_of_other_batches_are_refused():
+    kv = SimpleNamespace()
+    share = SimpleNamespace(cache=kv, B=4, T=2)
+    KVCache._shared(kv, share, 4, 2)
+    for args in ((kv, share, 3, 2), (kv, share, 4, 1), (SimpleNamespace(), share, 4, 2)):
+        with pytest.raises(ValueError):
+            KVCache._shared(*args)
