@@ -143,6 +143,21 @@ struct WarpAttn {
   float o[MB][D / 8][4];
   float m[MB][2], l[MB][2];  // l: this lane's share of the row's sum
 
+  // a lane's rows and pairs of dimensions where MB is 1
+  static constexpr int RL = 2, PAIRS = D / 8, WROWS = 16;
+  static __device__ __forceinline__ int row(int e, int lane) { return 8 * e + (lane >> 2); }
+  static __device__ __forceinline__ int dim(int i, int lane) { return col(i, lane & 3); }
+  static __device__ __forceinline__ bool tells(int lane) { return (lane & 3) == 0; }
+  __device__ __forceinline__ float2 pair(int i, int e) const {
+    return make_float2(o[0][i][2 * e], o[0][i][2 * e + 1]);
+  }
+  __device__ __forceinline__ void set_pair(int i, int e, float2 y) {
+    o[0][i][2 * e] = y.x;
+    o[0][i][2 * e + 1] = y.y;
+  }
+  __device__ __forceinline__ float& top(int e) { return m[0][e]; }
+  __device__ __forceinline__ float& sum(int e) { return l[0][e]; }
+
   // the fragment of the matrix instructions, or whole 16-byte units for fp32
   static __device__ __forceinline__ int col(int i, int t) {
     return F32 ? 16 * (i >> 1) + 4 * t + 2 * (i & 1) : 8 * i + 2 * t;

@@ -53,27 +53,40 @@ namespace {
 enum : int { DEC_PLAIN = 0, DEC_PREFIX = 1, DEC_OWN = 2 };
 
 constexpr int kBox = 16;        // keys of a TMA box: within one page (pages of 16 k keys)
+constexpr int kQuantBox = 32;   // rows of a column of quantised keys: a box's, or two of kBox's
 constexpr int kGapKeys = 256;   // what beginning and ending a row costs, as keys
 constexpr int kLeastKeys = 512; // keys that a CTA takes at least (of longer rows)
 constexpr int kRowParts = 96;   // parts of the longest row, about: one CTA joins them
 constexpr int kLostPart = 1 << 16;  // in a row's arrivals, beside their number: a part that is not there
 
-template <typename T, int D, int MW, bool Q>
+// Streams of MW warps; quantised pages: of 8 NQ rows a warp, else of 16 (NQ 0).
+template <typename T, int D, int MW, int NQ>
 struct DecCfg {
+  static constexpr bool Q = NQ > 0;
+  using Warp = std::conditional_t<Q, WarpAttnQuant<D, NQ, 8 * NQ * MW, kQuantBox>,
+                                  WarpAttn<T, D, 1, 16 * MW, kBox>>;
   static constexpr bool F32 = std::is_same<T, float>::value;
   // Outputs live in registers, D / 2 a lane: seven warps of 255 registers for
   // D = 256, ten of 168 for 128, fifteen of 128 for 64 (eight of 255 for fp32,
   // whose FMAs want more). A quarter of the registers belongs to each quarter
   // of the SM. Where they suffice a step takes 32 keys: what a step costs
   // whatever its size (waits, maxima over lanes) is most of it.
-  static constexpr int CPS = D == 256 ? 1 : F32 || D == 128 ? 2 : 3;  // CTAs per SM
-  static constexpr int NW = F32 ? (D == 256 ? 4 : 3) : D == 256 ? 6 : 4;
+  // Quantised pages, eight rows a warp: half the outputs, and more warps. More
+  // than five in a CTA leave too little of the ring on its way (128: seven 92 us
+  // for two rows of 109 to 131 k tokens instead of 89; one CTA of nine 104).
+  static constexpr int CPS = NQ == 1    ? (D == 64 ? 3 : 2)
+                             : D == 256 ? 1
+                             : F32 || D == 128 ? 2
+                                               : 3;  // CTAs per SM
+  static constexpr int NW = F32 ? (D == 256 ? 4 : 3) : NQ == 1 ? 5 : D == 256 ? 6 : 4;
   static constexpr int CH = F32 || (D == 256 && !Q) ? 16 : 32;  // keys of a chunk
+  static constexpr int GRP = D == 256 ? 2 : 4;         // chunks that are sent for together
   static constexpr int GAP = kGapKeys / CH;
   static constexpr int CT = NW * 32;                   // threads of the streams
   static constexpr int NT = CT + 32;                   // and the producer warp
   static constexpr int NG = NW / MW;                   // streams of a CTA
-  static constexpr int ROWS = 16 * MW;
+  static constexpr int WROWS = Warp::WROWS;            // rows of a warp
+  static constexpr int ROWS = WROWS * MW;
   static constexpr int UNIT = CH * D * (Q ? 1 : (int)sizeof(T));
   static constexpr int SCALES = Q ? CH * 2 : 0;        // of a chunk
   static constexpr int QBYTES = ROWS * D * (int)sizeof(T);
@@ -87,8 +100,9 @@ struct DecCfg {
   static constexpr int NU = FIT < 32 ? FIT : 32;       // units in the ring
   static constexpr int SMEM = NU * (UNIT + SCALES) + REST;
   static constexpr int PART = ROWS * (D + 2);          // floats of a part
-  static_assert(NU >= 2 * NG, "a chunk for each stream");
+  static_assert(NU >= 2 * NG && NU >= 2 * GRP, "a chunk for each stream, and a group of them");
   static_assert(CPS * kMaxSms * 2 * PART <= kPartFloats, "work buffer");
+  static_assert(CPS * kMaxSms <= kMaxParts, "arrivals");
 };
 
 // Slot whose table stands for those of all of a group's members: the first that
@@ -291,11 +305,13 @@ __device__ __forceinline__ bool named_any(int id, int count, bool x) {
   return any != 0;
 }
 
-template <typename T, int D, int MW, bool Q, int MODE>
-__global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::CPS)
+template <typename T, int D, int MW, int NQ, int MODE>
+__global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>::CPS)
     attn_decode_kernel(const __grid_constant__ DecodeParams p,
                        const __grid_constant__ KvMaps maps) {
-  using C = DecCfg<T, D, MW, Q>;
+  using C = DecCfg<T, D, MW, NQ>;
+  using W = typename C::Warp;
+  constexpr bool Q = NQ > 0;
   using Stretch = Line<C::CH, MODE, C::ROWS>;
   constexpr int NG = C::NG, NW = C::NW;
   extern __shared__ unsigned char sm_raw[];
@@ -429,7 +445,8 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
       if (ns >= 2) dead = !mbar_wait_bounded(&qempty[half], (uint32_t)((ns / 2 - 1) & 1));
       dead = __any_sync(kFull, dead);
       if (dead) break;
-      if (lane == 1) {  // lane 0 has bulk copies on their way, which a release would wait for
+      // a lane without bulk copies on their way, which a release would wait for
+      if (lane == (MODE != DEC_PLAIN || Q ? 31 : 1)) {
         segs[half] = sg;
         mbar_arrive(&qfull[half]);
       }
@@ -470,7 +487,67 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
                       (tok & ((1 << p.shift) - 1)));
         }
         const int cnt = min(32 / BPC, sg.c1 - cb);
-        for (int i = 0; i < cnt; ++i) {
+        // Copies go out from lanes side by side, a group of chunks at a time: lane u
+        // sees to it that the group's u-th place in the ring is free and says what
+        // will land there, then each sends for one copy. From one lane, chunk by
+        // chunk, the six copies of a quantised chunk in boxes of sixteen took 1300
+        // cycles, twice what their bytes take; from several, with boxes of 32, 865;
+        // in groups of four chunks 430 (two rows of 109 to 131 k tokens: 143, 107,
+        // 89 us).
+        constexpr int GRP = C::GRP;
+        for (int i = 0; i < cnt && (MODE != DEC_PLAIN || Q); i += GRP) {
+          const int units = 2 * min(GRP, cnt - i);
+          const int u = 2 * n + lane, at_u = u % C::NU;
+          if (lane < units && u >= C::NU)
+            dead = !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1));
+          dead = __any_sync(kFull, dead);
+          if (dead) {
+            if (lane == 0) *stop = 2 * n;
+            break;
+          }
+          if (lane < units)
+            mbar_expect_tx(&full[at_u], C::UNIT + (lane % 2 == 0 ? C::SCALES : 0));
+          __syncwarp();
+          if (lane == 0) *issued = 2 * n + units;
+          // boxes of the chunk of this lane's unit; one behind the last key is not
+          // loaded: the one before it stands in its place, and no row sees it
+          const int c = i + lane / 2;  // its chunk
+          int at_row[BPC];
+#pragma unroll
+          for (int b = 0; b < BPC; ++b) at_row[b] = __shfl_sync(kFull, row, (c * BPC + b) & 31);
+#pragma unroll
+          for (int b = 1; b < BPC; ++b) at_row[b] = at_row[b] >= 0 ? at_row[b] : at_row[0];
+          unsigned char* to = ring + at_u * C::UNIT;
+          const CUtensorMap* map = lane % 2 == 0 ? &maps.k : &maps.v;
+          if constexpr (Q) {
+            static_assert(C::CH == kQuantBox, "one box of a page of 32 tokens or more");
+            if (p.shift >= 5) {
+              if (lane < units) tma_load3(smem_addr(to), map, 0, at_row[0], 0, &full[at_u]);
+              if (lane < units && lane % 2 == 0)
+                bulk_g2s(ring_scales + at_u * C::SCALES, p.scales + 2 * (size_t)at_row[0],
+                         C::SCALES, &full[at_u]);
+            } else if (lane < units) {
+              constexpr int COLS = D == 256 ? 2 : 1;  // columns of 128 bytes (64: of 64)
+#pragma unroll
+              for (int b = 0; b < BPC; ++b) {
+#pragma unroll
+                for (int col = 0; col < COLS; ++col)
+                  tma_load3(smem_addr(to + col * (kQuantBox * 128) + b * (C::UNIT / COLS / 2)), map,
+                            0, at_row[b], col, &full[at_u]);
+                if (lane % 2 == 0)
+                  bulk_g2s(ring_scales + at_u * C::SCALES + b * (2 * kBox),
+                           p.scales + 2 * (size_t)at_row[b], 2 * kBox, &full[at_u]);
+              }
+            }
+          } else if (lane < units) {
+#pragma unroll
+            for (int b = 0; b < BPC; ++b)
+              tma_load3(smem_addr(to + b * (C::UNIT / BPC)), map, 0, at_row[b], 0, &full[at_u]);
+          }
+          __syncwarp();
+          n += units / 2;
+        }
+        for (int i = 0; i < cnt && MODE == DEC_PLAIN && !Q; ++i) {
           int at_row[BPC];
 #pragma unroll
           for (int b = 0; b < BPC; ++b) at_row[b] = __shfl_sync(kFull, row, i * BPC + b);
@@ -487,19 +564,12 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
                   !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1)))
                 dead = true, *stop = u;
               if (!dead) {
-                mbar_expect_tx(&full[at_u], C::UNIT + (kv == 0 ? C::SCALES : 0));
+                mbar_expect_tx(&full[at_u], C::UNIT);
 #pragma unroll
                 for (int b = 0; b < BPC; ++b)
                   tma_load3(smem_addr(ring + at_u * C::UNIT + b * (C::UNIT / BPC)),
                             kv == 0 ? &maps.k : &maps.v, 0, at_row[b < boxes ? b : 0], 0,
                             &full[at_u]);
-                if constexpr (Q) {
-#pragma unroll
-                  for (int b = 0; b < (kv == 0 ? BPC : 0); ++b)
-                    bulk_g2s(ring_scales + at_u * C::SCALES + b * (2 * kBox),
-                             p.scales + 2 * (size_t)at_row[b < boxes ? b : 0], 2 * kBox,
-                             &full[at_u]);
-                }
               }
             }
             if (!dead) *issued = 2 * n + 2;
@@ -525,8 +595,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
   }
 
   // ---- streams
-  const int grp = warp / MW, wr = 16 * (warp % MW);  // the warp's stream, its first row
-  const int g = lane >> 2, tq = lane & 3;
+  const int grp = warp / MW, wr = C::WROWS * (warp % MW);  // the warp's stream, its first row
   int n0 = 0;    // the segment's first chunk among the CTA's
   int seen = 0;  // units known to be on their way
   for (int ns = 0;; ++ns) {
@@ -547,17 +616,17 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
     const int R = min(C::ROWS, query_rows<MODE>(p, sg.row) - base);  // rows in use
     // how many keys the lane's rows see
     const int first = sg.keys - p.T;  // committed keys
-    int lim[1][2];
+    int lim[W::RL];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
-      lim[0][e] = MODE == DEC_PREFIX ? sg.keys
-                                     : first + (base + min(wr + 8 * e + g, R - 1)) / p.G + 1;
+    for (int e = 0; e < W::RL; ++e)
+      lim[e] = MODE == DEC_PREFIX ? sg.keys
+                                  : first + (base + min(wr + W::row(e, lane), R - 1)) / p.G + 1;
     const int fewest =
         MODE == DEC_PREFIX ? sg.keys : first + (base + min(wr, R - 1)) / p.G + 1;
-    std::conditional_t<Q, WarpAttnQuant<D, C::ROWS, kBox>, WarpAttn<T, D, 1, C::ROWS, kBox>> w;
+    W w;
     w.clear();
     const unsigned char* qw = qs + half * C::QBYTES + wr * 128;
-    [[maybe_unused]] float rf[2];
+    [[maybe_unused]] float rf[W::RL];
     if constexpr (Q) {
       // the block's queries as fp16, each row by a power of two of its own
       constexpr int L = D / 16;
@@ -567,7 +636,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
       }
       named_sync(1, C::CT);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) rf[e] = row_f[half * C::ROWS + wr + 8 * e + g];
+      for (int e = 0; e < W::RL; ++e) rf[e] = row_f[half * C::ROWS + wr + W::row(e, lane)];
     }
     auto out_row = [&](int rr) {
       const int tr = base + rr;
@@ -582,23 +651,19 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
         // the first stream goes on from where the prefix ended
         if (grp == 0 && !skip) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int rr = wr + 8 * e + g;
+          for (int e = 0; e < W::RL; ++e) {
+            const int rr = wr + W::row(e, lane);
             if (rr < R) {
               const size_t at = out_row(rr);
               const float2 ml = p.share.ml[at];
-              w.m[0][e] = ml.x;
-              w.l[0][e] = tq == 0 ? ml.y : 0.f;
+              w.top(e) = ml.x;
+              w.sum(e) = W::tells(lane) ? ml.y : 0.f;
               const float* from = p.share.o + at * D;
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                const float2 y = *reinterpret_cast<const float2*>(from + w.col(i, tq));
-                w.o[0][i][2 * e] = y.x;
-                w.o[0][i][2 * e + 1] = y.y;
-              }
+              for (int i = 0; i < W::PAIRS; ++i)
+                w.set_pair(i, e, *reinterpret_cast<const float2*>(from + W::dim(i, lane)));
             }
           }
-          if constexpr (Q) w.ordered();  // as the products leave them
         }
       }
     }
@@ -620,20 +685,25 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
     for (int i = (grp + NG - n0 % NG) % NG; i < nc && !dead; i += NG) {
       const int key0 = sg.start + (sg.c0 + i) * C::CH, u = 2 * (n0 + i);
       const int uk = u % C::NU, uv = (u + 1) % C::NU;
-      float x[1][C::CH / 8][4];
       dead = !landed(u);
+      std::conditional_t<Q, float[C::CH / 16][Q ? NQ : 1][4], float[1][C::CH / 8][4]> x;
+      [[maybe_unused]] int lim1[1][2] = {{lim[0], lim[1]}};
       if constexpr (Q) {
-        w.template weights<C::CH / 8>(x, qw, ring + uk * C::UNIT, ring_scales + uk * C::SCALES,
-                                      key0, lim, fewest, rf, lane);
+        w.template weights<C::CH / 16>(x, qw, ring + uk * C::UNIT, ring_scales + uk * C::SCALES,
+                                       key0, lim, fewest, rf, lane);
       } else {
-        w.template weights<C::CH / 8>(x, qw, ring + uk * C::UNIT, key0, lim, fewest, p.c, lane);
+        w.template weights<C::CH / 8>(x, qw, ring + uk * C::UNIT, key0, lim1, fewest, p.c, lane);
       }
       __syncwarp();
       // A unit that was not seen to land is not given back: the producer would
       // fill a slot, and arm a barrier, whose last copy is still on its way.
       if (lane == 0 && !dead) mbar_arrive(&empty[uk]);
       dead |= !landed(u + 1);
-      w.template add<C::CH / 8>(x, ring + uv * C::UNIT, key0, lim, fewest, lane);
+      if constexpr (Q) {
+        w.template add<C::CH / 16>(x, ring + uv * C::UNIT, key0, lim, fewest, lane);
+      } else {
+        w.template add<C::CH / 8>(x, ring + uv * C::UNIT, key0, lim1, fewest, lane);
+      }
       dead = __any_sync(kFull, dead);
       if (lane == 0 && !dead) mbar_arrive(&empty[uv]);
     }
@@ -646,34 +716,34 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
     const bool whole = sg.c0 == 0 && sg.c1 == sg.chunks;
     const bool head = sg.item0 < begin;  // the row began in an earlier CTA
     float* part = p.part + (size_t)(2 * blockIdx.x + (head ? 0 : 1)) * C::PART;
-    float f[2], inv[2];
+    float f[W::RL], inv[W::RL];
     if constexpr (NG > 1) {
-      if (tq == 0) {
+      if (W::tells(lane)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sm_m[grp * C::ROWS + wr + 8 * e + g] = w.m[0][e];
-          sm_l[grp * C::ROWS + wr + 8 * e + g] = w.l[0][e];
+        for (int e = 0; e < W::RL; ++e) {
+          sm_m[grp * C::ROWS + wr + W::row(e, lane)] = w.top(e);
+          sm_l[grp * C::ROWS + wr + W::row(e, lane)] = w.sum(e);
         }
       }
       named_sync(1, C::CT);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = wr + 8 * e + g;
-      float mx = w.m[0][e], sum = w.l[0][e];
+    for (int e = 0; e < W::RL; ++e) {
+      const int rr = wr + W::row(e, lane);
+      float mx = w.top(e), sum = w.sum(e);
       f[e] = 1.f;
       if constexpr (NG > 1) {
 #pragma unroll
         for (int k = 0; k < NG; ++k) mx = fmaxf(mx, sm_m[k * C::ROWS + rr]);
         const float mu = mx == kNegInf ? 0.f : mx;
-        f[e] = exp2_fast(w.m[0][e] - mu);
+        f[e] = exp2_fast(w.top(e) - mu);
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k)
           sum += sm_l[k * C::ROWS + rr] * exp2_fast(sm_m[k * C::ROWS + rr] - mu);
       }
       inv[e] = 1.f / sum;
-      if (grp == 0 && tq == 0 && rr < R) {
+      if (grp == 0 && W::tells(lane) && rr < R) {
         row_l[rr] = inv[e];
         if (!whole) {
           part[C::ROWS * D + rr] = mx;
@@ -687,21 +757,22 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
     }
     if constexpr (NG == 1) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = wr + 8 * e + g;
+      for (int e = 0; e < W::RL; ++e) {
+        const int rr = wr + W::row(e, lane);
         if (rr < R && !dead && !(skip && whole)) {
           const size_t at = out_row(rr) * D;
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const float a = w.o[0][i][2 * e], b = w.o[0][i][2 * e + 1];
+          for (int i = 0; i < W::PAIRS; ++i) {
+            const auto [a, b] = w.pair(i, e);
+            const int d = W::dim(i, lane);
             if (whole) {
               if constexpr (MODE == DEC_PREFIX) {
-                *reinterpret_cast<float2*>(p.share.o + at + w.col(i, tq)) = make_float2(a, b);
+                *reinterpret_cast<float2*>(p.share.o + at + d) = make_float2(a, b);
               } else {
-                store2(static_cast<T*>(p.o) + at + w.col(i, tq), a * inv[e], b * inv[e]);
+                store2(static_cast<T*>(p.o) + at + d, a * inv[e], b * inv[e]);
               }
             } else {
-              *reinterpret_cast<float2*>(part + rr * D + w.col(i, tq)) = make_float2(a, b);
+              *reinterpret_cast<float2*>(part + rr * D + d) = make_float2(a, b);
             }
           }
         }
@@ -710,14 +781,15 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
 #pragma unroll
       for (int s = 0; s < D / 64; ++s) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int rr = wr + 8 * e + g;
+        for (int e = 0; e < W::RL; ++e) {
+          const int rr = wr + W::row(e, lane);
           if (rr < R) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float2*>(os + (grp * C::ROWS + rr) * C::OP + w.col(i, tq)) =
-                  make_float2(w.o[0][8 * s + i][2 * e] * f[e],
-                              w.o[0][8 * s + i][2 * e + 1] * f[e]);
+            for (int i = 0; i < W::PAIRS * 64 / D; ++i) {
+              const float2 y = w.pair(W::PAIRS * 64 / D * s + i, e);
+              *reinterpret_cast<float2*>(os + (grp * C::ROWS + rr) * C::OP + W::dim(i, lane)) =
+                  make_float2(y.x * f[e], y.y * f[e]);
+            }
           }
         }
         named_sync(1, C::CT);
@@ -872,44 +944,51 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, Q>::NT, DecCfg<T, D, MW, Q>::
 
 // The kernels of one page type, by head size and warps of a stream: launches, or,
 // with p null, only asks for their shared memory.
-template <typename T, bool Q, int MODE, int D, int MW>
+template <typename T, int NQ, int MODE, int D, int MW>
 cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStream_t st) {
-  using C = DecCfg<T, D, MW, Q>;
-  const auto kernel = attn_decode_kernel<T, D, MW, Q, MODE>;
+  using C = DecCfg<T, D, MW, NQ>;
+  const auto kernel = attn_decode_kernel<T, D, MW, NQ, MODE>;
   if (p == nullptr)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   kernel<<<C::CPS * sms, C::NT, C::SMEM, st>>>(*p, *static_cast<const KvMaps*>(maps));
   return cudaGetLastError();
 }
 
+// The kernel for blocks of `rows` query rows (attn_decode_block_rows).
 template <typename T, bool Q, int MODE, int D>
-cudaError_t decode_of_size(const DecodeParams* p, const void* maps, int mw, int sms,
+cudaError_t decode_of_size(const DecodeParams* p, const void* maps, int rows, int sms,
                            cudaStream_t st) {
-  constexpr int MOST = D == 256 ? 3 : 4;
   const bool all = p == nullptr;
-  cudaError_t e = cudaErrorInvalidValue;
-  if (all || mw == 1) {
-    e = decode_one<T, Q, MODE, D, 1>(p, maps, sms, st);
-    if (!all || e != cudaSuccess) return e;
+  cudaError_t e = all ? cudaSuccess : cudaErrorInvalidValue;
+#define RSSM_ROWS(NQ, MW)                                                    \
+  if (e == cudaSuccess || !all) {                                           \
+    if (all || rows == DecCfg<T, D, MW, NQ>::ROWS) {                         \
+      e = decode_one<T, NQ, MODE, D, MW>(p, maps, sms, st);                  \
+      if (!all) return e;                                                    \
+    }                                                                        \
   }
-  if constexpr (!std::is_same<T, float>::value) {
-    if constexpr (MODE == DEC_PLAIN) {
-      if (all || mw == 2) {
-        e = decode_one<T, Q, MODE, D, 2>(p, maps, sms, st);
-        if (!all || e != cudaSuccess) return e;
-      }
+  if constexpr (Q) {
+    RSSM_ROWS(1, 1)
+    RSSM_ROWS(2, 1)
+    RSSM_ROWS(2, 2)
+    if constexpr (D == 256) { RSSM_ROWS(2, 3) } else { RSSM_ROWS(2, 4) }
+  } else {
+    RSSM_ROWS(0, 1)
+    if constexpr (!std::is_same<T, float>::value) {
+      if constexpr (MODE == DEC_PLAIN) { RSSM_ROWS(0, 2) }
+      if constexpr (D == 256) { RSSM_ROWS(0, 3) } else { RSSM_ROWS(0, 4) }
     }
-    if (all || mw == MOST) e = decode_one<T, Q, MODE, D, MOST>(p, maps, sms, st);
   }
+#undef RSSM_ROWS
   return e;
 }
 
 template <typename T, bool Q, int MODE>
-cudaError_t decode_any(const DecodeParams* p, const void* maps, int D, int mw, int sms,
+cudaError_t decode_any(const DecodeParams* p, const void* maps, int D, int rows, int sms,
                        cudaStream_t st) {
-  if (D == 64) return decode_of_size<T, Q, MODE, 64>(p, maps, mw, sms, st);
-  if (D == 128) return decode_of_size<T, Q, MODE, 128>(p, maps, mw, sms, st);
-  if (D == 256) return decode_of_size<T, Q, MODE, 256>(p, maps, mw, sms, st);
+  if (D == 64) return decode_of_size<T, Q, MODE, 64>(p, maps, rows, sms, st);
+  if (D == 128) return decode_of_size<T, Q, MODE, 128>(p, maps, rows, sms, st);
+  if (D == 256) return decode_of_size<T, Q, MODE, 256>(p, maps, rows, sms, st);
   return cudaErrorInvalidValue;
 }
 

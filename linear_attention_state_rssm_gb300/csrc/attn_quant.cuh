@@ -1,5 +1,5 @@
-// One warp's share of softmax attention over quantised pages: sixteen query
-// rows against a chunk of e4m3 keys and values in shared memory, each key's and
+// One warp's share of softmax attention over quantised pages: 8 NQ query rows
+// against a chunk of e4m3 keys and values in shared memory, each key's and
 // value's power of two beside them (kv_tokens.cuh).
 //
 //     x_ij = c 2^(a_i) 2^(e_j) (q'_i . k'_j)     q' = q 2^-a_i in fp16, k' the codes
@@ -20,12 +20,19 @@
 // p <= 2^(14 + 64). o and l refer to one m, so streams and parts join as those of
 // other pages.
 //
+// The products are transposed, S' = K q' and O' = V' P': the sixteen rows of an
+// instruction are keys, or dimensions, all of them of use, and its eight columns
+// queries, of which a single token has few. A code is converted once whatever
+// the number of queries is. (With queries as the rows, sixteen for four in use,
+// 56 rows of 1 to 8 k tokens, 16/4 heads of 256, took 100 us; so 73.)
+//
 // Eight-bit matrices are loaded as if they were of 16-bit pairs. A lane's word of
 // keys is then four neighbouring dimensions of one key, which serve as k = 2t,
 // 2t + 1, 2t + 8, 2t + 9 of a product (q lies permuted to match); a word of
 // values, transposed, is two dimensions of two neighbouring keys: one permutation
-// of bytes parts it into the even and the odd dimension's pair. Of the outputs a
-// lane holds dimensions 16 j + 4 t + {0, 2} in o[2 j] and {1, 3} in o[2 j + 1].
+// of bytes parts it into the even and the odd dimension's pair, rows g and g + 8
+// of the instruction. Weights come out as [key][query] and go in as [query][key]
+// by way of movmatrix.
 //
 // Keys that a row must not see are left out by selection as in attn_core.cuh; the
 // code NaN is looked for where other pages' infinities and NaN are.
@@ -86,122 +93,152 @@ __device__ __forceinline__ float scale_query(unsigned char* qs, int row, int par
   return power_of(a);
 }
 
-template <int D, int QR, int KR>
-struct WarpAttnQuant {
-  float o[1][D / 8][4];
-  float m[1][2], l[1][2];  // l: this lane's share of the row's sum
+// The transpose of an 8x8 matrix of 16-bit values (rows by lanes' fours).
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
-  // dimension of value e of o[i] for rows g (e < 2) and g + 8, once ordered()
-  static __device__ __forceinline__ int col(int i, int t) {
-    return 16 * (i >> 1) + 4 * t + 2 * (i & 1);
+template <int D, int NQ, int QR, int KR>
+struct WarpAttnQuant {
+  // lane (g, t): columns 2t, 2t + 1 of queries 8 n + .., rows g and g + 8 of o[j],
+  // which are dimensions 16 j + 2 g and 16 j + 2 g + 1
+  float o[D / 16][NQ][4];
+  float m[2 * NQ], l[2 * NQ];  // l: this lane's share of the row's sum
+
+  // ---- a lane's rows and pairs of dimensions (as WarpAttn has them)
+  static constexpr int RL = 2 * NQ, PAIRS = D / 16, WROWS = 8 * NQ;
+  static __device__ __forceinline__ int row(int e, int lane) {
+    return 8 * (e >> 1) + 2 * (lane & 3) + (e & 1);
   }
+  static __device__ __forceinline__ int dim(int i, int lane) { return 16 * i + 2 * (lane >> 2); }
+  static __device__ __forceinline__ bool tells(int lane) { return lane < 4; }
+  __device__ __forceinline__ float2 pair(int i, int e) const {
+    return make_float2(o[i][e >> 1][e & 1], o[i][e >> 1][2 + (e & 1)]);
+  }
+  __device__ __forceinline__ void set_pair(int i, int e, float2 y) {
+    o[i][e >> 1][e & 1] = y.x;
+    o[i][e >> 1][2 + (e & 1)] = y.y;
+  }
+  __device__ __forceinline__ float& top(int e) { return m[e]; }
+  __device__ __forceinline__ float& sum(int e) { return l[e]; }
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
+    for (int i = 0; i < D / 16; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[0][i][e] = 0.f;
-    }
-    m[0][0] = m[0][1] = kNegInf;
-    l[0][0] = l[0][1] = 0.f;
-  }
-
-  // neighbouring dimensions side by side (and back)
-  __device__ __forceinline__ void ordered() {
+      for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float x = o[0][2 * j][2 * r + 1];
-        o[0][2 * j][2 * r + 1] = o[0][2 * j + 1][2 * r];
-        o[0][2 * j + 1][2 * r] = x;
+        for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
       }
     }
+#pragma unroll
+    for (int e = 0; e < RL; ++e) m[e] = kNegInf, l[e] = 0.f;
   }
 
-  // Weights w of a chunk of 8 NT keys, m, l and o brought to the new reference.
-  // sc: the chunk's powers of two ([8 NT][2] bytes); rf: c 2^a of the lane's rows.
+  // Weights w of a chunk of 16 NT keys (x[.][.][2 h + e]: key 16 n + 8 h + g, row e
+  // of the lane's pair), m, l and o brought to the new reference. sc: the chunk's
+  // powers of two ([16 NT][2] bytes); rf: c 2^a of the lane's rows.
   template <int NT>
-  __device__ __forceinline__ void weights(float (&x)[1][NT][4], const unsigned char* qs,
+  __device__ __forceinline__ void weights(float (&x)[NT][NQ][4], const unsigned char* qs,
                                           const unsigned char* ks, const unsigned char* sc,
-                                          int key0, const int (&lim)[1][2], int all,
-                                          const float (&rf)[2], int lane) {
-    static_assert(NT % 2 == 0, "keys in sixteens");
+                                          int key0, const int (&lim)[RL], int all,
+                                          const float (&rf)[RL], int lane) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[0][n][e] = 0.f;
+      for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][q][e] = 0.f;
+      }
     }
-    const int i = lane >> 3, r = lane & 7, t = lane & 3;
+    const int i = lane >> 3, r = lane & 7, g = lane >> 2;
     const uint32_t qb = smem_addr(qs), kb = smem_addr(ks);
 #pragma unroll
     for (int u = 0; u < D / 16; u += 2) {
-      uint32_t a[2][4];
+      uint32_t b[NQ][4];  // k-steps u and u + 1
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        ldsm4(a[s], qb + unit_off<QR>((i & 1) * 8 + r, 2 * (u + s) + (i >> 1)));
+      for (int q = 0; q < NQ; ++q) ldsm4(b[q], qb + unit_off<QR>(8 * q + r, 2 * u + i));
 #pragma unroll
-      for (int n = 0; n < NT / 2; ++n) {
-        uint32_t kf[4];
-        ldsm4(kf, kb + code_off<D, KR>(16 * n + (i >> 1) * 8 + r, u + (i & 1)));
+      for (int n = 0; n < NT; ++n) {
+        uint32_t kf[4];  // keys 0-7 and 8-15 of unit u, of unit u + 1
+        ldsm4(kf, kb + code_off<D, KR>(16 * n + (i & 1) * 8 + r, u + (i >> 1)));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int s = 0; s < 2; ++s) {
+          uint32_t a[4];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const __half2 b0 = e4m3x2_half2(kf[2 * h + s]), b1 = e4m3x2_half2(kf[2 * h + s] >> 16);
-            mma16<__half>(x[0][2 * n + h], a[s], *reinterpret_cast<const uint32_t*>(&b0),
-                          *reinterpret_cast<const uint32_t*>(&b1));
+          for (int h = 0; h < 2; ++h) {
+            const __half2 lo = e4m3x2_half2(kf[2 * s + h]), hi = e4m3x2_half2(kf[2 * s + h] >> 16);
+            a[h] = *reinterpret_cast<const uint32_t*>(&lo);
+            a[2 + h] = *reinterpret_cast<const uint32_t*>(&hi);
+          }
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) mma16<__half>(x[n][q], a, b[q][2 * s], b[q][2 * s + 1]);
+        }
+      }
+    }
+    const bool masked = key0 + 16 * NT > all;
+    float vs[NT][2];  // powers of two of the lane's values
+    float top[RL];
+#pragma unroll
+    for (int e = 0; e < RL; ++e) top[e] = kNegInf;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = 16 * n + 8 * h + g;
+        const uint32_t w = *reinterpret_cast<const uint16_t*>(sc + 2 * key);
+        const float kscale = __uint_as_float((w & 0xffu) << 23);
+        const float f = (float)((int)(w >> 8) - kScaleBias);
+        vs[n][h] = __uint_as_float((w >> 8) << 23);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = x[n][q][2 * h + e] * (rf[2 * q + e] * kscale);
+            if (masked && key0 + key >= lim[2 * q + e]) y = kNegInf;
+            x[n][q][2 * h + e] = y;
+            top[2 * q + e] = fmaxf(top[2 * q + e], y + f);
           }
         }
       }
     }
-    const bool masked = key0 + 8 * NT > all;
-    float vs[NT][2];  // powers of two of the lane's values
-    float top[2] = {kNegInf, kNegInf};
+    float base[RL];
+    bool moved = false;
+    float a[RL];
+#pragma unroll
+    for (int e = 0; e < RL; ++e) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], d));
+      const float to = fmaxf(m[e], top[e] - kWeightTop);
+      base[e] = to == kNegInf ? 0.f : to;
+      a[e] = exp2_fast(m[e] - base[e]);
+      moved |= a[e] != 1.f;
+      m[e] = to;
+      l[e] *= a[e];
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(sc + 2 * (8 * n + 2 * t));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t kb8 = (w >> (16 * e)) & 0xffu, vb8 = (w >> (16 * e + 8)) & 0xffu;
-        const float kscale = __uint_as_float(kb8 << 23);
-        const float f = (float)((int)vb8 - kScaleBias);
-        vs[n][e] = __uint_as_float(vb8 << 23);
+      for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float y = x[0][n][2 * h + e] * rf[h] * kscale;
-          if (masked && key0 + 8 * n + 2 * t + e >= lim[0][h]) y = kNegInf;
-          x[0][n][2 * h + e] = y;
-          top[h] = fmaxf(top[h], y + f);
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2_fast(x[n][q][e] - base[2 * q + (e & 1)]);
+          l[2 * q + (e & 1)] += p;
+          // a key that is not seen has no weight, whatever its bytes hold
+          x[n][q][e] = masked && p == 0.f ? 0.f : p * vs[n][e >> 1];
         }
       }
     }
-    float a[2], base[2];
+    if (__any_sync(kFull, moved)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(kFull, top[h], 2));
-      const float to = fmaxf(m[0][h], top[h] - kWeightTop);
-      base[h] = to == kNegInf ? 0.f : to;
-      a[h] = exp2_fast(m[0][h] - base[h]);
-      m[0][h] = to;
-      l[0][h] *= a[h];
-    }
+      for (int j = 0; j < D / 16; ++j) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+        for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = exp2_fast(x[0][n][e] - base[e >> 1]);
-        l[0][e >> 1] += p;
-        // a key that is not seen has no weight, whatever its bytes hold
-        x[0][n][e] = masked && p == 0.f ? 0.f : p * vs[n][e & 1];
-      }
-    }
-    if (__any_sync(kFull, a[0] != 1.f || a[1] != 1.f)) {
-#pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[0][j][e] *= a[e >> 1];
+          for (int e = 0; e < 4; ++e) o[j][q][e] *= a[2 * q + (e & 1)];
+        }
       }
     }
   }
@@ -209,7 +246,7 @@ struct WarpAttnQuant {
   // the code NaN among the chunk's values (whole warp)
   template <int NT>
   static __device__ __forceinline__ bool any_nan(const unsigned char* vs, int lane) {
-    constexpr int W = 8 * NT * D / 16;
+    constexpr int W = 16 * NT * D / 16;
     bool bad = false;
     for (int i = lane; i < W; i += 32) {
       const uint4 u = reinterpret_cast<const uint4*>(vs)[i];
@@ -222,35 +259,38 @@ struct WarpAttnQuant {
 
   // o += w v
   template <int NT>
-  __device__ __forceinline__ void add(const float (&w)[1][NT][4], const unsigned char* vs,
-                                      int key0, const int (&lim)[1][2], int all, int lane) {
-    if (key0 + 8 * NT > all && any_nan<NT>(vs, lane)) {
+  __device__ __forceinline__ void add(const float (&w)[NT][NQ][4], const unsigned char* vs,
+                                      int key0, const int (&lim)[RL], int all, int lane) {
+    if (key0 + 16 * NT > all && any_nan<NT>(vs, lane)) {
       add_selected<NT>(w, vs, key0, lim, lane);
       return;
     }
     const int i = lane >> 3, r = lane & 7;
     const uint32_t vb = smem_addr(vs);
 #pragma unroll
-    for (int n = 0; n < NT / 2; ++n) {
-      uint32_t a[4];
-      a[0] = pack2<__half>(w[0][2 * n][0], w[0][2 * n][1]);
-      a[1] = pack2<__half>(w[0][2 * n][2], w[0][2 * n][3]);
-      a[2] = pack2<__half>(w[0][2 * n + 1][0], w[0][2 * n + 1][1]);
-      a[3] = pack2<__half>(w[0][2 * n + 1][2], w[0][2 * n + 1][3]);
+    for (int n = 0; n < NT; ++n) {
+      uint32_t b[NQ][2];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        b[q][0] = movmatrix(pack2<__half>(w[n][q][0], w[n][q][1]));
+        b[q][1] = movmatrix(pack2<__half>(w[n][q][2], w[n][q][3]));
+      }
 #pragma unroll
       for (int u = 0; u < D / 16; u += 2) {
         uint32_t vf[4];  // keys 0-7 and 8-15 of unit u, of unit u + 1
         ldsm4_t(vf, vb + code_off<D, KR>(16 * n + (i & 1) * 8 + r, u + (i >> 1)));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          const uint32_t b0 = __byte_perm(vf[2 * s], 0, 0x3120);
-          const uint32_t b1 = __byte_perm(vf[2 * s + 1], 0, 0x3120);
+          uint32_t a[4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const __half2 h0 = e4m3x2_half2(b0 >> (16 * h)), h1 = e4m3x2_half2(b1 >> (16 * h));
-            mma16<__half>(o[0][2 * (u + s) + h], a, *reinterpret_cast<const uint32_t*>(&h0),
-                          *reinterpret_cast<const uint32_t*>(&h1));
+            const uint32_t y = __byte_perm(vf[2 * s + h], 0, 0x3120);
+            const __half2 even = e4m3x2_half2(y), odd = e4m3x2_half2(y >> 16);
+            a[2 * h] = *reinterpret_cast<const uint32_t*>(&even);
+            a[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&odd);
           }
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) mma16<__half>(o[u + s][q], a, b[q][0], b[q][1]);
         }
       }
     }
@@ -258,49 +298,51 @@ struct WarpAttnQuant {
 
   // the same with the keys that a row does not see left out by selection
   template <int NT>
-  __device__ __forceinline__ void add_selected(const float (&w)[1][NT][4], const unsigned char* vs,
-                                            int key0, const int (&lim)[1][2], int lane) {
-    const int t = lane & 3;
+  __device__ __forceinline__ void add_selected(const float (&w)[NT][NQ][4],
+                                               const unsigned char* vs, int key0,
+                                               const int (&lim)[RL], int lane) {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll 1
-      for (int j = 0; j < 8; ++j) {
-        const int from = (lane & ~3) | (j >> 1), key = 8 * n + j;
-        float y[4];
+      for (int j = 0; j < 16; ++j) {
+        const int key = 16 * n + j, from = (j & 7) * 4 + t;
+        float p[RL];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __shfl_sync(kFull, w[0][n][e], from);
-        const float p0 = (j & 1) ? y[1] : y[0], p1 = (j & 1) ? y[3] : y[2];
-        const bool s0 = key0 + key < lim[0][0], s1 = key0 + key < lim[0][1];
+        for (int q = 0; q < NQ; ++q) {
+          // both halves' values, then one of them (an index that is not known when
+          // compiling would put w into local memory for every use)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float lo = __shfl_sync(kFull, w[n][q][e], from);
+            const float hi = __shfl_sync(kFull, w[n][q][2 + e], from);
+            p[2 * q + e] = j < 8 ? lo : hi;
+          }
+        }
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {
-          const uint32_t four =
-              *reinterpret_cast<const uint32_t*>(vs + code_off<D, KR>(key, d) + 4 * t);
-          float v[4];
-          e4m3x4_values(four, 1.f, v);
-          if (s0) {
-            o[0][2 * d][0] = fmaf(p0, v[0], o[0][2 * d][0]);
-            o[0][2 * d + 1][0] = fmaf(p0, v[1], o[0][2 * d + 1][0]);
-            o[0][2 * d][1] = fmaf(p0, v[2], o[0][2 * d][1]);
-            o[0][2 * d + 1][1] = fmaf(p0, v[3], o[0][2 * d + 1][1]);
-          }
-          if (s1) {
-            o[0][2 * d][2] = fmaf(p1, v[0], o[0][2 * d][2]);
-            o[0][2 * d + 1][2] = fmaf(p1, v[1], o[0][2 * d + 1][2]);
-            o[0][2 * d][3] = fmaf(p1, v[2], o[0][2 * d][3]);
-            o[0][2 * d + 1][3] = fmaf(p1, v[3], o[0][2 * d + 1][3]);
+          const uint32_t two =
+              *reinterpret_cast<const uint16_t*>(vs + code_off<D, KR>(key, d) + 2 * g);
+          const float2 v = __half22float2(e4m3x2_half2(two));
+#pragma unroll
+          for (int e = 0; e < RL; ++e) {
+            if (key0 + key < lim[e]) {
+              float* y = o[d][e >> 1];
+              y[e & 1] = fmaf(p[e], v.x, y[e & 1]);
+              y[2 + (e & 1)] = fmaf(p[e], v.y, y[2 + (e & 1)]);
+            }
           }
         }
       }
     }
   }
 
-  // sums of l over the row's lanes, outputs in order
+  // sums of l over the row's lanes
   __device__ __forceinline__ void finish() {
-    ordered();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[0][h] += __shfl_xor_sync(kFull, l[0][h], 1);
-      l[0][h] += __shfl_xor_sync(kFull, l[0][h], 2);
+    for (int e = 0; e < RL; ++e) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(kFull, l[e], d);
     }
   }
 };

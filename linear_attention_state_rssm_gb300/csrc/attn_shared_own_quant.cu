@@ -3,10 +3,10 @@
 
 namespace rssm {
 
-cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                                    int sms, cudaStream_t st) {
-  return dt == DT_BF16 ? decode_any<__nv_bfloat16, true, DEC_OWN>(p, maps, D, mw, sms, st)
-                       : decode_any<__half, true, DEC_OWN>(p, maps, D, mw, sms, st);
+  return dt == DT_BF16 ? decode_any<__nv_bfloat16, true, DEC_OWN>(p, maps, D, rows, sms, st)
+                       : decode_any<__half, true, DEC_OWN>(p, maps, D, rows, sms, st);
 }
 
 }  // namespace rssm

@@ -101,7 +101,7 @@ rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, v
   if (e == cudaSuccess)
     e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
                          (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
-                         cfg->D, cfg->dtype, scales != nullptr);
+                         cfg->D, cfg->dtype, scales != nullptr, cfg->page_size);
   if (e != cudaSuccess) {
     delete h;
     return RSSM_ERR_CUDA;
@@ -451,7 +451,7 @@ rssm_status rssm_attn_decode(rssm_kv_handle* h, int32_t layer, const void* q, in
   if (!tokens_ok(c, q, q_stride, c.HQ) || o == nullptr || !aligned16(o) || !aligned4(lse))
     return RSSM_ERR_INVALID_ARG;
   DecodeParams p = decode_params(h, layer, q, q_stride, slot, B, T, o, lse);
-  const int rows = attn_decode_block_rows(c.D, c.dtype, T * p.G);
+  const int rows = attn_decode_block_rows(c.D, c.dtype, h->scales != nullptr, T * p.G);
   p.nmb = (T * p.G + rows - 1) / rows;
   return from_cuda(
       attn_decode_launch(p, h->maps, c.D, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));

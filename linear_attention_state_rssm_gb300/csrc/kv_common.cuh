@@ -235,24 +235,24 @@ cudaError_t attn_decode_prepare(int D, int dt, bool quant);
 // tensor maps of the pool (kKvMapBytes, 64-byte aligned) and the launch with them
 constexpr int kKvMapBytes = 256;
 cudaError_t attn_decode_maps(void* maps, const void* k, const void* v, long long rows, int D,
-                             int dt, bool quant);
-// kernels of quantised pages, mw warps to a stream; p null: prepares them all
-cudaError_t attn_decode_quant(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                             int dt, bool quant, int page_size);
+// kernels of quantised pages, blocks of `rows`; p null: prepares them all
+cudaError_t attn_decode_quant(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                               int sms, cudaStream_t st);
 cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st);
-int attn_decode_block_rows(int D, int dt, int rows);  // rows of a block for T G rows
+int attn_decode_block_rows(int D, int dt, bool quant, int rows);  // rows of a block for T G rows
 // the two launches of attention over shared prefixes, and their preparation
 cudaError_t attn_shared_prepare(int D, int dt, bool quant);
 cudaError_t attn_shared_launch(DecodeParams p, const void* maps, int D, int dt, int num_sms,
                                cudaStream_t st);
-cudaError_t attn_shared_prefix(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+cudaError_t attn_shared_prefix(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                                int sms, cudaStream_t st);
 cudaError_t attn_shared_prefix_quant(const DecodeParams* p, const void* maps, int D, int dt,
-                                     int mw, int sms, cudaStream_t st);
-cudaError_t attn_shared_own(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+                                     int rows, int sms, cudaStream_t st);
+cudaError_t attn_shared_own(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                             int sms, cudaStream_t st);
-cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int mw,
+cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                                   int sms, cudaStream_t st);
 cudaError_t attn_prompt_prepare(int D, int dt);
 cudaError_t attn_prompt_launch(const PromptParams& p, cudaStream_t st);
