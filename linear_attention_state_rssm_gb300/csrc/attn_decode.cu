@@ -66,27 +66,41 @@ cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, i
                              : plain(&p, maps, D, dt, rows, sms, st);
 }
 
+// Shared prefixes: on the 5th-generation tensor cores where they take the pages,
+// else by the kernel of single rows with a group's query rows in its blocks.
 cudaError_t attn_shared_prepare(int D, int dt, bool quant) {
-  const cudaError_t e = quant ? attn_shared_prefix_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
-                              : attn_shared_prefix(nullptr, nullptr, D, dt, 0, 0, nullptr);
+  cudaError_t e = cudaSuccess;
+  if (attn_shared_tc_serves(dt, quant)) {
+    e = attn_shared_tc_prefix(nullptr, nullptr, D, dt, quant, nullptr);
+  } else {
+    e = quant ? attn_shared_prefix_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
+              : attn_shared_prefix(nullptr, nullptr, D, dt, 0, 0, nullptr);
+  }
   if (e != cudaSuccess) return e;
   return quant ? attn_shared_own_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
                : attn_shared_own(nullptr, nullptr, D, dt, 0, 0, nullptr);
 }
 
-cudaError_t attn_shared_launch(DecodeParams p, const void* maps, int D, int dt, int num_sms,
-                               cudaStream_t st) {
+cudaError_t attn_shared_launch(DecodeParams p, const void* maps, const void* tc_maps, int D,
+                               int dt, int num_sms, cudaStream_t st) {
   const int sms = num_sms < kMaxSms ? num_sms : kMaxSms;
   const bool quant = p.scales != nullptr;
-  // blocks of as many rows as there are, but none of 32 where pages are not quantised
+  // blocks of as many rows as there are
   auto block = [&](long long rows) {
     const int n = attn_decode_block_rows(D, dt, quant, rows < 4096 ? (int)rows : 4096);
     return n == 32 && !quant ? (D == 256 ? 48 : 64) : n;
   };
-  const int all = block((long long)p.B * p.T * p.G), own = block(p.T * p.G);
-  const cudaError_t e = quant ? attn_shared_prefix_quant(&p, maps, D, dt, all, sms, st)
-                              : attn_shared_prefix(&p, maps, D, dt, all, sms, st);
+  cudaError_t e;
+  if (attn_shared_tc_serves(dt, quant)) {
+    p.cut = 1;
+    e = attn_shared_tc_prefix(&p, tc_maps, D, dt, quant, st);
+  } else {
+    const int rows = block((long long)p.B * p.T * p.G);
+    e = quant ? attn_shared_prefix_quant(&p, maps, D, dt, rows, sms, st)
+              : attn_shared_prefix(&p, maps, D, dt, rows, sms, st);
+  }
   if (e != cudaSuccess) return e;
+  const int own = block(p.T * p.G);
   p.nmb = (p.T * p.G + own - 1) / own;
   return quant ? attn_shared_own_quant(&p, maps, D, dt, own, sms, st)
                : attn_shared_own(&p, maps, D, dt, own, sms, st);

@@ -55,6 +55,7 @@ enum : int { DEC_PLAIN = 0, DEC_PREFIX = 1, DEC_OWN = 2 };
 constexpr int kBox = 16;        // keys of a TMA box: within one page (pages of 16 k keys)
 constexpr int kQuantBox = 32;   // rows of a column of quantised keys: a box's, or two of kBox's
 constexpr int kGapKeys = 256;   // what beginning and ending a row costs, as keys
+constexpr int kGapOwn = 1024;    // the same behind a shared prefix: its parts are joined, tables compared
 constexpr int kLeastKeys = 512; // keys that a CTA takes at least (of longer rows)
 constexpr int kRowParts = 96;   // parts of the longest row, about: one CTA joins them
 constexpr int kLostPart = 1 << 16;  // in a row's arrivals, beside their number: a part that is not there
@@ -81,7 +82,6 @@ struct DecCfg {
   static constexpr int NW = F32 ? (D == 256 ? 4 : 3) : NQ == 1 ? 5 : D == 256 ? 6 : 4;
   static constexpr int CH = F32 || (D == 256 && !Q) ? 16 : 32;  // keys of a chunk
   static constexpr int GRP = D == 256 ? 2 : 4;         // chunks that are sent for together
-  static constexpr int GAP = kGapKeys / CH;
   static constexpr int CT = NW * 32;                   // threads of the streams
   static constexpr int NT = CT + 32;                   // and the producer warp
   static constexpr int NG = NW / MW;                   // streams of a CTA
@@ -92,6 +92,8 @@ struct DecCfg {
   static constexpr int QBYTES = ROWS * D * (int)sizeof(T);
   static constexpr int OP = 72;                        // row pitch of 64 columns of outputs
   static constexpr int OBYTES = NG > 1 ? NG * ROWS * OP * 4 : 0;
+  // the joined parts of a prefix fit in the room of the streams' outputs
+  static constexpr bool JOIN_HERE = OBYTES >= ROWS * D * 4;
   static constexpr int REST = 1024 + 2 * QBYTES + OBYTES + 2 * NG * ROWS * 4 + ROWS * 8 + 1024 +
                               (Q ? 2 * ROWS * 4 : 0);
   static constexpr int MOST = (228 / CPS - 1) * 1024;  // a CTA's share of the SM
@@ -172,9 +174,9 @@ __device__ __forceinline__ int row_blocks(const DecodeParams& p, int r) {
 }
 
 // places of a row's chunks of CH keys on the line, with the gap before them
-template <int CH>
+template <int CH, int GAP>
 __device__ __forceinline__ long long places(int keys) {
-  return keys > 0 ? ((long long)keys + CH - 1) / CH + kGapKeys / CH : 0;
+  return keys > 0 ? ((long long)keys + CH - 1) / CH + GAP : 0;
 }
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
@@ -196,14 +198,14 @@ struct Seg {
 // The CTA's stretch of the line, one Seg after the other.
 template <int CH, int MODE, int ROWS>
 struct Line {
-  static constexpr int kGap = kGapKeys / CH;
+  static constexpr int kGap = (MODE == DEC_OWN ? kGapOwn : kGapKeys) / CH;
   long long pos, end, row0;
   int row;
   __device__ __forceinline__ bool next(const DecodeParams& p, Seg& g) {
     while (pos < end) {
       g.keys = row_keys<MODE>(p, row, false, g.slot, g.start);
       const int nmb = row_blocks<MODE, ROWS>(p, row), items = p.HKV * nmb;
-      const int cost = (int)places<CH>(g.keys - g.start);
+      const int cost = (int)places<CH, kGap>(g.keys - g.start);
       if (pos >= row0 + (long long)cost * items) {
         row0 += (long long)cost * items;
         ++row;
@@ -279,15 +281,16 @@ __device__ __forceinline__ long long query_token(const DecodeParams& p, int r, i
 // Whether the row's pages up to its prefix's end are those that the group's keys
 // were read from (the plan may be older than the tables), and were read.
 template <int THREADS>
-__device__ __forceinline__ bool prefix_holds(const DecodeParams& p, const Seg& sg, int tid) {
-  bool same = *p.share.lost == 0;
-  const int lead = lead_slot(p, p.share.group[sg.row]);
+__device__ __forceinline__ bool prefix_holds(const DecodeParams& p, const Seg& sg,
+                                             const ShareRow& rec, int tid) {
+  int lead = p.slot[rec.lead];
+  if (lead < 0 || lead >= p.n_slots) lead = lead_slot(p, rec.group);
+  bool same = *p.share.lost == 0 && lead >= 0;
+  if (!same || sg.slot == lead) return same;
   const int32_t* a = p.table + (size_t)sg.slot * p.max_pages;
   const int32_t* b = p.table + (size_t)lead * p.max_pages;
   const int n = sg.start >> p.shift;
-  if (sg.slot != lead) {
-    for (int i = tid; i < n; i += THREADS) same = same && a[i] == b[i];
-  }
+  for (int i = tid; i < n; i += THREADS) same = same && a[i] == b[i];
   return same;
 }
 
@@ -303,6 +306,43 @@ __device__ __forceinline__ bool named_any(int id, int count, bool x) {
       : "r"(id), "r"(count), "r"((uint32_t)x)
       : "memory");
   return any != 0;
+}
+
+// The parts of a prefix that was cut, joined for a block's rows: outputs [R][D]
+// to where `to` says, maxima and sums into row_m and row_l. All threads of the
+// streams; a barrier has to follow. A thread has four dimensions of a row, so
+// that all its loads are one trip to memory.
+template <typename C, int D, typename F>
+__device__ __forceinline__ void join_parts(const DecodeParams& p, const Seg& sg,
+                                           const ShareRow& rec, int base, int R, F to,
+                                           float* row_m, float* row_l, int tid) {
+  const ShareView& s = p.share;
+  const size_t part = (size_t)s.part_rows * (D + 2);
+  for (int i = tid; i < R * (D / 4); i += C::CT) {
+    const int rr = i / (D / 4), d = i % (D / 4) * 4;
+    const int row = rec.first + base + rr, block = row / 128, r = row % 128;
+    const float* from =
+        s.part + (rec.part0 + ((size_t)sg.h * rec.blocks + block) * rec.parts) * part;
+    const float* at_o = from + (size_t)r * D + d;
+    const float* at_ml = from + (size_t)s.part_rows * D + 2 * r;
+    float m = kNegInf, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int k = 0; k < rec.parts; ++k) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(at_o + k * part));
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(at_ml + k * part));
+      const float top = fmaxf(m, ml.x), mu = top == kNegInf ? 0.f : top;
+      const float fa = exp2_fast(m - mu), fb = exp2_fast(ml.x - mu);
+      l = l * fa + ml.y * fb;
+      a.x = a.x * fa + y.x * fb;
+      a.y = a.y * fa + y.y * fb;
+      a.z = a.z * fa + y.z * fb;
+      a.w = a.w * fa + y.w * fb;
+      m = top;
+    }
+    *reinterpret_cast<float4*>(to(rr) + d) = a;
+    if (d == 0) row_m[rr] = m, row_l[rr] = l;
+  }
 }
 
 template <typename T, int D, int MW, int NQ, int MODE>
@@ -358,7 +398,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
   for (int r = tid; r < p.B; r += C::NT) {
     int s, start;
     const int keys = row_keys<MODE>(p, r, blockIdx.x == 0, s, start);
-    const long long cost = places<C::CH>(keys - start);
+    const long long cost = places<C::CH, Stretch::kGap>(keys - start);
     const long long w = cost * p.HKV * row_blocks<MODE, C::ROWS>(p, r);
     if (r < C::NT) first_w = w;
     mine += w;
@@ -389,7 +429,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
   share = share > few ? share : few;
   // not less than kLeastKeys, or a whole row where the longest has fewer
   const long long least =
-      longest < C::GAP + kLeastKeys / C::CH ? longest : C::GAP + kLeastKeys / C::CH;
+      longest < Stretch::kGap + kLeastKeys / C::CH ? longest : Stretch::kGap + kLeastKeys / C::CH;
   share = share > least ? share : least;
   Stretch line;
   line.pos = share * blockIdx.x;
@@ -407,7 +447,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     if (r0 + tid < p.B) {
       int s, start;
       const int keys = row_keys<MODE>(p, r0 + tid, false, s, start);
-      w = places<C::CH>(keys - start) * p.HKV * row_blocks<MODE, C::ROWS>(p, r0 + tid);
+      w = places<C::CH, Stretch::kGap>(keys - start) * p.HKV * row_blocks<MODE, C::ROWS>(p, r0 + tid);
     }
     const long long incl = warp_scan(w, lane);
     __syncthreads();  // the last sums have been read
@@ -645,26 +685,33 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     bool skip = false;  // no output of this segment
     if constexpr (MODE == DEC_OWN) {
       if (sg.start > 0 && sg.c0 == 0) {
-        skip = named_any(1, C::CT, !prefix_holds<C::CT>(p, sg, tid));
+        // The first stream goes on from where the prefix ended; from the parts of a
+        // prefix that was cut, joined by all streams where their outputs will be.
+        const ShareRow rec = p.share.rows[sg.row];
+        const int parts = p.cut ? rec.parts : 1;
+        auto joined = [&](int rr) {
+          return C::JOIN_HERE && parts > 1 ? os + rr * D : p.share.o + out_row(rr) * D;
+        };
+        if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
+        skip = named_any(1, C::CT, !prefix_holds<C::CT>(p, sg, rec, tid));
         if (skip && tid == 0)
           atomicOr(p.err, *p.share.lost != 0 ? (uint32_t)DEVERR_TIMEOUT : (uint32_t)DEVERR_PAGES);
-        // the first stream goes on from where the prefix ended
-        if (grp == 0 && !skip) {
+        if (!skip && grp == 0) {
 #pragma unroll
           for (int e = 0; e < W::RL; ++e) {
             const int rr = wr + W::row(e, lane);
-            if (rr < R) {
-              const size_t at = out_row(rr);
-              const float2 ml = p.share.ml[at];
-              w.top(e) = ml.x;
-              w.sum(e) = W::tells(lane) ? ml.y : 0.f;
-              const float* from = p.share.o + at * D;
+            if (rr >= R) continue;
+            const float2 ml =
+                parts > 1 ? make_float2(row_m[rr], row_l[rr]) : p.share.ml[out_row(rr)];
+            const float* from = joined(rr);
+            w.top(e) = ml.x;
+            w.sum(e) = W::tells(lane) ? ml.y : 0.f;
 #pragma unroll
-              for (int i = 0; i < W::PAIRS; ++i)
-                w.set_pair(i, e, *reinterpret_cast<const float2*>(from + W::dim(i, lane)));
-            }
+            for (int i = 0; i < W::PAIRS; ++i)
+              w.set_pair(i, e, *reinterpret_cast<const float2*>(from + W::dim(i, lane)));
           }
         }
+        if (parts > 1) named_sync(1, C::CT);  // before the streams' outputs take the room
       }
     }
 

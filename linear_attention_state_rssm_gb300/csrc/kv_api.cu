@@ -18,6 +18,7 @@ struct rssm_kv_handle {
   unsigned char* scales;  // e4m3 pages: [pool row][2] powers of two (else null)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   alignas(64) unsigned char maps[kKvMapBytes];  // the pool's tensor maps
+  alignas(64) unsigned char tc_maps[kKvMapBytes];  // and those of shared prefixes
 };
 
 namespace {
@@ -102,6 +103,10 @@ rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, v
     e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
                          (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
                          cfg->D, cfg->dtype, scales != nullptr, cfg->page_size);
+  if (e == cudaSuccess && attn_shared_tc_serves(cfg->dtype, scales != nullptr))
+    e = attn_shared_tc_maps(h->tc_maps, buf->k_pages, buf->v_pages,
+                            (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
+                            cfg->D, cfg->dtype, scales != nullptr, cfg->page_size);
   if (e != cudaSuccess) {
     delete h;
     return RSSM_ERR_CUDA;
@@ -462,7 +467,7 @@ rssm_status rssm_kv_share_bytes(const rssm_kv_config* cfg, int32_t B, int32_t T,
   if (st != RSSM_OK) return st;
   if (out == nullptr || B < 0 || B > kMaxRows || T < 1) return RSSM_ERR_INVALID_ARG;
   if (T > 64) return RSSM_ERR_UNSUPPORTED;
-  *out = ShareView::lay(nullptr, B, T, cfg->HQ, cfg->D, nullptr);
+  *out = ShareView::lay(nullptr, B, T, cfg->HQ, cfg->HKV, cfg->D, nullptr);
   return RSSM_OK;
 }
 
@@ -478,8 +483,9 @@ rssm_status rssm_kv_share(rssm_kv_handle* h, const int32_t* slot, int32_t B, int
   p.B = B;
   p.T = T;
   ShareView v;
-  ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.D, &v);
-  return from_cuda(kv_share_launch(v, p, static_cast<cudaStream_t>(stream)));
+  ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.HKV, h->cfg.D, &v);
+  return from_cuda(kv_share_launch(v, p, h->cfg.HKV, h->cfg.HQ / h->cfg.HKV,
+                                   static_cast<cudaStream_t>(stream)));
 }
 
 rssm_status rssm_attn_decode_shared(rssm_kv_handle* h, int32_t layer, const void* q,
@@ -495,9 +501,10 @@ rssm_status rssm_attn_decode_shared(rssm_kv_handle* h, int32_t layer, const void
       share == nullptr || !aligned16(share))
     return RSSM_ERR_INVALID_ARG;
   DecodeParams p = decode_params(h, layer, q, q_stride, slot, B, T, o, lse);
-  ShareView::lay(share, B, T, c.HQ, c.D, &p.share);
+  ShareView::lay(share, B, T, c.HQ, c.HKV, c.D, &p.share);
   return from_cuda(
-      attn_shared_launch(p, h->maps, c.D, c.dtype, h->num_sms, static_cast<cudaStream_t>(stream)));
+      attn_shared_launch(p, h->maps, h->tc_maps, c.D, c.dtype, h->num_sms,
+                         static_cast<cudaStream_t>(stream)));
 }
 
 rssm_status rssm_attn_prefill(rssm_kv_handle* h, const void* q, const void* k, const void* v,

@@ -132,8 +132,34 @@ struct GatherParams {
   int n_slots, n_pages, max_pages, shift, dt;
 };
 
-// What rows of a batch share (kv_share.cuh), in the caller's buffer: the groups,
+constexpr int kShareSplit = kMaxSms;  // stretches that prefixes are cut into, about
+
+// What rows of a batch share (kv_share.cu), in the caller's buffer: the groups,
 // and what the first of the two launches leaves for the second.
+// Stretches that a call can have: an even split over the SMs, and one more for
+// every block of 128 rows of a group (of two members at least) and key head.
+__host__ __device__ inline long long share_segments(int B, int T, int G, int HKV) {
+  return kShareSplit + (long long)HKV * ((long long)B * T * G / 128 + B / 2 + 1);
+}
+struct ShareSeg {  // a stretch of a prefix, for 128 query rows of a key head
+  int32_t begin;  // of its group's rows in order
+  int32_t lead;   // the first of them
+  int32_t group;
+  int32_t keys;   // of the whole prefix
+  int32_t rows;   // query rows of a key head of the group
+  int32_t at;     // key head * blocks + block of 128 rows
+  int32_t part;   // which stretch
+  int32_t out;    // its place among the parts; -1: the only one
+};
+struct ShareRow {  // of a row with a prefix
+  int32_t group;
+  int32_t lead;    // the group's first row
+  int32_t first;   // the row's first query row of a key head, among the group's
+  int32_t parts;   // stretches of each of the group's blocks of 128 query rows
+  int32_t part0;   // the first of them among the parts, where there are several
+  int32_t blocks;  // of a key head
+  int32_t pad[2];
+};
 struct ShareView {
   int32_t* of;          // [2] B and T of the plan
   int32_t* groups;      // [1] their number
@@ -143,12 +169,23 @@ struct ShareView {
   int32_t* order;       // [B] rows, group by group
   int32_t* begin;       // [B + 1] first place of a group in order
   int32_t* group_keys;  // [B] keys of a group's prefix
+  ShareRow* rows;       // [B]
+  int32_t* steps;       // [1] of 128 keys: a stretch of a prefix (attn_shared_tc.cuh)
+  int32_t* segments;    // [1] stretches of all groups
+  int32_t* seg;         // [B + 1] first stretch of a group
+  int32_t* parts;       // [B] stretches of a group's block of 128 rows and a key head
+  int32_t* part0;       // [B] its first place among the parts, where there are several
+  ShareSeg* segs;       // the stretches
   int32_t* scratch;     // [2 B] of the plan
   float2* ml;           // [B T][HQ] running maxima and sums of the prefixes
   float* o;             // [B T][HQ][D] and outputs
+  float* part;          // [2 kShareSplit] of the stretches of prefixes that are cut:
+                        // outputs [part_rows][D], maxima and sums [part_rows][2]
+  int part_rows;        // query rows of a key head in a stretch, at most 128
   __host__ __device__ static size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
   // the view of a buffer (null: only its size)
-  __host__ __device__ static size_t lay(void* base, int B, int T, int HQ, int D, ShareView* v) {
+  __host__ __device__ static size_t lay(void* base, int B, int T, int HQ, int HKV, int D,
+                                        ShareView* v) {
     char* at = static_cast<char*>(base);
     size_t n = 0;
     auto take = [&](size_t bytes) {
@@ -158,19 +195,34 @@ struct ShareView {
     };
     const size_t b = (size_t)B * 4, rows = (size_t)B * T * HQ;
     ShareView s{};
-    char* head = take(16);
+    char* head = take(32);
     char* prefix = take(b);
     char* group = take(b);
     char* order = take(b);
     char* begin = take(b + 4);
     char* keys = take(b);
+    char* rec = take((size_t)B * sizeof(ShareRow));
+    char* seg = take(b + 4);
+    char* parts = take(b);
+    char* part0 = take(b);
     char* scratch = take(2 * b);
+    char* segs = take((size_t)share_segments(B, T, HQ / HKV, HKV) * sizeof(ShareSeg));
     char* ml = take(rows * 8);
     char* o = take(rows * (size_t)D * 4);
+    // whole fours: parts begin on 16 bytes
+    const size_t part_rows = rows / HKV < 125 ? (rows / HKV + 3) / 4 * 4 : 128;
+    char* part = take(2 * kShareSplit * part_rows * (size_t)(D + 2) * 4);
     if (v != nullptr) {
       s.of = reinterpret_cast<int32_t*>(head);
       s.groups = s.of + 2;
       s.lost = s.of + 3;
+      s.steps = s.of + 4;
+      s.segments = s.of + 5;
+      s.segs = reinterpret_cast<ShareSeg*>(segs);
+      s.rows = reinterpret_cast<ShareRow*>(rec);
+      s.seg = reinterpret_cast<int32_t*>(seg);
+      s.parts = reinterpret_cast<int32_t*>(parts);
+      s.part0 = reinterpret_cast<int32_t*>(part0);
       s.prefix = reinterpret_cast<int32_t*>(prefix);
       s.group = reinterpret_cast<int32_t*>(group);
       s.order = reinterpret_cast<int32_t*>(order);
@@ -179,6 +231,8 @@ struct ShareView {
       s.scratch = reinterpret_cast<int32_t*>(scratch);
       s.ml = reinterpret_cast<float2*>(ml);
       s.o = reinterpret_cast<float*>(o);
+      s.part = reinterpret_cast<float*>(part);
+      s.part_rows = (int)part_rows;
       *v = s;
     }
     return n;
@@ -203,6 +257,7 @@ struct DecodeParams {
   long long qs;
   long long page0;  // the layer's first page among all layers'
   int B, T, HQ, HKV, G, n_slots, n_pages, max_pages, shift;
+  int cut;      // DEC_OWN: prefixes may be in parts (attn_shared_tc.cuh)
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   float c;      // scale * log2(e)
@@ -226,7 +281,7 @@ struct PromptParams {
 };
 
 cudaError_t kv_plan_launch(int mode, const PageParams& p, cudaStream_t st);
-cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, cudaStream_t st);
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G, cudaStream_t st);
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
@@ -244,8 +299,13 @@ cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, i
 int attn_decode_block_rows(int D, int dt, bool quant, int rows);  // rows of a block for T G rows
 // the two launches of attention over shared prefixes, and their preparation
 cudaError_t attn_shared_prepare(int D, int dt, bool quant);
-cudaError_t attn_shared_launch(DecodeParams p, const void* maps, int D, int dt, int num_sms,
-                               cudaStream_t st);
+cudaError_t attn_shared_launch(DecodeParams p, const void* maps, const void* tc_maps, int D,
+                               int dt, int num_sms, cudaStream_t st);
+bool attn_shared_tc_serves(int dt, bool quant);
+cudaError_t attn_shared_tc_maps(void* maps, const void* k, const void* v, long long rows, int D,
+                                int dt, bool quant, int page_size);
+cudaError_t attn_shared_tc_prefix(const DecodeParams* p, const void* maps, int D, int dt,
+                                  bool quant, cudaStream_t st);
 cudaError_t attn_shared_prefix(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                                int sms, cudaStream_t st);
 cudaError_t attn_shared_prefix_quant(const DecodeParams* p, const void* maps, int D, int dt,

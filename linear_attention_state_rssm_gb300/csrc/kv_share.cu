@@ -21,6 +21,7 @@ namespace rssm {
 namespace {
 
 constexpr int kShareThreads = 1024;
+constexpr int kLeastSteps = 4;  // of 128 keys: a stretch, but for a prefix's last
 
 struct PlanShareParams {
   ShareView v;
@@ -30,6 +31,7 @@ struct PlanShareParams {
   const int32_t* length;
   int32_t* map;  // [n_pages] of the cache's work buffer
   int B, T, n_slots, n_pages, max_pages, shift, least;
+  int HKV, rows, split;  // key heads; query rows of a row and key head; stretches at most, about
 };
 
 __device__ __forceinline__ int scan_of(int x, int* sums, int tid, int& total) {
@@ -59,14 +61,17 @@ __device__ __forceinline__ int scan_of(int x, int* sums, int tid, int& total) {
 __global__ void __launch_bounds__(kShareThreads)
     plan_share_kernel(const __grid_constant__ PlanShareParams p) {
   __shared__ int sums[32];
+  __shared__ int all_cut, all_whole;
+  __shared__ unsigned long long work;  // steps of 128 keys of all blocks
   const int tid = threadIdx.x;
   int32_t* full = p.v.order;                // whole committed pages, until phase 3
   int32_t* count = p.v.scratch;             // of a lead: members; then its group
-  int32_t* common = p.v.scratch + p.B;      // of a lead: pages; then the next place
+  int32_t* common = p.v.scratch + p.B;      // of a lead: pages; then its group's next place
   if (tid == 0) {
     p.v.of[0] = p.B;
     p.v.of[1] = p.T;
     *p.v.lost = 0;
+    work = 0;
   }
   // ---- 1: each row's whole pages, and the first row that begins with its page
   auto first_page = [&](int r) {
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kShareThreads)
       }
     }
     if (lane == 0) {
-      p.v.group[r] = lead;  // until phase 4
+      p.v.group[r] = lead;  // until phase 5
       if (page >= 0) {
         atomicMin(common + lead, same);
         atomicAdd(count + lead, 1);
@@ -135,22 +140,66 @@ __global__ void __launch_bounds__(kShareThreads)
     }
   }
   __syncthreads();
-  // ---- 3: the groups
-  int groups = 0, rows = 0;
+  // ---- 3: the groups, and the stretches that their prefixes are cut into
+  auto group_of = [&](int r, int& n, int& keys) {  // whether r leads one; members, keys
+    n = r < p.B ? __ldcg(count + r) : 0;
+    const int pages = r < p.B ? __ldcg(common + r) : 0;
+    keys = n >= 2 ? pages << p.shift : 0;
+    return n >= 2 && keys >= p.least;
+  };
+  auto blocks_of = [&](int n) { return (int)(((long long)n * p.rows + 127) / 128) * p.HKV; };
+  unsigned long long mine = 0;
+  for (int r = tid; r < p.B; r += kShareThreads) {
+    int n, keys;
+    if (group_of(r, n, keys))
+      mine += (unsigned long long)blocks_of(n) * (unsigned)((keys + 127) / 128);
+  }
+  if (mine > 0) atomicAdd(&work, mine);
+  __syncthreads();
+  const unsigned long long even = (work + p.split - 1) / p.split;
+  int per = even < kLeastSteps ? kLeastSteps : even > (1 << 24) ? 1 << 24 : (int)even;
+  // a second turn of a few CTAs costs as much as the first: longer stretches where
+  // that leaves one for each SM at most
+  for (int turn = 0; turn < 6; ++turn) {
+    int cut = 0, whole = 0;  // stretches, blocks
+    for (int r = tid; r < p.B; r += kShareThreads) {
+      int n, keys;
+      if (group_of(r, n, keys)) {
+        const int b = blocks_of(n);
+        whole += b;
+        cut += b * (((keys + 127) / 128 + per - 1) / per);
+      }
+    }
+    if (tid == 0) all_cut = all_whole = 0;
+    __syncthreads();
+    if (whole > 0) atomicAdd(&all_cut, cut), atomicAdd(&all_whole, whole);
+    __syncthreads();
+    const int n = all_cut, blocks = all_whole;
+    __syncthreads();
+    if (n <= p.split || blocks > p.split) break;
+    per += max(1, (int)((long long)per * (n - p.split) / p.split));
+  }
+  int groups = 0, rows = 0, segs = 0, slots = 0;
   for (int r0 = 0; r0 < p.B; r0 += kShareThreads) {
     const int r = r0 + tid;
-    const int n = r < p.B ? __ldcg(count + r) : 0;
-    const int pages = r < p.B ? __ldcg(common + r) : 0;
-    const bool on = n >= 2 && ((long long)pages << p.shift) >= p.least;
-    int all_groups, all_rows;
+    int n, keys;
+    const bool on = group_of(r, n, keys);
+    const int parts = on ? ((keys + 127) / 128 + per - 1) / per : 0;
+    const int here = on ? blocks_of(n) * parts : 0;
+    int all_groups, all_rows, all_segs, all_slots;
     const int g = groups + scan_of(on, sums, tid, all_groups);
     const int at = rows + scan_of(on ? n : 0, sums, tid, all_rows);
+    const int seg = segs + scan_of(here, sums, tid, all_segs);
+    const int slot = slots + scan_of(parts > 1 ? here : 0, sums, tid, all_slots);
     if (r < p.B) {
       if (on) {
         p.v.begin[g] = at;
-        p.v.group_keys[g] = pages << p.shift;
+        p.v.group_keys[g] = keys;
+        p.v.seg[g] = seg;
+        p.v.parts[g] = parts;
+        p.v.part0[g] = slot;
         p.v.order[at] = r;
-        common[r] = at + 1;
+        common[r] = 1;
         count[r] = g;
       } else {
         count[r] = -1;
@@ -158,17 +207,51 @@ __global__ void __launch_bounds__(kShareThreads)
     }
     groups += all_groups;
     rows += all_rows;
+    segs += all_segs;
+    slots += all_slots;
   }
   if (tid == 0) {
     *p.v.groups = groups;
+    *p.v.steps = per;
+    *p.v.segments = segs;
     p.v.begin[groups] = rows;
+    p.v.seg[groups] = segs;
   }
   __syncthreads();
-  // ---- 4: their members
+  // ---- 4: a record of each stretch, so that a CTA that takes it has one look-up
+  for (int i = tid; i < segs; i += kShareThreads) {
+    int lo = 0, hi = groups;  // the last group whose first stretch is not behind i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.v.seg[mid] <= i) lo = mid; else hi = mid;
+    }
+    const int parts = p.v.parts[lo], within = i - p.v.seg[lo];
+    ShareSeg s;
+    s.begin = p.v.begin[lo];
+    s.lead = p.v.order[s.begin];
+    s.group = lo;
+    s.keys = p.v.group_keys[lo];
+    s.rows = (p.v.begin[lo + 1] - s.begin) * p.rows;
+    s.at = within / parts;
+    s.part = within % parts;
+    s.out = parts > 1 ? p.v.part0[lo] + within : -1;
+    p.v.segs[i] = s;
+  }
+  // ---- 5: their members
   for (int r = tid; r < p.B; r += kShareThreads) {
-    const int lead = p.v.group[r], g = count[lead];
+    const int lead = p.v.group[r], g = __ldcg(count + lead);
     if (g < 0) continue;
-    if (lead != r) p.v.order[atomicAdd(common + lead, 1)] = r;
+    const int at = lead == r ? 0 : atomicAdd(common + lead, 1);
+    const int begin = p.v.begin[g];
+    if (at > 0) p.v.order[begin + at] = r;
+    ShareRow x{};
+    x.group = g;
+    x.lead = lead;
+    x.first = at * p.rows;
+    x.parts = p.v.parts[g];
+    x.part0 = p.v.part0[g];
+    x.blocks = ((p.v.begin[g + 1] - begin) * p.rows + 127) / 128;
+    p.v.rows[r] = x;
     p.v.prefix[r] = p.v.group_keys[g];
     p.v.group[r] = g;
   }
@@ -176,7 +259,7 @@ __global__ void __launch_bounds__(kShareThreads)
 
 }  // namespace
 
-cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, cudaStream_t st) {
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G, cudaStream_t st) {
   PlanShareParams s{};
   s.v = v;
   s.slot = p.slot;
@@ -191,6 +274,11 @@ cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, cudaStream_
   s.max_pages = p.max_pages;
   s.shift = p.shift;
   s.least = 1;
+  s.HKV = HKV;
+  s.rows = p.T * G;
+  // Blocks that are cut leave fewer than 2 kShareSplit parts: an even split, and the
+  // last stretch of each, which has another before it.
+  s.split = kShareSplit;
   plan_share_kernel<<<1, kShareThreads, 0, st>>>(s);
   return cudaGetLastError();
 }

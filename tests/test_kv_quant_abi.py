@@ -89,8 +89,12 @@ def test_rows_that_the_kernels_cannot_write_are_refused(kw):
 def test_share_buffers(lib):
     cfg = config()
     n = _lib.rssm_kv_share_bytes(cfg, 64, 2)
-    out = 64 * 2 * 16 * (128 + 2) * 4
-    assert out <= n <= out + 8 * 64 * 4 + 9 * 256
+    # outputs of every query row, of 2 x 152 stretches of 128 rows, lists of the rows
+    out = (64 * 2 * 16 + 2 * 152 * 128) * (128 + 2) * 4
+    segs = 152 + 4 * (64 * 2 * 4 // 128 + 64 // 2 + 1)
+    assert out + 32 * segs <= n <= out + 32 * segs + 12 * 64 * 4 + 16 * 256
+    small = (2 * 16 + 2 * 152 * 8) * (128 + 2) * 4     # eight rows of a key head in all
+    assert small <= _lib.rssm_kv_share_bytes(cfg, 2, 1) <= small + 32 * 160 + 17 * 256
     assert _lib.rssm_kv_share_bytes(cfg, 0, 1) >= 16
     for B, T, status in ((-1, 1, 1), (65536, 1, 1), (4, 0, 1), (4, 65, 2)):
         with pytest.raises(_lib.RssmError) as e:
