@@ -392,80 +392,106 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     if (p.hook_cta == (int)blockIdx.x) mbar_promise(&full[p.hook_unit % C::NU], 16);
     fence_mbar_init();
   }
-  // ---- the line's length and its longest row, and the row that holds this
-  // CTA's first place: one look at the lengths for up to NT rows, else two
-  long long mine = 0, most = 0, first_w = 0;
-  for (int r = tid; r < p.B; r += C::NT) {
-    int s, start;
-    const int keys = row_keys<MODE>(p, r, blockIdx.x == 0, s, start);
-    const long long cost = places<C::CH, Stretch::kGap>(keys - start);
-    const long long w = cost * p.HKV * row_blocks<MODE, C::ROWS>(p, r);
-    if (r < C::NT) first_w = w;
-    mine += w;
-    most = cost > most ? cost : most;
-  }
-  const long long first_incl = warp_scan(first_w, lane);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    mine += __shfl_xor_sync(kFull, mine, d);
-    const long long y = __shfl_xor_sync(kFull, most, d);
-    most = y > most ? y : most;
-  }
-  if (lane == 31) {
-    scan[warp] = mine;
-    scan[NW + 1 + warp] = most;
-    scan[2 * (NW + 1) + warp] = first_incl;
-  }
-  __syncthreads();
-  long long total = 0, longest = 0, at = 0, firsts = 0;
-  for (int w = 0; w <= NW; ++w) {
-    total += scan[w];
-    longest = scan[NW + 1 + w] > longest ? scan[NW + 1 + w] : longest;
-    if (w < warp) at += scan[2 * (NW + 1) + w];
-    firsts += scan[2 * (NW + 1) + w];
-  }
-  long long share = (total + gridDim.x - 1) / gridDim.x;
-  const long long few = longest / kRowParts + 1;
-  share = share > few ? share : few;
-  // not less than kLeastKeys, or a whole row where the longest has fewer
-  const long long least =
-      longest < Stretch::kGap + kLeastKeys / C::CH ? longest : Stretch::kGap + kLeastKeys / C::CH;
-  share = share > least ? share : least;
   Stretch line;
-  line.pos = share * blockIdx.x;
-  line.end = line.pos + share < total ? line.pos + share : total;
-  if (line.pos >= line.end) return;
-  at += first_incl - first_w;
-  long long* found = scan + 3 * (NW + 1);  // row, its first place
-  if (at <= line.pos && line.pos < at + first_w) {
-    found[0] = tid;
-    found[1] = at;
-  }
-  long long before = firsts;
-  for (int r0 = C::NT; r0 < p.B && before <= line.pos; r0 += C::NT) {
-    long long w = 0;
-    if (r0 + tid < p.B) {
+  long long share = 0;  // places of a CTA's stretch
+  bool direct = false;
+  if constexpr (MODE == DEC_OWN) {
+    // Rows with few keys of their own: an item to a CTA, without a look at the
+    // others' lengths and never two beginnings one behind the other.
+    const int items = p.HKV * p.nmb;
+    direct = (long long)p.B * items <= gridDim.x && *p.share.direct != 0;
+    if (!direct && (int)blockIdx.x >= p.line_ctas) return;
+    if (direct) {
+      line.row = blockIdx.x / items;
+      if (line.row >= p.B) return;
       int s, start;
-      const int keys = row_keys<MODE>(p, r0 + tid, false, s, start);
-      w = places<C::CH, Stretch::kGap>(keys - start) * p.HKV * row_blocks<MODE, C::ROWS>(p, r0 + tid);
-    }
-    const long long incl = warp_scan(w, lane);
-    __syncthreads();  // the last sums have been read
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long first = before + incl - w;
-    for (int i = 0; i <= NW; ++i) {
-      if (i < warp) first += scan[i];
-      before += scan[i];
-    }
-    if (first <= line.pos && line.pos < first + w) {
-      found[0] = r0 + tid;
-      found[1] = first;
+      const int keys = row_keys<MODE>(p, line.row, blockIdx.x % items == 0 && tid == 0, s, start);
+      const long long cost = places<C::CH, Stretch::kGap>(keys - start);
+      if (cost == 0) return;
+      line.row0 = 0;
+      line.pos = blockIdx.x % items * cost;
+      line.end = line.pos + cost;
+      share = cost;
+      __syncthreads();  // barriers are set up
     }
   }
-  __syncthreads();
-  line.row = (int)found[0];
-  line.row0 = found[1];
+  if (!direct) {
+    const int ctas = MODE == DEC_OWN ? p.line_ctas : (int)gridDim.x;
+    // ---- the line's length and its longest row, and the row that holds this
+    // CTA's first place: one look at the lengths for up to NT rows, else two
+    long long mine = 0, most = 0, first_w = 0;
+    for (int r = tid; r < p.B; r += C::NT) {
+      int s, start;
+      const int keys = row_keys<MODE>(p, r, blockIdx.x == 0, s, start);
+      const long long cost = places<C::CH, Stretch::kGap>(keys - start);
+      const long long w = cost * p.HKV * row_blocks<MODE, C::ROWS>(p, r);
+      if (r < C::NT) first_w = w;
+      mine += w;
+      most = cost > most ? cost : most;
+    }
+    const long long first_incl = warp_scan(first_w, lane);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      mine += __shfl_xor_sync(kFull, mine, d);
+      const long long y = __shfl_xor_sync(kFull, most, d);
+      most = y > most ? y : most;
+    }
+    if (lane == 31) {
+      scan[warp] = mine;
+      scan[NW + 1 + warp] = most;
+      scan[2 * (NW + 1) + warp] = first_incl;
+    }
+    __syncthreads();
+    long long total = 0, longest = 0, at = 0, firsts = 0;
+    for (int w = 0; w <= NW; ++w) {
+      total += scan[w];
+      longest = scan[NW + 1 + w] > longest ? scan[NW + 1 + w] : longest;
+      if (w < warp) at += scan[2 * (NW + 1) + w];
+      firsts += scan[2 * (NW + 1) + w];
+    }
+    share = (total + ctas - 1) / ctas;
+    const long long few = longest / kRowParts + 1;
+    share = share > few ? share : few;
+    // not less than kLeastKeys, or a whole row where the longest has fewer
+    const long long least =
+        longest < Stretch::kGap + kLeastKeys / C::CH ? longest : Stretch::kGap + kLeastKeys / C::CH;
+    share = share > least ? share : least;
+    line.pos = share * blockIdx.x;
+    line.end = line.pos + share < total ? line.pos + share : total;
+    if (line.pos >= line.end) return;
+    at += first_incl - first_w;
+    long long* found = scan + 3 * (NW + 1);  // row, its first place
+    if (at <= line.pos && line.pos < at + first_w) {
+      found[0] = tid;
+      found[1] = at;
+    }
+    long long before = firsts;
+    for (int r0 = C::NT; r0 < p.B && before <= line.pos; r0 += C::NT) {
+      long long w = 0;
+      if (r0 + tid < p.B) {
+        int s, start;
+        const int keys = row_keys<MODE>(p, r0 + tid, false, s, start);
+        w = places<C::CH, Stretch::kGap>(keys - start) * p.HKV * row_blocks<MODE, C::ROWS>(p, r0 + tid);
+      }
+      const long long incl = warp_scan(w, lane);
+      __syncthreads();  // the last sums have been read
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      long long first = before + incl - w;
+      for (int i = 0; i <= NW; ++i) {
+        if (i < warp) first += scan[i];
+        before += scan[i];
+      }
+      if (first <= line.pos && line.pos < first + w) {
+        found[0] = r0 + tid;
+        found[1] = first;
+      }
+    }
+    __syncthreads();
+    line.row = (int)found[0];
+    line.row0 = found[1];
+
+  }
 
   const long long begin = line.pos;
   // for a CTA that gives up; the sums that stood there have been read
@@ -635,6 +661,29 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
   }
 
   // ---- streams
+  // where the CTA has one row, what its prefix left is got ready while the queries
+  // and the first keys are on their way
+  [[maybe_unused]] ShareRow rec{};
+  [[maybe_unused]] bool early = false, early_bad = false;
+  if constexpr (MODE == DEC_OWN) {
+    Seg sg;
+    Stretch ahead = line;
+    if (direct && ahead.next(p, sg) && sg.start > 0) {
+      early = true;
+      rec = p.share.rows[sg.row];
+      const int base = sg.mb * C::ROWS, R = min(C::ROWS, p.T * p.G - base);
+      if (p.cut && rec.parts > 1) {
+        auto joined = [&](int rr) {
+          const int tr = base + rr;
+          return C::JOIN_HERE ? os + rr * D
+                              : p.share.o + ((size_t)query_token<MODE>(p, sg.row, tr) * p.HQ +
+                                             sg.h * p.G + tr % p.G) * D;
+        };
+        join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
+      }
+      early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
+    }
+  }
   const int grp = warp / MW, wr = C::WROWS * (warp % MW);  // the warp's stream, its first row
   int n0 = 0;    // the segment's first chunk among the CTA's
   int seen = 0;  // units known to be on their way
@@ -687,13 +736,16 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
       if (sg.start > 0 && sg.c0 == 0) {
         // The first stream goes on from where the prefix ended; from the parts of a
         // prefix that was cut, joined by all streams where their outputs will be.
-        const ShareRow rec = p.share.rows[sg.row];
+        if (!early) rec = p.share.rows[sg.row];
         const int parts = p.cut ? rec.parts : 1;
         auto joined = [&](int rr) {
           return C::JOIN_HERE && parts > 1 ? os + rr * D : p.share.o + out_row(rr) * D;
         };
-        if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
-        skip = named_any(1, C::CT, !prefix_holds<C::CT>(p, sg, rec, tid));
+        if (!early) {
+          if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
+          early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
+        }
+        skip = named_any(1, C::CT, early_bad);
         if (skip && tid == 0)
           atomicOr(p.err, *p.share.lost != 0 ? (uint32_t)DEVERR_TIMEOUT : (uint32_t)DEVERR_PAGES);
         if (!skip && grp == 0) {
@@ -997,7 +1049,17 @@ cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStr
   const auto kernel = attn_decode_kernel<T, D, MW, NQ, MODE>;
   if (p == nullptr)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  kernel<<<C::CPS * sms, C::NT, C::SMEM, st>>>(*p, *static_cast<const KvMaps*>(maps));
+  if constexpr (MODE == DEC_OWN) {
+    // Two turns of CTAs for rows with few keys, an item each: 20 groups of 4 rows,
+    // four heads (320 items, 304 places) PLACEHOLDER
+    DecodeParams own = *p;
+    own.line_ctas = C::CPS * sms;
+    const long long items = (long long)p->B * p->HKV * p->nmb;
+    const int grid = items <= own.line_ctas || items > 2 * own.line_ctas ? own.line_ctas : (int)items;
+    kernel<<<grid, C::NT, C::SMEM, st>>>(own, *static_cast<const KvMaps*>(maps));
+  } else {
+    kernel<<<C::CPS * sms, C::NT, C::SMEM, st>>>(*p, *static_cast<const KvMaps*>(maps));
+  }
   return cudaGetLastError();
 }
 

@@ -41,7 +41,8 @@ struct SharedTcCfg {
   static constexpr int NU = D == 256 ? 2 : D == 128 ? (Q8 ? 4 : 6) : 8;  // units in the ring
   static constexpr int RAW = Q8 ? 128 * D : 0;             // the same as codes
   static constexpr int NR = !Q8 ? 0 : D == 256 ? 1 : D == 128 ? 3 : 4;
-  static constexpr int NT = Q8 ? 384 : 256;
+  static constexpr int CONV = 256;                         // threads that turn codes
+  static constexpr int NT = 256 + (Q8 ? CONV : 0);
   static constexpr int RING = QS;
   static constexpr int RAWS = RING + NU * UNIT;
   static constexpr int SCALES = RAWS + NR * RAW;           // [NR][128][2] bytes
@@ -100,8 +101,8 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
   const int R = (int)min(128ll, rows - 128ll * blk);
   bool dead = false;
   if (warp == 4 && lane == 0) {
-    for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], Q8 ? 128 : 1), mbar_init(&empty[u], 1);
-    for (int u = 0; u < C::NR; ++u) mbar_init(&rfull[u], 1), mbar_init(&rempty[u], 128);
+    for (int u = 0; u < C::NU; ++u) mbar_init(&full[u], Q8 ? C::CONV : 1), mbar_init(&empty[u], 1);
+    for (int u = 0; u < C::NR; ++u) mbar_init(&rfull[u], 1), mbar_init(&rempty[u], C::CONV);
     for (int b = 0; b < 2; ++b)
       mbar_init(&sfull[b], 1), mbar_init(&pfull[b], 128), mbar_init(&odone[b], 1);
     mbar_init(drained, 1);
@@ -158,10 +159,10 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
     mbar_arrive(qfull);
   }
 
-  // Three warpgroups at 168 registers where there are converters: the softmax's
-  // takes 232, that of the roles keeps 104.
+  // Four warpgroups at 128 registers where there are converters: the softmax's takes
+  // 208, that of the roles keeps 64, the converters 120 each.
   if (warp >= 4 && warp < 8) {
-  if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 4) {
     // ---- producer: keys and values by turns, boxes of up to 128 tokens of a page
     const int32_t* tab = p.table + (size_t)slot * p.max_pages;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
     __syncwarp();
   }
   } else if (warp < 4) {
-    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax: thread `tid` has row `tid`
     const uint32_t lane_at = (uint32_t)(32 * warp) << 16;
     float m = kNegInf;  // reference maximum (raw score)
@@ -401,9 +402,10 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       __syncwarp();
     }
   } else {
-    // ---- codes to bf16: a thread to a row of a unit
+    // ---- codes to bf16: two threads to a row of a unit
     if constexpr (Q8) {
-      const int r = tid - 256;
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      const int r = (tid - 256) % 128, half = (tid - 256) / 128;
       for (int i = 0; i < 2 * ns; ++i) {
         const int n = min(128, keys - (s0 + i / 2) * 128);
         const int ur = i % C::NR, u = i % C::NU;
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
             __uint_as_float((uint32_t)sm[C::SCALES + ur * 256 + 2 * r + (i & 1)] << 23);
         constexpr int WIDE = D == 256 ? 2 : 1, W = D / WIDE;  // a box's width
 #pragma unroll 4
-        for (int d = 0; d < D; d += 16) {
+        for (int d = D / 2 * half; d < D / 2 * (half + 1); d += 16) {
           // sixteen codes; neighbouring threads' rows by turns in their columns, or
           // all lanes would ask one bank
           const int at = (d + 16 * r) % D;

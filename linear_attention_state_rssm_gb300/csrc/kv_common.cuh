@@ -172,6 +172,7 @@ struct ShareView {
   ShareRow* rows;       // [B]
   int32_t* steps;       // [1] of 128 keys: a stretch of a prefix (attn_shared_tc.cuh)
   int32_t* segments;    // [1] stretches of all groups
+  int32_t* direct;      // [1] each row's own keys, of one key head, are one CTA's
   int32_t* seg;         // [B + 1] first stretch of a group
   int32_t* parts;       // [B] stretches of a group's block of 128 rows and a key head
   int32_t* part0;       // [B] its first place among the parts, where there are several
@@ -218,6 +219,7 @@ struct ShareView {
       s.lost = s.of + 3;
       s.steps = s.of + 4;
       s.segments = s.of + 5;
+      s.direct = s.of + 6;
       s.segs = reinterpret_cast<ShareSeg*>(segs);
       s.rows = reinterpret_cast<ShareRow*>(rec);
       s.seg = reinterpret_cast<int32_t*>(seg);
@@ -257,6 +259,7 @@ struct DecodeParams {
   long long qs;
   long long page0;  // the layer's first page among all layers'
   int B, T, HQ, HKV, G, n_slots, n_pages, max_pages, shift;
+  int line_ctas;  // DEC_OWN: CTAs that the line is split over
   int cut;      // DEC_OWN: prefixes may be in parts (attn_shared_tc.cuh)
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off

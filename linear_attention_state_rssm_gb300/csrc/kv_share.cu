@@ -21,6 +21,7 @@ namespace rssm {
 namespace {
 
 constexpr int kShareThreads = 1024;
+constexpr int kMostOwn = 1024;  // keys that a CTA takes of one row's own at most, if it has one row
 constexpr int kLeastSteps = 4;  // of 128 keys: a stretch, but for a prefix's last
 
 struct PlanShareParams {
@@ -61,7 +62,7 @@ __device__ __forceinline__ int scan_of(int x, int* sums, int tid, int& total) {
 __global__ void __launch_bounds__(kShareThreads)
     plan_share_kernel(const __grid_constant__ PlanShareParams p) {
   __shared__ int sums[32];
-  __shared__ int all_cut, all_whole;
+  __shared__ int all_cut, all_whole, longest;
   __shared__ unsigned long long work;  // steps of 128 keys of all blocks
   const int tid = threadIdx.x;
   int32_t* full = p.v.order;                // whole committed pages, until phase 3
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kShareThreads)
     p.v.of[1] = p.T;
     *p.v.lost = 0;
     work = 0;
+    longest = 0;
   }
   // ---- 1: each row's whole pages, and the first row that begins with its page
   auto first_page = [&](int r) {
@@ -255,6 +257,14 @@ __global__ void __launch_bounds__(kShareThreads)
     p.v.prefix[r] = p.v.group_keys[g];
     p.v.group[r] = g;
   }
+  // ---- 6: whether a CTA for each row and key head is the better split of the rows'
+  // own keys. Slots grow: the answer is a matter of speed alone.
+  for (int r = tid; r < p.B; r += kShareThreads) {
+    const int s = p.slot[r];
+    if (s >= 0 && s < p.n_slots) atomicMax(&longest, p.length[s] + p.T - p.v.prefix[r]);
+  }
+  __syncthreads();
+  if (tid == 0) *p.v.direct = longest <= kMostOwn;
 }
 
 }  // namespace
