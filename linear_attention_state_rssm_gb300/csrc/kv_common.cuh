@@ -1,8 +1,9 @@
 // Parameters and launches of the full-attention layers' operators: the paged
-// key-value cache (kv_pages.cu), the rotary append (kv_append.cu), pages read
-// back in a row (kv_gather.cu), attention of new tokens over the pages
-// (attn_decode.cu) and of whole prompts (attn_prompt.cu, attn_prompt_tc.cu).
-// Internal to librssm.
+// key-value cache (kv_pages.cu), the rotary append (kv_append.cu,
+// kv_append_norm.cu), pages read back in a row (kv_gather.cu), attention of new
+// tokens over the pages (attn_decode.cu), with prefixes that rows share
+// (kv_share.cu, attn_shared_tc.cu), and of whole prompts (attn_prompt.cu,
+// attn_prompt_tc.cu). Internal to librssm.
 #pragma once
 
 #include "rssm_common.cuh"
@@ -288,6 +289,7 @@ cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, in
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);
+cudaError_t kv_append_norm_launch(const AppendParams& p, cudaStream_t st);
 cudaError_t kv_gather_launch(const GatherParams& p, int num_sms, cudaStream_t st);
 cudaError_t attn_decode_prepare(int D, int dt, bool quant);
 // tensor maps of the pool (kKvMapBytes, 64-byte aligned) and the launch with them

@@ -6,7 +6,8 @@
 //
 // Bytes bound it. A page keeps a head's tokens side by side, the row a token's
 // heads: a CTA takes a block of tokens and all heads, so both sides see runs of
-// D values, and its threads have kAhead loads each on their way.
+// D values, and its threads have kAhead loads of keys and of values each on their
+// way.
 #include "kv_common.cuh"
 #include "kv_tokens.cuh"
 
@@ -14,15 +15,16 @@ namespace rssm {
 
 namespace {
 
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
 constexpr int kGatherTokens = 16;  // of a CTA at most
-constexpr int kAhead = 4;
+constexpr int kAhead = 2;
 
 // Where token `tok` begins in the layer's pages (its first head), in units of D
 // values; -1 where it is not read.
-__device__ __forceinline__ long long gather_place(const GatherParams& p, int tok) {
+__device__ __forceinline__ long long gather_place(const GatherParams& p, const int32_t* cu,
+                                                  int tok) {
   int r, i;
-  if (!token_row(p.cu, p.B, p.T, p.N, tok, r, i)) return -1;
+  if (!token_row(cu, p.B, p.T, p.N, tok, r, i)) return -1;
   const int s = p.slot[r];
   if (s < 0) return -1;
   uint32_t bad = 0;
@@ -51,7 +53,8 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(kGatherThreads)
     kv_gather_kernel(const __grid_constant__ GatherParams p, int tokens) {
   using V = Vec16<T>;
-  constexpr int E = V::E;
+  constexpr int SIZE = E4M3 ? 1 : (int)sizeof(T);  // of a page's value
+  constexpr int E = 16 / SIZE;                     // values of a load
   __shared__ long long places[kGatherTokens];
   const int tid = threadIdx.x;
   if (p.cu != nullptr && blockIdx.x == 0) {
@@ -61,48 +64,57 @@ __global__ void __launch_bounds__(kGatherThreads)
   }
   const int tok0 = blockIdx.x * tokens;
   const int n = min(tokens, p.N - tok0);
-  if (tid < n) places[tid] = gather_place(p, tok0 + tid);
+  __shared__ int32_t offsets[kGatherThreads];
+  const int32_t* cu = copy_offsets<kGatherThreads>(p.cu, p.B, offsets, tid);
+  if (p.cu != nullptr) __syncthreads();
+  if (tid < n) places[tid] = gather_place(p, cu, tok0 + tid);
   __syncthreads();
-  // 16 bytes of the output a thread: [which][token][head][unit]
-  const int units = p.D / E, row = p.HKV * units, all = n * row;
-  for (int which = 0; which < 2; ++which) {
-    T* out = static_cast<T*>(which ? p.v_out : p.k_out);
-    if (out == nullptr) continue;
-    const unsigned char* pages = which ? p.vp : p.kp;
-    uint4* to = reinterpret_cast<uint4*>(out + (size_t)tok0 * p.HKV * p.D);
-    for (int i0 = tid; i0 < all; i0 += kGatherThreads * kAhead) {
-      uint4 x[kAhead];
-      unsigned char sc[kAhead];
-      bool live[kAhead];
+  // a thread has one place in the heads and goes from (token, head) to the next
+  const int units = p.D / E;  // a power of two, at most 64
+  const int u = tid & (units - 1), step = kGatherThreads / units;
+  const int dt = step / p.HKV, dh = step % p.HKV;
+  int t = tid / units / p.HKV, h = tid / units % p.HKV;
+  const bool want_k = p.k_out != nullptr, want_v = p.v_out != nullptr;
+  while (t < n) {
+    uint4 k[kAhead], v[kAhead];
+    uint32_t sc[kAhead];
+    long long to[kAhead];  // of the outputs, in heads; -1: nothing
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k * kGatherThreads;
-        live[k] = i < all && places[i / row] >= 0;
-        if (live[k]) {
-          const int h = i % row / units, u = i % units;
-          const size_t at = (size_t)places[i / row] + ((size_t)h << p.shift);
-          if constexpr (E4M3) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(pages + at * p.D) + u);
-            x[k].x = c.x, x[k].y = c.y;
-            sc[k] = __ldg(p.scales + 2 * at + which);
-          } else {
-            x[k] = __ldg(reinterpret_cast<const uint4*>(pages + at * p.D * sizeof(T)) + u);
-          }
-        }
+    for (int i = 0; i < kAhead; ++i) {
+      to[i] = -1;
+      if (t < n && places[t] >= 0) {
+        const size_t at = (size_t)places[t] + ((size_t)h << p.shift);
+        to[i] = (long long)(tok0 + t) * p.HKV + h;
+        const size_t from = at * p.D * SIZE;
+        if (want_k) k[i] = __ldcs(reinterpret_cast<const uint4*>(p.kp + from) + u);
+        if (want_v) v[i] = __ldcs(reinterpret_cast<const uint4*>(p.vp + from) + u);
+        if constexpr (E4M3) sc[i] = __ldg(reinterpret_cast<const uint16_t*>(p.scales) + at);
       }
+      t += dt;
+      h += dh;
+      if (h >= p.HKV) h -= p.HKV, ++t;
+    }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k * kGatherThreads;
-        if (live[k]) {
-          if constexpr (E4M3) {
-            static_assert(!E4M3 || E == 8, "sixteen-bit outputs");
-            float v[8];
-            const float up = __uint_as_float((uint32_t)sc[k] << 23);
-            e4m3x4_values(x[k].x, up, v);
-            e4m3x4_values(x[k].y, up, v + 4);
-            x[k] = V::pack(v);
+    for (int i = 0; i < kAhead; ++i) {
+      if (to[i] < 0) continue;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        if (!(which ? want_v : want_k)) continue;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(which ? p.v_out : p.k_out) +
+                                              to[i] * p.D + u * E);
+        const uint4 x = which ? v[i] : k[i];
+        if constexpr (E4M3) {
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const float up = __uint_as_float((sc[i] >> (8 * which) & 0xffu) << 23);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float f[8];
+            e4m3x4_values(w[2 * y], up, f);
+            e4m3x4_values(w[2 * y + 1], up, f + 4);
+            out[y] = V::pack(f);
           }
-          to[i] = x[k];
+        } else {
+          out[0] = x;
         }
       }
     }

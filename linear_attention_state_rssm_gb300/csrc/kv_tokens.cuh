@@ -1,5 +1,5 @@
-// Vectors of 16 bytes as fp32 values, the row of a packed token, and the e4m3
-// values of quantised pages.
+// Vectors of 16 bytes as fp32 values, the row and the place of a packed token, and
+// the e4m3 values of quantised pages.
 //
 // A token's keys (or values) of one head are held as e4m3 values and a power of
 // two: with a = max |x_i| over the finite ones, e is the least whole number with
@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 
 #include "attn_core.cuh"
+#include "kv_common.cuh"
 
 namespace rssm {
 
@@ -53,14 +54,12 @@ __device__ __forceinline__ int scale_exponent(float a) {
 __device__ __forceinline__ float power_of(int e) {  // 2^e, e in [-126, 127]
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
-// four values, e4m3 of x 2^-e; the finite ones are at most 448 2^e or saturate
+// four values, e4m3 of x 2^-e (no infinities among x); beyond 448 2^e they saturate
 __device__ __forceinline__ uint32_t e4m3x4(const float* x, float down) {
-  float y[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    y[i] = fabsf(x[i]) == INFINITY ? __uint_as_float(0x7fffffffu) : x[i] * down;
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * down, x[1] * down),
+                                               __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * down, x[3] * down),
+                                               __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
 // two e4m3 values as fp16, exactly
@@ -92,6 +91,73 @@ __device__ __forceinline__ bool token_row(const int32_t* cu, int B, int T, int N
   const int first = cu[r], end = cu[r + 1];
   i = tok - first;
   return first >= 0 && tok >= first && tok < end && end <= N;
+}
+
+// The rows' offsets in shared memory where a CTA's threads can take one each: a
+// search there costs no trips to memory. All threads; the barrier is the caller's.
+template <int THREADS>
+__device__ __forceinline__ const int32_t* copy_offsets(const int32_t* cu, int B, int32_t* room,
+                                                       int tid) {
+  if (cu == nullptr || B >= THREADS) return cu;
+  if (tid <= B) room[tid] = cu[tid];
+  return room;
+}
+
+struct TokenPlace {
+  size_t off;             // bytes of its first head within the layer's pages
+  int pos[kMaxRopeAxes];
+  int live;
+};
+
+// Row, page and positions of token `tok`; token_bytes: of one head in the pages.
+// cu: the call's offsets, or a copy of them.
+__device__ __forceinline__ TokenPlace place_of(const AppendParams& p, const int32_t* cu, int tok,
+                                               int token_bytes) {
+  TokenPlace t{};
+  int r, i;  // the token's row and place in its window
+  if (!token_row(cu, p.B, p.T, p.N, tok, r, i)) return t;
+  const int s = p.slot[r];
+  // looked up beside the slot, not behind its page
+  if (p.rope != nullptr && p.positions != nullptr) {
+#pragma unroll
+    for (int a = 0; a < kMaxRopeAxes; ++a) {
+      if (a < p.axes) t.pos[a] = p.positions[(size_t)a * p.N + tok];
+    }
+  }
+  if (s < 0) return t;
+  uint32_t bad = 0;
+  int len = 0;
+  if (s >= p.n_slots) {
+    bad = DEVERR_SLOT;
+  } else {
+    len = p.length[s];
+    const int held = p.held[s];
+    if (len < 0) {
+      bad = DEVERR_CURSOR;
+    } else if (held < 0 || held > p.max_pages || (long long)len + i >= ((long long)held << p.shift)) {
+      bad = DEVERR_PAGES;
+    }
+  }
+  int page = 0;
+  if (bad == 0) {
+    page = p.table[(size_t)s * p.max_pages + ((len + i) >> p.shift)];
+    if (page < 0 || page >= p.n_pages) bad = DEVERR_PAGES;
+  }
+  if (p.rope != nullptr && bad == 0) {
+#pragma unroll
+    for (int a = 0; a < kMaxRopeAxes; ++a) {
+      if (a >= p.axes || p.positions == nullptr) t.pos[a] = len + i;
+      if (a < p.axes && (t.pos[a] < 0 || t.pos[a] >= p.max_pos)) bad = DEVERR_POSITION;
+    }
+  }
+  if (bad) {
+    atomicOr(p.err, bad);
+    return t;
+  }
+  t.off = ((size_t)page * p.HKV << p.shift) * token_bytes +
+          (size_t)((len + i) & ((1 << p.shift) - 1)) * token_bytes;
+  t.live = 1;
+  return t;
 }
 
 }  // namespace rssm
