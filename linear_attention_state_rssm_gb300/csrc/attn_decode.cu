@@ -66,16 +66,12 @@ cudaError_t attn_decode_launch(const DecodeParams& p, const void* maps, int D, i
                              : plain(&p, maps, D, dt, rows, sms, st);
 }
 
-// Shared prefixes: on the 5th-generation tensor cores where they take the pages,
-// else by the kernel of single rows with a group's query rows in its blocks.
+// Shared prefixes: on the 5th-generation tensor cores, fp32 ones by the kernel of
+// single rows with a group's query rows in its blocks.
 cudaError_t attn_shared_prepare(int D, int dt, bool quant) {
-  cudaError_t e = cudaSuccess;
-  if (attn_shared_tc_serves(dt, quant)) {
-    e = attn_shared_tc_prefix(nullptr, nullptr, D, dt, quant, nullptr);
-  } else {
-    e = quant ? attn_shared_prefix_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
-              : attn_shared_prefix(nullptr, nullptr, D, dt, 0, 0, nullptr);
-  }
+  const cudaError_t e = dt == DT_F32
+                            ? attn_shared_prefix(nullptr, nullptr, D, dt, 0, 0, nullptr)
+                            : attn_shared_tc_prefix(nullptr, nullptr, D, dt, quant, nullptr);
   if (e != cudaSuccess) return e;
   return quant ? attn_shared_own_quant(nullptr, nullptr, D, dt, 0, 0, nullptr)
                : attn_shared_own(nullptr, nullptr, D, dt, 0, 0, nullptr);
@@ -90,15 +86,10 @@ cudaError_t attn_shared_launch(DecodeParams p, const void* maps, const void* tc_
     const int n = attn_decode_block_rows(D, dt, quant, rows < 4096 ? (int)rows : 4096);
     return n == 32 && !quant ? (D == 256 ? 48 : 64) : n;
   };
-  cudaError_t e;
-  if (attn_shared_tc_serves(dt, quant)) {
-    p.cut = 1;
-    e = attn_shared_tc_prefix(&p, tc_maps, D, dt, quant, st);
-  } else {
-    const int rows = block((long long)p.B * p.T * p.G);
-    e = quant ? attn_shared_prefix_quant(&p, maps, D, dt, rows, sms, st)
-              : attn_shared_prefix(&p, maps, D, dt, rows, sms, st);
-  }
+  p.cut = dt != DT_F32;
+  const cudaError_t e =
+      dt == DT_F32 ? attn_shared_prefix(&p, maps, D, dt, block((long long)p.B * p.T * p.G), sms, st)
+                   : attn_shared_tc_prefix(&p, tc_maps, D, dt, quant, st);
   if (e != cudaSuccess) return e;
   const int own = block(p.T * p.G);
   p.nmb = (p.T * p.G + own - 1) / own;

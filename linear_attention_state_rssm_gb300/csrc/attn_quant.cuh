@@ -64,6 +64,13 @@ __device__ __forceinline__ void permute_words(const uint32_t (&w)[8], uint4& lo,
   hi = make_uint4(w[1], w[3], w[5], w[7]);
 }
 
+// a for a row whose largest is `top`: 2^-a brings that into [2^13, 2^14) (a row of
+// zeros stays as it is, one of values under 2^-87 smaller).
+__device__ __forceinline__ int query_exponent(float top) {
+  const int a = top > 0.f ? (int)(__float_as_uint(top) >> 23) - 127 - 13 : 0;
+  return a < -100 ? -100 : a;
+}
+
 // One row of q in shared memory (swizzled units of a block of ROWS rows), by D /
 // 16 neighbouring lanes, `part` of them: scaled, permuted, in place. Returns 2^a.
 template <typename T, int D, int ROWS>
@@ -82,9 +89,7 @@ __device__ __forceinline__ float scale_query(unsigned char* qs, int row, int par
   }
 #pragma unroll
   for (int d = 1; d < L; d <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-  // largest in [2^13, 2^14); a row of zeros (or of values under 2^-87) as it is
-  int a = top > 0.f ? (int)(__float_as_uint(top) >> 23) - 127 - 13 : 0;
-  a = a < -100 ? -100 : a;
+  const int a = query_exponent(top);
   const float down = power_of(-a);
   uint32_t w[8];
 #pragma unroll

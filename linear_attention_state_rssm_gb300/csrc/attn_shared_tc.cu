@@ -32,10 +32,6 @@ cudaError_t attn_shared_tc_maps(void* maps, const void* k, const void* v, long l
   return cudaSuccess;
 }
 
-bool attn_shared_tc_serves(int dt, bool quant) {
-  return quant ? dt == DT_BF16 : dt != DT_F32;
-}
-
 cudaError_t attn_shared_tc_prefix(const DecodeParams* p, const void* maps, int D, int dt,
                                   bool quant, cudaStream_t st) {
   // every block of a group has a part behind the last of an even split
@@ -45,9 +41,11 @@ cudaError_t attn_shared_tc_prefix(const DecodeParams* p, const void* maps, int D
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   }
   const int n = (int)ctas;
-  if (quant) return shared_tc_any<__nv_bfloat16, true>(p, maps, D, n, st);
-  if (dt == DT_BF16) return shared_tc_any<__nv_bfloat16, false>(p, maps, D, n, st);
-  return shared_tc_any<__half, false>(p, maps, D, n, st);
+  if (dt == DT_BF16)
+    return quant ? shared_tc_any<__nv_bfloat16, true>(p, maps, D, n, st)
+                 : shared_tc_any<__nv_bfloat16, false>(p, maps, D, n, st);
+  return quant ? shared_tc_any<__half, true>(p, maps, D, n, st)
+               : shared_tc_any<__half, false>(p, maps, D, n, st);
 }
 
 }  // namespace rssm

@@ -103,7 +103,7 @@ rssm_status make_handle(const rssm_kv_config* cfg, const rssm_kv_buffers* buf, v
     e = attn_decode_maps(h->maps, buf->k_pages, buf->v_pages,
                          (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
                          cfg->D, cfg->dtype, scales != nullptr, cfg->page_size);
-  if (e == cudaSuccess && attn_shared_tc_serves(cfg->dtype, scales != nullptr))
+  if (e == cudaSuccess && cfg->dtype != RSSM_F32)
     e = attn_shared_tc_maps(h->tc_maps, buf->k_pages, buf->v_pages,
                             (long long)cfg->n_layers * cfg->n_pages * cfg->HKV * cfg->page_size,
                             cfg->D, cfg->dtype, scales != nullptr, cfg->page_size);

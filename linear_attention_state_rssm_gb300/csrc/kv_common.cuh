@@ -306,15 +306,12 @@ int attn_decode_block_rows(int D, int dt, bool quant, int rows);  // rows of a b
 cudaError_t attn_shared_prepare(int D, int dt, bool quant);
 cudaError_t attn_shared_launch(DecodeParams p, const void* maps, const void* tc_maps, int D,
                                int dt, int num_sms, cudaStream_t st);
-bool attn_shared_tc_serves(int dt, bool quant);
 cudaError_t attn_shared_tc_maps(void* maps, const void* k, const void* v, long long rows, int D,
                                 int dt, bool quant, int page_size);
 cudaError_t attn_shared_tc_prefix(const DecodeParams* p, const void* maps, int D, int dt,
                                   bool quant, cudaStream_t st);
 cudaError_t attn_shared_prefix(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                                int sms, cudaStream_t st);
-cudaError_t attn_shared_prefix_quant(const DecodeParams* p, const void* maps, int D, int dt,
-                                     int rows, int sms, cudaStream_t st);
 cudaError_t attn_shared_own(const DecodeParams* p, const void* maps, int D, int dt, int rows,
                             int sms, cudaStream_t st);
 cudaError_t attn_shared_own_quant(const DecodeParams* p, const void* maps, int D, int dt, int rows,

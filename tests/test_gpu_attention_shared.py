@@ -41,7 +41,8 @@ class Batch:
     """Slots by groups: (prefix tokens, own tokens of each member); a member's table begins
     with the pages that the prefix fills. Pages hold random tokens everywhere."""
 
-    def __init__(self, rng, groups, T, HQ, HKV, D, dtype, pages, page, scale=None):
+    def __init__(self, rng, groups, T, HQ, HKV, D, dtype, pages, page, scale=None, powers=(-2, 2),
+                 key_powers=(0, 0)):
         from linear_attention_state_rssm_gb300.store import KVCache
         self.T, self.dtype = T, dtype
         self.lens, self.tables, used = [], [], 0
@@ -74,7 +75,8 @@ class Batch:
                 pool[1] = t.cuda()
                 self.values.append(t.double().numpy())
             else:
-                x = x * 2.0 ** rng.uniform(-2, 2, x.shape[:3])[..., None] if which else x
+                lo, hi = powers if which else key_powers
+                x = x * 2.0 ** rng.uniform(lo, hi, x.shape[:3])[..., None]
                 codes, scale_ = quant.quantise(x)
                 pool[1].view(torch.uint8).copy_(torch.from_numpy(codes))
                 c.page_scales[1, ..., which] = torch.from_numpy(scale_).cuda()
@@ -93,16 +95,17 @@ class Batch:
 
 def check(got, want, mass, dtype):
     got = got.double().cpu().numpy()
-    off, lim = np.abs(got - want), REL[dtype] * mass + 1e-7
+    floor = 1e-7 if dtype == "f32" else {"f16": 2.0 ** -24, "bf16": 2.0 ** -126}[dtype]
+    off, lim = np.abs(got - want), REL[dtype] * mass + floor   # the types' smallest steps
     assert np.all(off <= lim), (off / lim).max()
 
 
-def run(kind, groups, T, HQ, HKV, D, page, seed, null=(), shuffle=True, strided=False):
+def run(kind, groups, T, HQ, HKV, D, page, seed, null=(), shuffle=True, strided=False, by=1.2, **kw):
     dtype, pages = kind
     rng = np.random.default_rng([seed, D, T, HQ])
-    b = Batch(rng, groups, T, HQ, HKV, D, dtype, pages, page)
+    b = Batch(rng, groups, T, HQ, HKV, D, dtype, pages, page, **kw)
     B = len(b.lens)
-    q, qd = draw(rng, (B * T, HQ + (2 if strided else 0), D), dtype, 1.2)
+    q, qd = draw(rng, (B * T, HQ + (2 if strided else 0), D), dtype, by)
     q, qd = q[:, :HQ], qd[:, :HQ]
     perm = rng.permutation(B) if shuffle else np.arange(B)
     slots = [-1 if r in null else int(perm[r]) for r in range(B)]
@@ -117,7 +120,8 @@ def run(kind, groups, T, HQ, HKV, D, page, seed, null=(), shuffle=True, strided=
     off = torch.from_numpy(~on)
     assert (o[off] == SENTINEL).all() and (lse[off] == SENTINEL).all()
     check(o[~off], want[on], mass[on], dtype)
-    assert np.abs(lse.double().cpu().numpy()[on] - wlse[on]).max(initial=0) <= LSE
+    gl = lse.double().cpu().numpy()[on]
+    assert np.all(np.abs(gl - wlse[on]) <= LSE + 1e-6 * np.abs(wlse[on]))
     for _ in range(2):   # the same sums whatever the order of arrival, or of a plan's members
         again = torch.empty_like(o)
         b.c.rssm_kv_share(ints(slots), T, share)
@@ -169,6 +173,19 @@ def test_groups_of_many_rows(kind):
     groups = [(int(n), [int(x) for x in rng.integers(0, 30, m)])
               for n, m in zip(rng.integers(0, 90, 300), rng.integers(1, 8, 300))]
     run(kind, groups, 1, 2, 1, 64, 16, 46, null=(0, 7, 1000))
+
+
+@pytest.mark.parametrize("powers", [(-60, -45), (-12, 12), (-25, 25), (30, 50)])
+def test_quantised_values_of_very_different_sizes(powers):
+    """Powers of two far apart within a step of a prefix, and from step to step."""
+    run(("bf16", "e4m3"), [(700, [0, 40, 3]), (300, [5, 60])], 2, 4, 2, 64, 16, 58, powers=powers)
+
+
+@pytest.mark.parametrize("by,keys", [(1e-20, (40, 60)), (1e20, (-75, -65)), (0.3, (-9, 3)),
+                                     (0.0, (0, 0))])
+def test_quantised_keys_and_queries_of_very_different_sizes(by, keys):
+    run(("bf16", "e4m3"), [(700, [0, 40, 3]), (300, [5, 60])], 2, 4, 2, 128, 16, 59, by=by,
+        key_powers=keys)
 
 
 def test_nothing_shared_and_one_row():
