@@ -627,9 +627,10 @@ rssm_status rssm_kv_append_norm(rssm_kv_handle *h, int32_t layer, const void *q,
  * [N][HKV][D] in dtype, 16-byte aligned, either may be null (both: nothing is
  * done), take tokens [first[r], first[r] + T_r) of slot[r] (first: device
  * int32[B], null: 0) at [cu_seqlens[r], cu_seqlens[r+1]), or with cu_seqlens
- * null at [r T, (r + 1) T) of N = B T. Quantised pages give the values that their codes stand for,
- * rounded to dtype. That is the part of a prompt's keys that the cache holds
- * already, as rssm_attn_prefill reads it. A slot may be named by several rows.
+ * null at [r T, (r + 1) T) of N = B T. Quantised pages give the values that
+ * their codes stand for, rounded to dtype. That is the part of a prompt's keys
+ * that the cache holds already, as rssm_attn_prefill reads it. A slot may be
+ * named by several rows.
  * A token that its slot's pages do not hold, or before the first one, sets
  * RSSM_DEVERR_PAGES: it is skipped, its outputs left as they are. Offsets that
  * decrease or leave [0, N] set RSSM_DEVERR_SEQLEN and skip the row.
@@ -662,7 +663,7 @@ rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
  * begin with the same page, as many pages as all of them begin with and have
  * committed whole. It writes them to `share`, a device buffer of the caller's of
  * rssm_kv_share_bytes(B, T) bytes, 16-byte aligned, which also takes what the
- * attention holds between its two launches: a buffer serves one call at a time.
+ * attention holds between its two launches.
  * The rows may be in any order; rows that share nothing are served as by
  * rssm_attn_decode, whose arguments, contract and results these are (sums in
  * another order).
@@ -670,10 +671,11 @@ rssm_status rssm_attn_decode(rssm_kv_handle *h, int32_t layer, const void *q,
  * The plan is of B, T and the rows' slots. It stays true while the slots grow,
  * and through rssm_kv_compact; it has to be made anew where a row has another
  * slot, and where a slot was released or forked into; rows whose slot has become
- * null are left out. A row whose table does not begin with its group's pages any more, or whose slot has become shorter
- * than its prefix, sets RSSM_DEVERR_PAGES and is skipped, and so is every row
- * where B or T are not the plan's. Rows with a null slot, or one that is
- * refused, are left out by rssm_kv_share, which sets no error bits. Where a wait
+ * null are left out. A row whose table does not begin with its group's pages any
+ * more, or whose slot has become shorter than its prefix, sets
+ * RSSM_DEVERR_PAGES and is skipped, and so is every row where B or T are not the
+ * plan's, or its cache had other heads or another page size. Rows with a null
+ * slot, or one that is refused, are left out by rssm_kv_share, which sets no error bits. Where a wait
  * runs out over a prefix (RSSM_DEVERR_TIMEOUT), the rows of groups are skipped
  * until rssm_kv_share is called again.
  */

@@ -30,15 +30,21 @@
 // 160, 113 us; the gap on the line 93 for the windows; this ring 86; rows of a
 // join loaded side by side and 32 keys a step 68.
 //
-// Quantised pages (Q): the same with e4m3 boxes and, beside each, the 32 bytes of
-// its sixteen keys' powers of two (attn_quant.cuh).
+// Quantised pages (Q): the same with e4m3 boxes and, beside each, two bytes a key
+// with its powers of two (attn_quant.cuh); blocks of 8 rows too. Measured: 56 rows
+// of 1 to 8 k tokens, 16/4 heads of 256: 78 us, 5.6 TB/s (83% of the copy rate);
+// two rows of 109 to 131 k tokens, 32/8 heads of 128: 89 us, 5.8 TB/s (86%). What a
+// step costs besides its bytes holds them back: half the bytes, as many keys.
+// Windows of 8 tokens (32 rows to a head): 80 us, 1.9 TB/s, bound by two warps'
+// steps per stream, one instruction after the other.
 //
-// Prefixes that rows share (kv_share.cuh) take two launches of this kernel.
-// PREFIX: a line of groups instead of rows; the query rows of all of a group's
-// members are the rows of its blocks, all of the prefix is seen by all, and what
-// is left is the running maximum, sum and output of every query row, in fp32.
-// OWN: each row from the end of its prefix on, its first stream beginning with
-// what PREFIX left. Rows without a group begin at their first key.
+// Prefixes that rows share (kv_share.cu) come in two launches. PREFIX, here for
+// fp32 alone (else attn_shared_tc.cuh): a line of groups instead of rows; the query
+// rows of all of a group's members are the rows of its blocks, all of the prefix is
+// seen by all, and what is left is the running maximum, sum and output of every
+// query row, in fp32. OWN: each row from the end of its prefix on, its first stream
+// beginning with what the prefix left. Rows without a group begin at their first
+// key.
 #pragma once
 
 #include "attn_core.cuh"
@@ -354,6 +360,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
   constexpr bool Q = NQ > 0;
   using Stretch = Line<C::CH, MODE, C::ROWS>;
   constexpr int NG = C::NG, NW = C::NW;
+  static_assert(MODE != DEC_PREFIX || (C::F32 && NG > 1), "else on the tensor cores");
   extern __shared__ unsigned char sm_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~(uintptr_t)1023);
@@ -490,7 +497,6 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     __syncthreads();
     line.row = (int)found[0];
     line.row0 = found[1];
-
   }
 
   const long long begin = line.pos;
@@ -848,7 +854,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
           part[C::ROWS * D + rr] = mx;
           part[C::ROWS * (D + 1) + rr] = sum;
         } else if constexpr (MODE == DEC_PREFIX) {
-          if (NG > 1 ? flag[0] == 0 : !dead) p.share.ml[out_row(rr)] = make_float2(mx, sum);
+          if (flag[0] == 0) p.share.ml[out_row(rr)] = make_float2(mx, sum);
         } else if (p.lse != nullptr && (NG > 1 ? flag[0] == 0 : !dead) && !skip) {
           p.lse[out_row(rr)] = lse_of(mx, sum);
         }
@@ -865,11 +871,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
             const auto [a, b] = w.pair(i, e);
             const int d = W::dim(i, lane);
             if (whole) {
-              if constexpr (MODE == DEC_PREFIX) {
-                *reinterpret_cast<float2*>(p.share.o + at + d) = make_float2(a, b);
-              } else {
-                store2(static_cast<T*>(p.o) + at + d, a * inv[e], b * inv[e]);
-              }
+              store2(static_cast<T*>(p.o) + at + d, a * inv[e], b * inv[e]);
             } else {
               *reinterpret_cast<float2*>(part + rr * D + d) = make_float2(a, b);
             }
@@ -1040,7 +1042,6 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
   }
 }
 
-
 // The kernels of one page type, by head size and warps of a stream: launches, or,
 // with p null, only asks for their shared memory.
 template <typename T, int NQ, int MODE, int D, int MW>
@@ -1050,8 +1051,9 @@ cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStr
   if (p == nullptr)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if constexpr (MODE == DEC_OWN) {
-    // Two turns of CTAs for rows with few keys, an item each: 20 groups of 4 rows,
-    // four heads (320 items, 304 places) PLACEHOLDER
+    // Up to two turns of CTAs for rows with few keys, an item each: 20 groups of 4
+    // rows with four heads, 320 items for 304 places, 189 us of four layers, by the
+    // line 198.
     DecodeParams own = *p;
     own.line_ctas = C::CPS * sms;
     const long long items = (long long)p->B * p->HKV * p->nmb;

@@ -24,7 +24,7 @@
 // instruction are keys, or dimensions, all of them of use, and its eight columns
 // queries, of which a single token has few. A code is converted once whatever
 // the number of queries is. (With queries as the rows, sixteen for four in use,
-// 56 rows of 1 to 8 k tokens, 16/4 heads of 256, took 100 us; so 73.)
+// 56 rows of 1 to 8 k tokens, 16/4 heads of 256, took 100 us; so 78.)
 //
 // Eight-bit matrices are loaded as if they were of 16-bit pairs. A lane's word of
 // keys is then four neighbouring dimensions of one key, which serve as k = 2t,

@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
 
   // Four warpgroups at 128 registers where there are converters: the softmax's takes
   // 208, that of the roles keeps 64, the converters 120 each.
-  if (warp >= 4 && warp < 8) {
-  if constexpr (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  if constexpr (Q8) {
+    if (warp >= 4 && warp < 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+  }
   if (warp == 4) {
     // ---- producer: keys and values by turns, boxes of up to 128 tokens of a page
     const int32_t* tab = p.table + (size_t)slot * p.max_pages;
@@ -328,7 +329,6 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       tc_wait(drained, 0, late);
     }
     __syncwarp();
-  }
   } else if (warp < 4) {
     if constexpr (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax: thread `tid` has row `tid`
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       }
       __syncwarp();
     }
-  } else {
+  } else if (warp >= 8) {
     // ---- codes to fp16, two threads to a row of a unit. (Half the warps to the keys,
     // half to the values is no faster: 198 for 190 us of 20 groups; shared memory, which
     // feeds the products beside 96 KB a step here, is what they wait for.)

@@ -467,7 +467,7 @@ rssm_status rssm_kv_share_bytes(const rssm_kv_config* cfg, int32_t B, int32_t T,
   if (st != RSSM_OK) return st;
   if (out == nullptr || B < 0 || B > kMaxRows || T < 1) return RSSM_ERR_INVALID_ARG;
   if (T > 64) return RSSM_ERR_UNSUPPORTED;
-  *out = ShareView::lay(nullptr, B, T, cfg->HQ, cfg->HKV, cfg->D, nullptr);
+  *out = ShareView::lay(nullptr, B, T, cfg->HQ, cfg->HKV, cfg->D, 0, nullptr);
   return RSSM_OK;
 }
 
@@ -483,7 +483,7 @@ rssm_status rssm_kv_share(rssm_kv_handle* h, const int32_t* slot, int32_t B, int
   p.B = B;
   p.T = T;
   ShareView v;
-  ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.HKV, h->cfg.D, &v);
+  ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.HKV, h->cfg.D, h->shift, &v);
   return from_cuda(kv_share_launch(v, p, h->cfg.HKV, h->cfg.HQ / h->cfg.HKV,
                                    static_cast<cudaStream_t>(stream)));
 }
@@ -501,7 +501,7 @@ rssm_status rssm_attn_decode_shared(rssm_kv_handle* h, int32_t layer, const void
       share == nullptr || !aligned16(share))
     return RSSM_ERR_INVALID_ARG;
   DecodeParams p = decode_params(h, layer, q, q_stride, slot, B, T, o, lse);
-  ShareView::lay(share, B, T, c.HQ, c.HKV, c.D, &p.share);
+  ShareView::lay(share, B, T, c.HQ, c.HKV, c.D, h->shift, &p.share);
   return from_cuda(
       attn_shared_launch(p, h->maps, h->tc_maps, c.D, c.dtype, h->num_sms,
                          static_cast<cudaStream_t>(stream)));

@@ -139,7 +139,7 @@ constexpr int kShareSplit = kMaxSms;  // stretches that prefixes are cut into, a
 // and what the first of the two launches leaves for the second.
 // Stretches that a call can have: an even split over the SMs, and one more for
 // every block of 128 rows of a group (of two members at least) and key head.
-__host__ __device__ inline long long share_segments(int B, int T, int G, int HKV) {
+inline long long share_segments(int B, int T, int G, int HKV) {
   return kShareSplit + (long long)HKV * ((long long)B * T * G / 128 + B / 2 + 1);
 }
 struct ShareSeg {  // a stretch of a prefix, for 128 query rows of a key head
@@ -171,6 +171,7 @@ struct ShareView {
   int32_t* begin;       // [B + 1] first place of a group in order
   int32_t* group_keys;  // [B] keys of a group's prefix
   ShareRow* rows;       // [B]
+  int32_t* made_for;    // [1] the stamp of its cache
   int32_t* steps;       // [1] of 128 keys: a stretch of a prefix (attn_shared_tc.cuh)
   int32_t* segments;    // [1] stretches of all groups
   int32_t* direct;      // [1] each row's own keys, of one key head, are one CTA's
@@ -184,10 +185,10 @@ struct ShareView {
   float* part;          // [2 kShareSplit] of the stretches of prefixes that are cut:
                         // outputs [part_rows][D], maxima and sums [part_rows][2]
   int part_rows;        // query rows of a key head in a stretch, at most 128
+  int32_t stamp;        // of the cache of this call
   __host__ __device__ static size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
   // the view of a buffer (null: only its size)
-  __host__ __device__ static size_t lay(void* base, int B, int T, int HQ, int HKV, int D,
-                                        ShareView* v) {
+  static size_t lay(void* base, int B, int T, int HQ, int HKV, int D, int shift, ShareView* v) {
     char* at = static_cast<char*>(base);
     size_t n = 0;
     auto take = [&](size_t bytes) {
@@ -221,6 +222,7 @@ struct ShareView {
       s.steps = s.of + 4;
       s.segments = s.of + 5;
       s.direct = s.of + 6;
+      s.made_for = s.of + 7;
       s.segs = reinterpret_cast<ShareSeg*>(segs);
       s.rows = reinterpret_cast<ShareRow*>(rec);
       s.seg = reinterpret_cast<int32_t*>(seg);
@@ -236,13 +238,16 @@ struct ShareView {
       s.o = reinterpret_cast<float*>(o);
       s.part = reinterpret_cast<float*>(part);
       s.part_rows = (int)part_rows;
+      // what places and records depend on: HQ <= 4096, HQ / HKV <= 64, D in 64s, page size
+      s.stamp = HQ | HQ / HKV << 13 | D / 64 << 20 | shift << 23 | 1 << 30;
       *v = s;
     }
     return n;
   }
 };
+// Whether the plan is one of B rows of T tokens, of a cache like this call's.
 __device__ __forceinline__ bool share_is_of(const ShareView& s, int B, int T) {
-  return s.of[0] == B && s.of[1] == T;
+  return s.of[0] == B && s.of[1] == T && *s.made_for == s.stamp;
 }
 
 struct DecodeParams {
@@ -261,7 +266,7 @@ struct DecodeParams {
   long long page0;  // the layer's first page among all layers'
   int B, T, HQ, HKV, G, n_slots, n_pages, max_pages, shift;
   int line_ctas;  // DEC_OWN: CTAs that the line is split over
-  int cut;      // DEC_OWN: prefixes may be in parts (attn_shared_tc.cuh)
+  int cut;        // DEC_OWN: prefixes may be in parts (attn_shared_tc.cuh)
   int nmb;      // row blocks of a (row, key head): ceil(T G / rows of a block)
   int hook_cta, hook_unit;  // test hook of the bounded waits; -1: off
   float c;      // scale * log2(e)

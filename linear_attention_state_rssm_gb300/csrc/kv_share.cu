@@ -31,7 +31,7 @@ struct PlanShareParams {
   const int32_t* held;
   const int32_t* length;
   int32_t* map;  // [n_pages] of the cache's work buffer
-  int B, T, n_slots, n_pages, max_pages, shift, least;
+  int B, T, n_slots, n_pages, max_pages, shift;
   int HKV, rows, split;  // key heads; query rows of a row and key head; stretches at most, about
 };
 
@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kShareThreads)
   if (tid == 0) {
     p.v.of[0] = p.B;
     p.v.of[1] = p.T;
+    *p.v.made_for = p.v.stamp;
     *p.v.lost = 0;
     work = 0;
     longest = 0;
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kShareThreads)
     n = r < p.B ? __ldcg(count + r) : 0;
     const int pages = r < p.B ? __ldcg(common + r) : 0;
     keys = n >= 2 ? pages << p.shift : 0;
-    return n >= 2 && keys >= p.least;
+    return keys > 0;
   };
   auto blocks_of = [&](int n) { return (int)(((long long)n * p.rows + 127) / 128) * p.HKV; };
   unsigned long long mine = 0;
@@ -269,7 +270,8 @@ __global__ void __launch_bounds__(kShareThreads)
 
 }  // namespace
 
-cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G, cudaStream_t st) {
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G,
+                            cudaStream_t st) {
   PlanShareParams s{};
   s.v = v;
   s.slot = p.slot;
@@ -283,7 +285,6 @@ cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, in
   s.n_pages = p.n_pages;
   s.max_pages = p.max_pages;
   s.shift = p.shift;
-  s.least = 1;
   s.HKV = HKV;
   s.rows = p.T * G;
   // Blocks that are cut leave fewer than 2 kShareSplit parts: an even split, and the

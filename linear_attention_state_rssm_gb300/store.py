@@ -356,8 +356,8 @@ class KVCache:
         _lib.rssm_attn_decode(self.handle, layer, q, qs, slot, B, T, o, lse, stream)
 
     def new_share(self, B, T=1):
-        """Room for rssm_kv_share's plan of B rows of T tokens; one for each call
-        that may be on its way at a time."""
+        """Room for rssm_kv_share's plan of B rows of T tokens, and for what the
+        attention holds between its launches."""
         return Share(self, B, T)
 
     def rssm_kv_share(self, slot, T, share, stream=None):

@@ -522,3 +522,61 @@ def test_a_step_of_all_together():
                                np.array([0, m + 30]), c.scale)
     check(o, want, mass, "bf16")
     assert c.rssm_kv_get_device_error() == 0
+
+
+def test_plans_of_another_cache_are_refused():
+    """The same rows and tokens, other heads, sizes of heads or pages: every row is skipped,
+    and none of the plan's places is used."""
+    from linear_attention_state_rssm_gb300 import _lib as lib
+    rng = np.random.default_rng(60)
+    sizes = [(4, 2, 64, 16), (8, 2, 64, 16), (8, 1, 64, 16), (4, 2, 128, 16), (4, 2, 64, 32)]
+    caches = [Batch(rng, [(64, [0, 5, 20])], 2, HQ, HKV, D, "bf16", None, page).c
+              for HQ, HKV, D, page in sizes]
+    most = max(lib.rssm_kv_share_bytes(c.cfg, 3, 2) for c in caches)
+    slot = ints(range(3))
+    for of in caches:
+        buffer = torch.zeros(most, dtype=torch.uint8, device="cuda")
+        lib.rssm_kv_share(of.handle, slot, 3, 2, buffer)
+        for c in caches:
+            q = draw(rng, (6, c.HQ, c.D), "bf16")[0]
+            o = torch.full_like(q, SENTINEL)
+            lib.rssm_attn_decode_shared(c.handle, 1, q, c.HQ * c.D, slot, 3, 2, buffer, o, None)
+            err = c.rssm_kv_get_device_error()
+            if c is of:
+                assert err == 0 and not (o == SENTINEL).all(-1).any()
+            else:
+                assert err == lib.DEVERR["pages"] and (o == SENTINEL).all()
+
+
+@pytest.mark.parametrize("kind", [("bf16", None), ("f16", "e4m3"), ("f32", None)])
+def test_the_longest_windows_with_the_most_heads(kind):
+    run(kind, [(64, [0, 3]), (16, [1])], 64, 64, 1, 64, 16, 61)
+
+
+@pytest.mark.parametrize("kind", [("bf16", None), ("bf16", "e4m3"), ("f32", None)])
+def test_pools_past_32_bit_offsets(kind):
+    from linear_attention_state_rssm_gb300.store import KVCache
+    dtype, pages = kind
+    D, HKV, page = 256, 4, 256
+    n = (1 << 32) // (HKV * page * D) + 40        # past 2^32 values, and bytes
+    c = KVCache(n_slots=2, HQ=2 * HKV, HKV=HKV, D=D, n_pages=n, page_size=page, max_pages=3,
+                dtype=dtype, page_dtype=pages)
+    for s in range(2):
+        c.table[s] = ints([n - 1, n - 3, n - 5 - s])
+    c.held[:] = 3
+    rng = np.random.default_rng(62)
+    (k, kd), (v, vd) = (draw(rng, (2 * 600, HKV, D), dtype) for _ in range(2))
+    q, qd = draw(rng, (2, 2 * HKV, D), dtype)
+    c.rssm_kv_append(0, None, k[:600], v[:600], ints([0]), cu_seqlens=ints([0, 600]))
+    c.length[1] = 512
+    c.rssm_kv_append(0, None, k[1112:], v[1112:], ints([1]), cu_seqlens=ints([0, 88]))
+    c.length[:] = 599
+    share, o = c.new_share(2), torch.zeros_like(q)
+    c.rssm_kv_share(ints([0, 1]), 1, share)
+    assert plan(share, 2)[:2] == (1, [512, 512])
+    c.rssm_attn_decode_shared(0, q, ints([0, 1]), 1, share, o)
+    assert c.rssm_kv_get_device_error() == 0
+    kv = [quant.value(*quant.quantise(x)) if pages else x for x in (kd, vd)]
+    rows = [tuple(x[:600] for x in kv), tuple(np.concatenate([x[:512], x[1112:]]) for x in kv)]
+    want, _, mass = ref.window(qd, rows, [599, 599], 1, c.scale)
+    check(o, want, mass, dtype)
