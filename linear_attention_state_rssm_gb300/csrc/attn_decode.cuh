@@ -35,7 +35,7 @@
 // of 1 to 8 k tokens, 16/4 heads of 256: 78 us, 5.6 TB/s (83% of the copy rate);
 // two rows of 109 to 131 k tokens, 32/8 heads of 128: 89 us, 5.8 TB/s (86%). What a
 // step costs besides its bytes holds them back: half the bytes, as many keys.
-// Windows of 8 tokens (32 rows to a head): 80 us, 1.9 TB/s, bound by two warps'
+// Windows of 8 tokens (32 rows to a head): 74 us, 2.1 TB/s, bound by two warps'
 // steps per stream, one instruction after the other.
 //
 // Prefixes that rows share (kv_share.cu) come in two launches. PREFIX, here for
@@ -61,7 +61,6 @@ enum : int { DEC_PLAIN = 0, DEC_PREFIX = 1, DEC_OWN = 2 };
 constexpr int kBox = 16;        // keys of a TMA box: within one page (pages of 16 k keys)
 constexpr int kQuantBox = 32;   // rows of a column of quantised keys: a box's, or two of kBox's
 constexpr int kGapKeys = 256;   // what beginning and ending a row costs, as keys
-constexpr int kGapOwn = 1024;    // the same behind a shared prefix: its parts are joined, tables compared
 constexpr int kLeastKeys = 512; // keys that a CTA takes at least (of longer rows)
 constexpr int kRowParts = 96;   // parts of the longest row, about: one CTA joins them
 constexpr int kLostPart = 1 << 16;  // in a row's arrivals, beside their number: a part that is not there
@@ -81,11 +80,22 @@ struct DecCfg {
   // Quantised pages, eight rows a warp: half the outputs, and more warps. More
   // than five in a CTA leave too little of the ring on its way (128: seven 92 us
   // for two rows of 109 to 131 k tokens instead of 89; one CTA of nine 104).
-  static constexpr int CPS = NQ == 1    ? (D == 64 ? 3 : 2)
-                             : D == 256 ? 1
-                             : F32 || D == 128 ? 2
-                                               : 3;  // CTAs per SM
-  static constexpr int NW = F32 ? (D == 256 ? 4 : 3) : NQ == 1 ? 5 : D == 256 ? 6 : 4;
+  // Sixteen rows a warp of heads of 128: as many warps as 168 registers leave room
+  // for, in two CTAs, or in one where a stream is several warps, whose steps then wait
+  // less for one another (125 windows of 8 tokens over 3300 tokens, 16/4 heads: two
+  // CTAs of four warps 166 us, one of ten 151, of twelve 202; of 16 tokens, four warps
+  // to a stream: two of four 485, one of eight 329).
+  static constexpr bool WIDE = NQ == 2 && D == 128 && MW > 1;
+  static constexpr int CPS = NQ == 1              ? (D == 64 ? 3 : 2)
+                             : D == 256 || WIDE   ? 1
+                             : F32 || D == 128    ? 2
+                                                  : 3;  // CTAs per SM
+  static constexpr int NW = F32                    ? (D == 256 ? 4 : 3)
+                            : NQ == 1              ? 5
+                            : WIDE                 ? (MW == 2 ? 10 : 8)
+                            : NQ == 2 && D == 128  ? 5
+                            : D == 256             ? 6
+                                                   : 4;  // warps of the streams
   static constexpr int CH = F32 || (D == 256 && !Q) ? 16 : 32;  // keys of a chunk
   static constexpr int GRP = D == 256 ? 2 : 4;         // chunks that are sent for together
   static constexpr int CT = NW * 32;                   // threads of the streams
@@ -204,7 +214,7 @@ struct Seg {
 // The CTA's stretch of the line, one Seg after the other.
 template <int CH, int MODE, int ROWS>
 struct Line {
-  static constexpr int kGap = (MODE == DEC_OWN ? kGapOwn : kGapKeys) / CH;
+  static constexpr int kGap = kGapKeys / CH;
   long long pos, end, row0;
   int row;
   __device__ __forceinline__ bool next(const DecodeParams& p, Seg& g) {

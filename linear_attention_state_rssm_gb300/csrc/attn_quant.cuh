@@ -142,6 +142,17 @@ struct WarpAttnQuant {
     for (int e = 0; e < RL; ++e) m[e] = kNegInf, l[e] = 0.f;
   }
 
+  // Address of the lane's row of a chunk's first sixteen and its unit of the first two,
+  // and of sixteen n and unit u on: units differ in bits that the swizzle has for
+  // itself, so one register and an exclusive or serve a whole chunk. (With addresses of
+  // their own kept in registers, windows of 32 query rows spilled.)
+  static __device__ __forceinline__ uint32_t codes_of(const unsigned char* xs, int lane) {
+    return smem_addr(xs) + code_off<D, KR>((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4);
+  }
+  static __device__ __forceinline__ uint32_t code_at(uint32_t base, int n, int u) {
+    return (base ^ (u % 8) << 4) + u / 8 * (KR * 128) + n * (16 * (D < 128 ? D : 128));
+  }
+
   // Weights w of a chunk of 16 NT keys (x[.][.][2 h + e]: key 16 n + 8 h + g, row e
   // of the lane's pair), m, l and o brought to the new reference. sc: the chunk's
   // powers of two ([16 NT][2] bytes); rf: c 2^a of the lane's rows.
@@ -159,16 +170,17 @@ struct WarpAttnQuant {
       }
     }
     const int i = lane >> 3, r = lane & 7, g = lane >> 2;
-    const uint32_t qb = smem_addr(qs), kb = smem_addr(ks);
+    const uint32_t qb = smem_addr(qs) + unit_off<QR>(r, i), kb = codes_of(ks, lane);
 #pragma unroll
     for (int u = 0; u < D / 16; u += 2) {
       uint32_t b[NQ][4];  // k-steps u and u + 1
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) ldsm4(b[q], qb + unit_off<QR>(8 * q + r, 2 * u + i));
+      for (int q = 0; q < NQ; ++q)
+        ldsm4(b[q], (qb ^ (2 * u % 8) << 4) + 2 * u / 8 * QR * 128 + q * 1024);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t kf[4];  // keys 0-7 and 8-15 of unit u, of unit u + 1
-        ldsm4(kf, kb + code_off<D, KR>(16 * n + (i & 1) * 8 + r, u + (i >> 1)));
+        ldsm4(kf, code_at(kb, n, u));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           uint32_t a[4];
@@ -200,13 +212,17 @@ struct WarpAttnQuant {
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = x[n][q][2 * h + e] * (rf[2 * q + e] * kscale);
-            if (masked && key0 + key >= lim[2 * q + e]) y = kNegInf;
-            x[n][q][2 * h + e] = y;
-            top[2 * q + e] = fmaxf(top[2 * q + e], y + f);
+          for (int e = 0; e < 2; ++e) x[n][q][2 * h + e] *= rf[2 * q + e] * kscale;
+        }
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < RL; ++e) {
+            if (key0 + key >= lim[e]) x[n][e >> 1][2 * h + (e & 1)] = kNegInf;
           }
         }
+#pragma unroll
+        for (int e = 0; e < RL; ++e)
+          top[e] = fmaxf(top[e], x[n][e >> 1][2 * h + (e & 1)] + f);
       }
     }
     float base[RL];
@@ -231,8 +247,19 @@ struct WarpAttnQuant {
         for (int e = 0; e < 4; ++e) {
           const float p = exp2_fast(x[n][q][e] - base[2 * q + (e & 1)]);
           l[2 * q + (e & 1)] += p;
-          // a key that is not seen has no weight, whatever its bytes hold
-          x[n][q][e] = masked && p == 0.f ? 0.f : p * vs[n][e >> 1];
+          x[n][q][e] = p * vs[n][e >> 1];
+        }
+      }
+    }
+    if (masked) {  // a key that is not seen has no weight, whatever its bytes hold
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int e = 0; e < RL; ++e) {
+            if (key0 + 16 * n + 8 * h + g >= lim[e]) x[n][e >> 1][2 * h + (e & 1)] = 0.f;
+          }
         }
       }
     }
@@ -270,8 +297,7 @@ struct WarpAttnQuant {
       add_selected<NT>(w, vs, key0, lim, lane);
       return;
     }
-    const int i = lane >> 3, r = lane & 7;
-    const uint32_t vb = smem_addr(vs);
+    const uint32_t vb = codes_of(vs, lane);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       uint32_t b[NQ][2];
@@ -283,7 +309,7 @@ struct WarpAttnQuant {
 #pragma unroll
       for (int u = 0; u < D / 16; u += 2) {
         uint32_t vf[4];  // keys 0-7 and 8-15 of unit u, of unit u + 1
-        ldsm4_t(vf, vb + code_off<D, KR>(16 * n + (i & 1) * 8 + r, u + (i >> 1)));
+        ldsm4_t(vf, code_at(vb, n, u));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           uint32_t a[4];

@@ -29,6 +29,12 @@
 // fp16 down to 2^-15 of the step's largest token; below it a value is off by 2^-25
 // of that one's unit, 2^-33 of its largest value.
 //
+// Measured (GB300): a step of heads of 128 takes 0.72 us of 16-bit pages, near the
+// 0.55 of its products, and 1.48 of e4m3 ones (shared memory: codes read, fp16
+// written, operands read). 64 rows behind 8200 keys, four key heads: 9 to 11 us a
+// layer, of which the bytes would take 2.5 and two steps a CTA 1.5; the rest are the
+// trips to the plan, the queries, the table and the first keys, and the way out.
+//
 // Even a group of few rows takes the whole instruction, whose 128 rows cost less
 // than the prefix's bytes take to arrive: 128 keys of 128 values are 64 KB, 1.5
 // us of an SM's share of the memory, and 0.55 us of products.

@@ -485,7 +485,7 @@ rssm_status rssm_kv_share(rssm_kv_handle* h, const int32_t* slot, int32_t B, int
   ShareView v;
   ShareView::lay(share, B, T, h->cfg.HQ, h->cfg.HKV, h->cfg.D, h->shift, &v);
   return from_cuda(kv_share_launch(v, p, h->cfg.HKV, h->cfg.HQ / h->cfg.HKV,
-                                   static_cast<cudaStream_t>(stream)));
+                                   h->scales != nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 rssm_status rssm_attn_decode_shared(rssm_kv_handle* h, int32_t layer, const void* q,

@@ -14,6 +14,12 @@
 // weights of queries, then of keys, lie in registers; products go in pairs of
 // fp32. Where tokens are few, groups share out a token's heads. Loads of four
 // heads are on their way at a time.
+//
+// Measured (GB300, in a graph): 14.2 k tokens, 16/4 heads of 256, norms, rotation of
+// 64 dimensions, e4m3 pages: 73 us, 5.2 TB/s (77% of the copy rate); 2816 tokens,
+// 32/8 heads of 128, three axes, bf16 pages: 19 us, 3.7 TB/s (one wave of CTAs that
+// begin and end together); 56 single tokens 5.2 us, trips to memory. With a thread for
+// a vector of a head, cosines looked up by each, 115 us; in pairs of fp32 110.
 #include "attn_tc.cuh"
 #include "kv_common.cuh"
 #include "kv_tokens.cuh"

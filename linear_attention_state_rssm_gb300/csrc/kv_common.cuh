@@ -290,7 +290,8 @@ struct PromptParams {
 };
 
 cudaError_t kv_plan_launch(int mode, const PageParams& p, cudaStream_t st);
-cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G, cudaStream_t st);
+cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G, bool quant,
+                            cudaStream_t st);
 cudaError_t kv_copy_launch(const CopyParams& p, int num_sms, cudaStream_t st);
 cudaError_t kv_length_launch(const LengthParams& p, cudaStream_t st);
 cudaError_t kv_append_launch(const AppendParams& p, cudaStream_t st);

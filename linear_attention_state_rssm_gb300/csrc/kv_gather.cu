@@ -7,7 +7,9 @@
 // Bytes bound it. A page keeps a head's tokens side by side, the row a token's
 // heads: a CTA takes a block of tokens and all heads, so both sides see runs of
 // D values, and its threads have kAhead loads of keys and of values each on their
-// way.
+// way. Measured (GB300): 12 rows of 0.5 to 16 k tokens, 8 heads of 128, e4m3 to bf16:
+// 52 us, 4.9 TB/s (72% of the copy rate; one byte read for two written); one load
+// ahead 57, cached ones 63.
 #include "kv_common.cuh"
 #include "kv_tokens.cuh"
 

@@ -9,6 +9,10 @@
 // in two parts of its keys, which meet in the running maximum, sum and output
 // (attn_decode.cuh): what the second launch begins with is what the first left.
 //
+// It is bound by trips to memory: one CTA, seven phases one after the other, 10 us
+// for 64 rows of 130 pages. Once a step, so beside all layers' attention it is small;
+// more CTAs would need waits over the grid.
+//
 // The plan says which rows and how many keys, not which pages: pages may move
 // (all tables follow) and slots grow. Where a table no longer begins with its
 // group's pages the attention sees that, and skips the row.
@@ -21,8 +25,14 @@ namespace rssm {
 namespace {
 
 constexpr int kShareThreads = 1024;
-constexpr int kMostOwn = 1024;  // keys that a CTA takes of one row's own at most, if it has one row
-constexpr int kLeastSteps = 4;  // of 128 keys: a stretch, but for a prefix's last
+// Keys that a CTA takes of one row's own at most, if it has one row; longer ones are
+// cut. 64 rows with four heads of 128 behind one prefix, four layers with the plan:
+// 600 keys of their own 139 us an item to a CTA, 163 cut; 1500 keys 211 and 184, but
+// over quantised pages 161 and 184.
+constexpr int kMostOwn = 1024, kMostOwnQuant = 2048;
+// Steps of 128 keys: a stretch at least, but for a prefix's last. 64 rows behind 8200
+// keys: 2 or 4 116 us, 8 124.
+constexpr int kLeastSteps = 4;
 
 struct PlanShareParams {
   ShareView v;
@@ -33,6 +43,7 @@ struct PlanShareParams {
   int32_t* map;  // [n_pages] of the cache's work buffer
   int B, T, n_slots, n_pages, max_pages, shift;
   int HKV, rows, split;  // key heads; query rows of a row and key head; stretches at most, about
+  int most_own;
 };
 
 __device__ __forceinline__ int scan_of(int x, int* sums, int tid, int& total) {
@@ -162,7 +173,8 @@ __global__ void __launch_bounds__(kShareThreads)
   const unsigned long long even = (work + p.split - 1) / p.split;
   int per = even < kLeastSteps ? kLeastSteps : even > (1 << 24) ? 1 << 24 : (int)even;
   // a second turn of a few CTAs costs as much as the first: longer stretches where
-  // that leaves one for each SM at most
+  // that leaves one for each SM at most (20 groups of 4 rows of 700 to 5000 keys, four
+  // heads: four layers 193 us, without this 230)
   for (int turn = 0; turn < 6; ++turn) {
     int cut = 0, whole = 0;  // stretches, blocks
     for (int r = tid; r < p.B; r += kShareThreads) {
@@ -265,13 +277,13 @@ __global__ void __launch_bounds__(kShareThreads)
     if (s >= 0 && s < p.n_slots) atomicMax(&longest, p.length[s] + p.T - p.v.prefix[r]);
   }
   __syncthreads();
-  if (tid == 0) *p.v.direct = longest <= kMostOwn;
+  if (tid == 0) *p.v.direct = longest <= p.most_own;
 }
 
 }  // namespace
 
 cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, int G,
-                            cudaStream_t st) {
+                            bool quant, cudaStream_t st) {
   PlanShareParams s{};
   s.v = v;
   s.slot = p.slot;
@@ -287,6 +299,7 @@ cudaError_t kv_share_launch(const ShareView& v, const PageParams& p, int HKV, in
   s.shift = p.shift;
   s.HKV = HKV;
   s.rows = p.T * G;
+  s.most_own = quant ? kMostOwnQuant : kMostOwn;
   // Blocks that are cut leave fewer than 2 kShareSplit parts: an even split, and the
   // last stretch of each, which has another before it.
   s.split = kShareSplit;
