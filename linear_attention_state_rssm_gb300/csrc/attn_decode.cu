@@ -38,7 +38,7 @@ cudaError_t attn_decode_maps(void* maps, const void* k, const void* v, long long
   const cuuint64_t dims[3] = {inner, (cuuint64_t)rows, bytes / column};
   const cuuint64_t strides[2] = {bytes, column};
   const bool wide = quant && page_size >= kQuantBox;
-  const cuuint32_t box[3] = {(cuuint32_t)inner, wide ? kQuantBox : kBox,
+  const cuuint32_t box[3] = {(cuuint32_t)inner, (cuuint32_t)(wide ? kQuantBox : kBox),
                              quant && !wide ? 1 : (cuuint32_t)(bytes / column)};
   const cuuint32_t ones[3] = {1, 1, 1};
   KvMaps* m = static_cast<KvMaps*>(maps);

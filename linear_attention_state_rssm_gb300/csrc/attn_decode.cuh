@@ -43,8 +43,9 @@
 // rows of all of a group's members are the rows of its blocks, all of the prefix is
 // seen by all, and what is left is the running maximum, sum and output of every
 // query row, in fp32. OWN: each row from the end of its prefix on, its first stream
-// beginning with what the prefix left. Rows without a group begin at their first
-// key.
+// beginning with what the prefix left. Rows without a group begin at their
+// first key. Behind the tensor cores' launch OWN's CTAs start as its own leave, and
+// wait for its end only there (20 groups of 4 rows, four layers: 191 us, now NEWG).
 #pragma once
 
 #include "attn_core.cuh"
@@ -295,19 +296,25 @@ __device__ __forceinline__ long long query_token(const DecodeParams& p, int r, i
 }
 
 // Whether the row's pages up to its prefix's end are those that the group's keys
-// were read from (the plan may be older than the tables), and were read.
+// are read from (the plan may be older than the tables).
 template <int THREADS>
 __device__ __forceinline__ bool prefix_holds(const DecodeParams& p, const Seg& sg,
                                              const ShareRow& rec, int tid) {
   int lead = p.slot[rec.lead];
   if (lead < 0 || lead >= p.n_slots) lead = lead_slot(p, rec.group);
-  bool same = *p.share.lost == 0 && lead >= 0;
+  bool same = lead >= 0;
   if (!same || sg.slot == lead) return same;
   const int32_t* a = p.table + (size_t)sg.slot * p.max_pages;
   const int32_t* b = p.table + (size_t)lead * p.max_pages;
   const int n = sg.start >> p.shift;
   for (int i = tid; i < n; i += THREADS) same = same && a[i] == b[i];
   return same;
+}
+
+// The end of the launch before this one, whose memory is then there to be read
+// (at once where the launch does not overlap it).
+__device__ __forceinline__ void launch_before_ended() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Whether any of the `count` threads of a named barrier says so (a barrier too).
@@ -409,6 +416,11 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     if (p.hook_cta == (int)blockIdx.x) mbar_promise(&full[p.hook_unit % C::NU], 16);
     fence_mbar_init();
   }
+  // A CTA of OWN does not leave before the prefixes' launch has ended, or the launch
+  // after them could begin while it runs.
+  auto nothing_to_do = [] {
+    if constexpr (MODE == DEC_OWN) launch_before_ended();
+  };
   Stretch line;
   long long share = 0;  // places of a CTA's stretch
   bool direct = false;
@@ -417,14 +429,14 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     // others' lengths and never two beginnings one behind the other.
     const int items = p.HKV * p.nmb;
     direct = (long long)p.B * items <= gridDim.x && *p.share.direct != 0;
-    if (!direct && (int)blockIdx.x >= p.line_ctas) return;
+    if (!direct && (int)blockIdx.x >= p.line_ctas) return nothing_to_do();
     if (direct) {
       line.row = blockIdx.x / items;
-      if (line.row >= p.B) return;
+      if (line.row >= p.B) return nothing_to_do();
       int s, start;
       const int keys = row_keys<MODE>(p, line.row, blockIdx.x % items == 0 && tid == 0, s, start);
       const long long cost = places<C::CH, Stretch::kGap>(keys - start);
-      if (cost == 0) return;
+      if (cost == 0) return nothing_to_do();
       line.row0 = 0;
       line.pos = blockIdx.x % items * cost;
       line.end = line.pos + cost;
@@ -475,7 +487,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     share = share > least ? share : least;
     line.pos = share * blockIdx.x;
     line.end = line.pos + share < total ? line.pos + share : total;
-    if (line.pos >= line.end) return;
+    if (line.pos >= line.end) return nothing_to_do();
     at += first_incl - first_w;
     long long* found = scan + 3 * (NW + 1);  // row, its first place
     if (at <= line.pos && line.pos < at + first_w) {
@@ -688,6 +700,8 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
       early = true;
       rec = p.share.rows[sg.row];
       const int base = sg.mb * C::ROWS, R = min(C::ROWS, p.T * p.G - base);
+      early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
+      launch_before_ended();
       if (p.cut && rec.parts > 1) {
         auto joined = [&](int rr) {
           const int tr = base + rr;
@@ -697,7 +711,6 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
         };
         join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
       }
-      early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
     }
   }
   const int grp = warp / MW, wr = C::WROWS * (warp % MW);  // the warp's stream, its first row
@@ -758,12 +771,14 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
           return C::JOIN_HERE && parts > 1 ? os + rr * D : p.share.o + out_row(rr) * D;
         };
         if (!early) {
-          if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
           early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
+          launch_before_ended();
+          if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
         }
-        skip = named_any(1, C::CT, early_bad);
+        const bool lost = __ldcg(p.share.lost) != 0;
+        skip = named_any(1, C::CT, early_bad || lost);
         if (skip && tid == 0)
-          atomicOr(p.err, *p.share.lost != 0 ? (uint32_t)DEVERR_TIMEOUT : (uint32_t)DEVERR_PAGES);
+          atomicOr(p.err, lost ? (uint32_t)DEVERR_TIMEOUT : (uint32_t)DEVERR_PAGES);
         if (!skip && grp == 0) {
 #pragma unroll
           for (int e = 0; e < W::RL; ++e) {
@@ -1046,6 +1061,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     __syncwarp();
     if (lane == 0) mbar_arrive(&qempty[half]);
   }
+  nothing_to_do();
   if (dead && lane == 0) {
     atomicOr(p.err, DEVERR_TIMEOUT);
     if constexpr (MODE == DEC_PREFIX) atomicExch(p.share.lost, 1);
@@ -1068,7 +1084,19 @@ cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStr
     own.line_ctas = C::CPS * sms;
     const long long items = (long long)p->B * p->HKV * p->nmb;
     const int grid = items <= own.line_ctas || items > 2 * own.line_ctas ? own.line_ctas : (int)items;
-    kernel<<<grid, C::NT, C::SMEM, st>>>(own, *static_cast<const KvMaps*>(maps));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::NT);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    // Its CTAs may start while the prefixes' launch runs, but not beside PREFIX, which
+    // has its parts in the same work buffer.
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = p->cut;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, own, *static_cast<const KvMaps*>(maps));
   } else {
     kernel<<<C::CPS * sms, C::NT, C::SMEM, st>>>(*p, *static_cast<const KvMaps*>(maps));
   }

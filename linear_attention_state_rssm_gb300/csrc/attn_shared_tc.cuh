@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
   volatile uint32_t* gave_up = tslot + 1;  // a wait ran out: nothing is stored any more
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the rows' launch
   // ---- the CTA's stretch
   const ShareView& sv = p.share;
   static_assert(sizeof(ShareSeg) == 32, "two vectors");

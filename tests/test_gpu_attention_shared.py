@@ -580,3 +580,35 @@ def test_pools_past_32_bit_offsets(kind):
     rows = [tuple(x[:600] for x in kv), tuple(np.concatenate([x[:512], x[1112:]]) for x in kv)]
     want, _, mass = ref.window(qd, rows, [599, 599], 1, c.scale)
     check(o, want, mass, dtype)
+
+
+@pytest.mark.parametrize("kind,own", [(("bf16", None), [3, 40, 0]), (("bf16", "e4m3"), [700, 1500, 3]),
+                                      (("f32", None), [3, 40, 0])])
+def test_calls_that_follow_one_another_closely(kind, own):
+    """Layers that use one plan's room in turn, with nothing between them: each answers as
+    it does alone, bit for bit."""
+    rng = np.random.default_rng(63)
+    b = Batch(rng, [(2000, own), (64, [0, 1]), (0, [30])], 1, 8, 2, 128, kind[0], kind[1], 16)
+    B = len(b.lens)
+    slot, share = ints(range(B)), b.c.new_share(B)
+    b.c.rssm_kv_share(slot, 1, share)
+    qs = [draw(rng, (B, 8, 128), kind[0])[0] for _ in range(5)]
+    alone = []
+    for q in qs:
+        alone.append(torch.empty_like(q))
+        torch.cuda.synchronize()
+        b.c.rssm_attn_decode_shared(1, q, slot, 1, share, alone[-1])
+        torch.cuda.synchronize()
+    close = [torch.empty_like(qs[0]) for _ in range(60)]
+    for i, o in enumerate(close):
+        b.c.rssm_attn_decode_shared(1, qs[i % 5], slot, 1, share, o)
+    g, replayed = torch.cuda.CUDAGraph(), [torch.empty_like(q) for q in qs]
+    with torch.cuda.graph(g):
+        for q, o in zip(qs, replayed):
+            b.c.rssm_attn_decode_shared(1, q, slot, 1, share, o)
+    g.replay()
+    g.replay()
+    for i, o in enumerate(close):
+        assert torch.equal(o, alone[i % 5])
+    assert all(torch.equal(x, y) for x, y in zip(replayed, alone))
+    assert b.c.rssm_kv_get_device_error() == 0
