@@ -45,7 +45,7 @@
 // query row, in fp32. OWN: each row from the end of its prefix on, its first stream
 // beginning with what the prefix left. Rows without a group begin at their
 // first key. Behind the tensor cores' launch OWN's CTAs start as its own leave, and
-// wait for its end only there (20 groups of 4 rows, four layers: 191 us, now NEWG).
+// wait for its end only there (20 groups of 4 rows, four layers: 191 us, so 179).
 #pragma once
 
 #include "attn_core.cuh"
@@ -1078,8 +1078,8 @@ cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStr
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if constexpr (MODE == DEC_OWN) {
     // Up to two turns of CTAs for rows with few keys, an item each: 20 groups of 4
-    // rows with four heads, 320 items for 304 places, 189 us of four layers, by the
-    // line 198.
+    // rows with four heads, 320 items for 304 places, 179 us of four layers, by the
+    // line 191.
     DecodeParams own = *p;
     own.line_ctas = C::CPS * sms;
     const long long items = (long long)p->B * p->HKV * p->nmb;

@@ -27,7 +27,7 @@ namespace {
 constexpr int kShareThreads = 1024;
 // Keys that a CTA takes of one row's own at most, if it has one row; longer ones are
 // cut. 64 rows with four heads of 128 behind one prefix, four layers with the plan:
-// 600 keys of their own 139 us an item to a CTA, 163 cut; 1500 keys 211 and 184, but
+// 600 keys of their own 139 us an item to a CTA, 163 cut; 1500 keys 210 and 184, but
 // over quantised pages 161 and 184.
 constexpr int kMostOwn = 1024, kMostOwnQuant = 2048;
 // Steps of 128 keys: a stretch at least, but for a prefix's last. 64 rows behind 8200
