@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
       if (r0 + tid < p.B) {
         int s, start;
         const int keys = row_keys<MODE>(p, r0 + tid, false, s, start);
-        w = places<C::CH, Stretch::kGap>(keys - start) * p.HKV * row_blocks<MODE, C::ROWS>(p, r0 + tid);
+        w = places<C::CH, Stretch::kGap>(keys - start) * p.HKV *
+            row_blocks<MODE, C::ROWS>(p, r0 + tid);
       }
       const long long incl = warp_scan(w, lane);
       __syncthreads();  // the last sums have been read
@@ -1083,7 +1084,8 @@ cudaError_t decode_one(const DecodeParams* p, const void* maps, int sms, cudaStr
     DecodeParams own = *p;
     own.line_ctas = C::CPS * sms;
     const long long items = (long long)p->B * p->HKV * p->nmb;
-    const int grid = items <= own.line_ctas || items > 2 * own.line_ctas ? own.line_ctas : (int)items;
+    const bool turns = items > own.line_ctas && items <= 2 * own.line_ctas;
+    const int grid = turns ? (int)items : own.line_ctas;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(C::NT);

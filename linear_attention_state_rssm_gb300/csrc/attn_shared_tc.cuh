@@ -515,9 +515,12 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
           powers[i / 2 % C::NE] = make_int2((int)most_k - kScaleBias, (int)most_v - kScaleBias);
           mbar_arrive(&efull[i / 2 % C::NE]);
         }
-        const int mine = (int)(bytes[r] >> (8 * (i & 1)) & 0xff), d2 = mine - (int)(i & 1 ? most_v : most_k);
+        const int mine = (int)(bytes[r] >> (8 * (i & 1)) & 0xff);
+        const int d2 = mine - (int)(i & 1 ? most_v : most_k);
         // 2^d2 in fp16: normal to 2^-14, then one bit; 0 below 2^-24 and behind the last
-        const uint32_t bits = r >= n || d2 < -24 ? 0u : d2 >= -14 ? (uint32_t)(15 + d2) << 10 : 1u << (24 + d2);
+        const uint32_t bits = r >= n || d2 < -24 ? 0u
+                              : d2 >= -14        ? (uint32_t)(15 + d2) << 10
+                                                 : 1u << (24 + d2);
         const uint32_t two = bits | bits << 16;
         const __half2 by = *reinterpret_cast<const __half2*>(&two);
         constexpr int WIDE = D == 256 ? 2 : 1, W = D / WIDE;  // a box's width
