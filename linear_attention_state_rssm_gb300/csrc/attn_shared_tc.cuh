@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       if constexpr (Q8) {
         tc_wait(&efull[j % C::NE], (uint32_t)((j / C::NE) & 1), dead, gave_up);
         const int2 e = powers[j % C::NE];
-        c = row_c * power_of(e.x);
+        // Tiny queries on keys of zeros: not 0, by which the -inf of a score behind the last
+        // key would be NaN. Scores are below 2^31, so what this keeps is below 2^-95.
+        c = fmaxf(row_c * power_of(e.x), 1.17549435e-38f);
         from = (float)e.y;
       }
       tc_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1), dead, gave_up);

@@ -1,0 +1,87 @@
+"""Attention over pages and shared prefixes where sizes lie far apart: powers of two of
+quantised tokens, weights far below the largest, queries near the ends of their type;
+and what calls leave behind.
+
+Tolerances are those of the two modules whose batches are used here: a weight is rounded
+to the type of the products (2^-8; fp16, quantised pages too: 2^-11), the output to its
+own, fp32 sums and the exponential add 1e-4 of the mass sum_j p_j |v_j|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_attention_shared as shared
+from oracle import attention as ref
+from oracle import quant
+from test_gpu_attention_shared import SENTINEL, TORCH, Batch, draw, ints
+
+pytestmark = pytest.mark.gpu
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+FLOOR = {"bf16": 2.0 ** -126, "f16": 2.0 ** -24}   # the types' smallest steps
+LSE = 5e-5
+ARRIVALS = 4 * 3 * 152    # bytes of the work buffer that count parts
+
+
+def rel(dtype, pages):
+    return HALF[dtype] + HALF["f16" if pages else dtype] + 1e-4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from linear_attention_state_rssm_gb300 import build
+    build.build()
+
+
+def put(b, which, s, x):
+    """x [n, HKV, D]: slot s's first n keys (0) or values (1), in the pool and the oracle."""
+    c, page = b.c, b.c.page_size
+    pool = (c.k_pages, c.v_pages)[which]
+    for i, pg in enumerate(b.tables[s]):
+        part = x[i * page:(i + 1) * page].transpose(1, 0, 2)
+        n = part.shape[1]
+        if n == 0:
+            break
+        if c.page_scales is None:
+            t = torch.from_numpy(part.copy()).to(TORCH[b.dtype])
+            pool[1, pg, :, :n] = t.cuda()
+            b.values[which][pg, :, :n] = t.double().numpy()
+        else:
+            codes, scale = quant.quantise(part)
+            pool.view(torch.uint8)[1, pg, :, :n] = torch.from_numpy(codes).cuda()
+            c.page_scales[1, pg, :, :n, which] = torch.from_numpy(scale).cuda()
+            b.values[which][pg, :, :n] = quant.value(codes, scale)
+
+
+def close(got, want, mass, dtype, pages):
+    got = got.double().cpu().numpy()
+    off, lim = np.abs(got - want), rel(dtype, pages) * mass + FLOOR[dtype]
+    assert np.all(off <= lim), (off / lim).max()
+
+
+def both(b, q, pages):
+    """The batch by the shared attention and row by row, against the oracle."""
+    c, B, T = b.c, len(b.lens), b.T
+    want, wlse, mass = b.want(q.double().cpu().numpy(), list(range(B)))
+    slot, share = ints(range(B)), c.new_share(B, T)
+    c.rssm_kv_share(slot, T, share)
+    for call in (lambda *a, **k: c.rssm_attn_decode_shared(1, q, slot, T, share, *a, **k),
+                 lambda *a, **k: c.rssm_attn_decode(1, q, slot, T, *a, **k)):
+        o = torch.full_like(q, SENTINEL)
+        lse = torch.full(q.shape[:2], SENTINEL, device="cuda")
+        call(o, lse=lse)
+        assert c.rssm_kv_get_device_error() == 0
+        close(o, want, mass, b.dtype, pages)
+        assert np.all(np.abs(lse.double().cpu().numpy() - wlse) <= LSE + 1e-6 * np.abs(wlse))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("by", [2.0 ** -75, 2.0 ** -110])
+def test_small_queries_on_keys_of_zeros(D, by):
+    """Every score is 0, in a last step that is not whole too: the answer is the mean."""
+    rng = np.random.default_rng([70, D])
+    b = Batch(rng, [(100, [0, 30]), (200, [3, 1])], 1, 4, 2, D, "bf16", "e4m3", 16)
+    for s in range(4):
+        put(b, 0, s, np.zeros((b.lens[s] + 1, 2, D)))
+    both(b, draw(rng, (4, 4, D), "bf16", by)[0], "e4m3")
