@@ -20,14 +20,20 @@
 //
 // e4m3 pages: eight more warps turn codes into fp16 in shared memory, and the
 // products are those of fp16, whatever the cache's type (a query row is scaled by a
-// power of two into fp16's range, as in attn_quant.cuh). Keys and values are given
-// the powers of two of their tokens relative to the largest of their step's 128,
-// E and F: so a step has one factor for all its scores, c 2^a 2^E, and one for its
-// values, which the reference m follows,
-//     w = 2^(c' s + F - m),   l = l + 2^-F sum w,   O = O + w V',
-// and nothing is done column by column. A code times a power of two is exact in
-// fp16 down to 2^-15 of the step's largest token; below it a value is off by 2^-25
-// of that one's unit, 2^-33 of its largest value.
+// power of two into fp16's range, as in attn_quant.cuh). With e and f the exponents
+// of a key's and a value's power of two, E and F the largest among the step's 128:
+//  - even steps: codes times 2^(e - E) and 2^(f - F), which fp16 holds exactly down
+//    to a difference of 15. A step has one factor for all its scores, c' = c 2^a 2^E,
+//    and one for its values, which the reference m follows,
+//        w = 2^(c' s + F - m),   l = l + 2^-F sum w,   O = O + w V'.
+//    The weights' headroom is that of a token of F, so f may differ by 6 only; and F
+//    itself has its bounds, so that no w falls out of fp32's range beside another step's.
+//  - other steps: codes as they are, powers column by column in fp32,
+//        x = (c 2^a) (2^e s),   p = 2^(x - m),   w = 2^f p,   l = l + sum p,
+//    and m follows x + f: no token's size matters for another's.
+// Both are exact but for the rounding of w to fp16. The second takes longer (20 groups of
+// 4 rows, four layers: 317 us if every step goes that way, 187 if none does), and a
+// model's tokens hardly differ like that.
 //
 // Measured (GB300): a step of heads of 128 takes 0.72 us of 16-bit pages, near the
 // 0.55 of its products, and 1.48 of e4m3 ones (shared memory: codes read, fp16
@@ -58,17 +64,42 @@ struct SharedTcCfg {
   static constexpr int RING = QS;
   static constexpr int RAWS = RING + NU * UNIT;
   static constexpr int SCALES = RAWS + NR * RAW;           // [NR][128][2] bytes
-  static constexpr int BARS = SCALES + NR * 256;
-  static constexpr int NE = Q8 ? 8 : 0;                    // steps whose powers are kept
+  // Steps whose powers are kept: the converters begin step j's keys when they are done
+  // with the values before them, whose place was free because step j - 1 - NU / 2 has
+  // its weights.
+  static constexpr int NE = Q8 ? NU / 2 + 1 : 0;
+  static constexpr int POWERS = SCALES + NR * 256;         // [NE][128][2] bytes
+  static constexpr int BARS = POWERS + NE * 256;
   // the queries' places as they are, or where room is short as rows and heads
   static constexpr bool FAR = !(Q8 && D == 256);
-  // barriers, the rows' places (then their powers of two), the steps' powers of two
+  // barriers, the rows' places (then their powers of two), the steps' E and F
   static constexpr int REST =
       (16 * (NU + NR) + 96 + (FAR ? 1024 : 512) + (Q8 && FAR ? 512 : 0) + 16 * NE + 127) / 128 * 128;
   static constexpr int SMEM = BARS + REST + 1024;          // + alignment of the base
   static constexpr uint32_t O0 = 256;                      // first column of O
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// What an even step's bytes of powers may differ by, and the bytes that its values' may
+// have.
+constexpr unsigned kEvenKeys = 15, kEvenValues = 6;
+constexpr unsigned kEvenLeast = kScaleBias - 30, kEvenMost = kScaleBias + 30;
+constexpr int kUneven = 1 << 20;  // in the place of E
+
+// Of a word with the powers' bytes of two tokens (key's and value's, twice): 2^e, 2^f
+// and f of both. The bytes are biased as fp32's exponents are.
+__device__ __forceinline__ uint64_t key_powers(uint32_t w) {
+  return f2(__uint_as_float(w << 23 & 0x7f800000u), __uint_as_float(w << 7 & 0x7f800000u));
+}
+__device__ __forceinline__ uint64_t value_powers(uint32_t w) {
+  return f2(__uint_as_float(w << 15 & 0x7f800000u), __uint_as_float(w >> 1 & 0x7f800000u));
+}
+__device__ __forceinline__ uint64_t value_exponents(uint32_t w) {
+  constexpr float kBias = -(8388608.f + kScaleBias);  // 2^23: a byte is its last places
+  return add2(f2(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)),
+                 __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443))),
+              f2(kBias, kBias));
+}
 
 struct SharedTcMaps {
   CUtensorMap k, v;
@@ -127,7 +158,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       mbar_init(&sfull[b], 1), mbar_init(&pfull[b], 128), mbar_init(&odone[b], 1);
     mbar_init(drained, 1);
     mbar_init(qfull, C::NT - 64);
-    for (int i = 0; i < C::NE; ++i) mbar_init(&efull[i], 1);
+    for (int i = 0; i < C::NE; ++i) mbar_init(&efull[i], 128);
     *gave_up = 0;
     if (p.hook_cta == (int)blockIdx.x) {
       if constexpr (Q8) mbar_promise(&rfull[p.hook_unit % C::NR], 16);
@@ -142,7 +173,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
   int* row_at = reinterpret_cast<int*>(places);            // else: [128] token HQ + head
   // Q8: [128] 2^a; in a row's place once it is loaded, where that is all there is
   float* row_f = reinterpret_cast<float*>(places + (C::FAR ? 1024 : 0));
-  int2* powers = reinterpret_cast<int2*>(places + (C::FAR ? 1536 : 512));  // Q8: [NE] E, F
+  int2* largest = reinterpret_cast<int2*>(places + (C::FAR ? 1536 : 512));  // Q8: [NE] E, F
   int at = 0;  // token HQ + head of row `tid`
   if (tid < 128) {
     if (tid < R) {
@@ -345,6 +376,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) l2[i] = f2(0.f, 0.f);
     float c = p.c, from = 0.f;  // a score's factor; what its values' power adds to it
+    bool even = true;           // the step has one power for its keys, and one for its values
     [[maybe_unused]] float row_c = 0.f;
     [[maybe_unused]] float l = 0.f;
     if constexpr (Q8) {
@@ -354,35 +386,67 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
     for (int j = 0; j < ns; ++j) {
       if constexpr (Q8) {
         tc_wait(&efull[j % C::NE], (uint32_t)((j / C::NE) & 1), dead, gave_up);
-        const int2 e = powers[j % C::NE];
-        // Tiny queries on keys of zeros: not 0, by which the -inf of a score behind the last
-        // key would be NaN. Scores are below 2^31, so what this keeps is below 2^-95.
-        c = fmaxf(row_c * power_of(e.x), 1.17549435e-38f);
-        from = (float)e.y;
+        const int2 e = largest[j % C::NE];
+        even = e.x != kUneven;
+        // Not 0 for tiny queries, by which the -inf of a score behind the last key would be
+        // NaN: a score is below 2^31, times its key's power below 2^95, so what this keeps
+        // is nothing. Nor infinite for large ones, by which a score of 0 would be.
+        c = even ? row_c * power_of(e.x) : row_c;
+        c = fminf(fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
+        from = even ? (float)e.y : 0.f;
       }
       tc_wait(&sfull[j & 1], (uint32_t)((j >> 1) & 1), dead, gave_up);
       dead = __any_sync(kFull, dead);
       tc_fence_after();
       const uint32_t ts = tb + lane_at + (j & 1) * 128;
       const int n = min(128, keys - (s0 + j) * 128);  // a multiple of 16
+      const uint64_t c2 = f2(c, c);
+      // of step j: words of two tokens (the softmax's warps read the same at a time)
+      [[maybe_unused]] const uint4* powers =
+          reinterpret_cast<const uint4*>(sm + C::POWERS + (Q8 ? j % C::NE : 0) * 256);
       float x[128], t[4];
+      if (!Q8 || even) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32_max(ts + 32 * q, x + 32 * q, t[q]);
+        for (int q = 0; q < 4; ++q) tmem_ld32_max(ts + 32 * q, x + 32 * q, t[q]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) { tmem_ld_wait32(x + 32 * q); asm volatile("" : "+f"(t[q])); }
-      if (n < 128) {
+        for (int q = 0; q < 4; ++q) { tmem_ld_wait32(x + 32 * q); asm volatile("" : "+f"(t[q])); }
+        if (n < 128) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) x[i] = i < n ? x[i] : kNegInf;
+          for (int i = 0; i < 128; ++i) x[i] = i < n ? x[i] : kNegInf;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = kNegInf;
+#pragma unroll
+          for (int i = 0; i < 128; i += 8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[i + 2 * k], x[i + 2 * k + 1]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t[k] = t[k] * c + from;  // c is not negative
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, x + 32 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_wait32(x + 32 * q);
 #pragma unroll
         for (int k = 0; k < 4; ++k) t[k] = kNegInf;
 #pragma unroll
-        for (int i = 0; i < 128; i += 8) {
+        for (int q = 0; q < 16; ++q) {
+          const uint4 w4 = powers[q];
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) t[k] = max3(t[k], x[i + 2 * k], x[i + 2 * k + 1]);
+          for (int k = 0; k < 4; ++k) {
+            const int i = 8 * q + 2 * k;
+            un2(mul2(f2(x[i], x[i + 1]), key_powers(w[k])), x[i], x[i + 1]);
+            x[i] = i < n ? x[i] : kNegInf;
+            x[i + 1] = i + 1 < n ? x[i + 1] : kNegInf;
+            float a, b;
+            un2(fma2(f2(x[i], x[i + 1]), c2, value_exponents(w[k])), a, b);
+            t[k] = max3(t[k], a, b);
+          }
         }
       }
-      // largest weight's exponent; c is not negative
-      const float mx = max3(max3(t[0], t[1], t[2]), t[3], kNegInf) * c + from;
+      const float mx = max3(max3(t[0], t[1], t[2]), t[3], kNegInf);  // largest weight's exponent
       // move the reference: always from -inf, else when the row outgrew it
       constexpr float MOST = Q8 ? 14.f : 8.f, LEFT = Q8 ? 6.f : 0.f;
       const bool move = mx - m > MOST;
@@ -412,21 +476,32 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
         m = to;
       }
       const float base = m == kNegInf ? 0.f : m - from;
-      const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
+      const uint64_t b2 = f2(-base, -base);
+      auto weigh = [&](auto uneven) {
+        constexpr bool U = decltype(uneven)::value;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t w[16];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+          [[maybe_unused]] uint4 w4;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a, b;
-          un2(fma2(f2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), c2, b2), a, b);
-          a = exp2_fast(a);
-          b = exp2_fast(b);
-          l2[i & 3] = add2(l2[i & 3], f2(a, b));
-          w[i] = pack2<M>(a, b);
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            un2(fma2(f2(x[32 * q + 2 * i], x[32 * q + 2 * i + 1]), c2, b2), a, b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            l2[i & 3] = add2(l2[i & 3], f2(a, b));
+            if constexpr (U) {
+              if (i % 4 == 0) w4 = powers[4 * q + i / 4];
+              const uint32_t two = i % 4 == 0 ? w4.x : i % 4 == 1 ? w4.y : i % 4 == 2 ? w4.z : w4.w;
+              un2(mul2(f2(a, b), value_powers(two)), a, b);
+            }
+            w[i] = pack2<M>(a, b);
+          }
+          tmem_st16u(ts + 16 * q, w);
         }
-        tmem_st16u(ts + 16 * q, w);
-      }
+      };
+      if (!Q8 || even) weigh(std::false_type{});
+      else weigh(std::true_type{});
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&pfull[j & 1]);
@@ -493,6 +568,8 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
     if constexpr (Q8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
       const int r = (tid - 256) % 128, half = (tid - 256) / 128;
+      unsigned both = 0, most_k = 0, most_v = 0;  // the row's powers, and the step's largest
+      bool even = true;
       for (int i = 0; i < 2 * ns; ++i) {
         const int n = min(128, keys - (s0 + i / 2) * 128);
         const int ur = i % C::NR, u = i % C::NU;
@@ -502,29 +579,37 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
         if (dead) break;
         const unsigned char* raw = sm + C::RAWS + ur * C::RAW;
         unsigned char* to = sm + C::RING + u * C::UNIT;
-        // the step's largest powers, as bytes
-        const uint16_t* bytes = reinterpret_cast<const uint16_t*>(sm + C::SCALES + ur * 256);
-        unsigned most_k = 0, most_v = 0;
+        if (i % 2 == 0) {  // a step's keys come first, and its powers, as bytes, with them
+          const uint16_t* bytes = reinterpret_cast<const uint16_t*>(sm + C::SCALES + ur * 256);
+          unsigned least_k = 255, least_v = 255;
+          most_k = most_v = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const unsigned both = lane + 32 * k < n ? bytes[lane + 32 * k] : 0;
-          most_k = max(most_k, both & 0xff);
-          most_v = max(most_v, both >> 8);
+          for (int k = 0; k < 4; ++k) {
+            const bool on = lane + 32 * k < n;
+            const unsigned two = bytes[lane + 32 * k];
+            most_k = max(most_k, on ? two & 0xff : 0), least_k = min(least_k, on ? two & 0xff : 255);
+            most_v = max(most_v, on ? two >> 8 : 0), least_v = min(least_v, on ? two >> 8 : 255);
+          }
+          most_k = __reduce_max_sync(kFull, most_k);
+          most_v = __reduce_max_sync(kFull, most_v);
+          least_k = __reduce_min_sync(kFull, least_k);
+          least_v = __reduce_min_sync(kFull, least_v);
+          even = most_k - least_k <= kEvenKeys && most_v - least_v <= kEvenValues &&
+                 least_v >= kEvenLeast && most_v <= kEvenMost;
+          both = r < n ? bytes[r] : 0;
+          if (half == 0) {
+            reinterpret_cast<uint16_t*>(sm + C::POWERS + i / 2 % C::NE * 256)[r] = (uint16_t)both;
+            if (r == 0)
+              largest[i / 2 % C::NE] = make_int2(even ? (int)most_k - kScaleBias : kUneven,
+                                                 (int)most_v - kScaleBias);
+            mbar_arrive(&efull[i / 2 % C::NE]);
+          }
         }
-        most_k = __reduce_max_sync(kFull, most_k);
-        most_v = __reduce_max_sync(kFull, most_v);
-        if (i % 2 == 0 && tid == 256) {  // a step's keys come first
-          powers[i / 2 % C::NE] = make_int2((int)most_k - kScaleBias, (int)most_v - kScaleBias);
-          mbar_arrive(&efull[i / 2 % C::NE]);
-        }
-        const int mine = (int)(bytes[r] >> (8 * (i & 1)) & 0xff);
-        const int d2 = mine - (int)(i & 1 ? most_v : most_k);
-        // 2^d2 in fp16: normal to 2^-14, then one bit; 0 below 2^-24 and behind the last
-        const uint32_t bits = r >= n || d2 < -24 ? 0u
-                              : d2 >= -14        ? (uint32_t)(15 + d2) << 10
-                                                 : 1u << (24 + d2);
-        const uint32_t two = bits | bits << 16;
-        const __half2 by = *reinterpret_cast<const __half2*>(&two);
+        // 2^(e - E) or 2^(f - F) in fp16: normal to 2^-14, then its second largest bit
+        const int d2 = (int)(i & 1 ? both >> 8 : both & 0xff) - (int)(i & 1 ? most_v : most_k);
+        const uint32_t bits = !even || r >= n ? 0x3c00u : d2 >= -14 ? (uint32_t)(15 + d2) << 10 : 0x200u;
+        const uint32_t twice = bits | bits << 16;
+        const __half2 by = *reinterpret_cast<const __half2*>(&twice);
         constexpr int WIDE = D == 256 ? 2 : 1, W = D / WIDE;  // a box's width
 #pragma unroll 4
         for (int d = D / 2 * half; d < D / 2 * (half + 1); d += 16) {

@@ -32,12 +32,6 @@ constexpr int kNormThreads = 128;
 constexpr int kNormCtas = 4;   // of an SM
 constexpr int kNormAhead = 4;  // heads
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 // What a lane has of its group's token for all heads.
 template <typename T, int D>
 struct NormLane {

@@ -85,3 +85,44 @@ def test_small_queries_on_keys_of_zeros(D, by):
     for s in range(4):
         put(b, 0, s, np.zeros((b.lens[s] + 1, 2, D)))
     both(b, draw(rng, (4, 4, D), "bf16", by)[0], "e4m3")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", [5, 20, 27, 45])
+def test_a_large_value_of_no_weight_beside_small_ones(dtype, D, gap):
+    """Tokens of values 2^gap times the others' and a weight of 2^-80: the answer is the
+    others', in the large tokens' step, behind it and in the rows' own keys."""
+    rng = np.random.default_rng([71, D, gap])
+    b = Batch(rng, [(1000, [0, 40, 9]), (300, [5, 60])], 2, 4, 2, D, dtype, "e4m3", 16, scale=1.0)
+    for s, n in enumerate(b.lens):
+        k, v = 0.3 * rng.standard_normal((n + 2, 2, D)), rng.standard_normal((n + 2, 2, D))
+        k[..., 0] = 0.0
+        for at in (7, 140, n - 3):
+            k[at] = 0.0
+            k[at, :, 0] = -56.0                     # 2^-80.8 beside scores of 0
+            v[at] *= 2.0 ** gap
+        put(b, 0, s, k)
+        put(b, 1, s, v)
+    q = draw(rng, (2 * len(b.lens), 4, D), dtype, 0.1)[0]
+    q[..., 0] = 1.0
+    both(b, q, "e4m3")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("gap", [13, 16, 27, 50])
+def test_a_large_key_without_a_score_beside_small_ones(dtype, D, gap):
+    """Keys 2^gap times the others', orthogonal to every query."""
+    rng = np.random.default_rng([72, D, gap])
+    b = Batch(rng, [(1000, [0, 40, 9]), (300, [5, 60])], 2, 4, 2, D, dtype, "e4m3", 16)
+    for s, n in enumerate(b.lens):
+        k = 1.2 * rng.standard_normal((n + 2, 2, D))
+        k[..., 1] = 0.0
+        for at in (7, 140, n - 3):
+            k[at] = 0.0
+            k[at, :, 1] = 2.0 ** gap
+        put(b, 0, s, k)
+    q = draw(rng, (2 * len(b.lens), 4, D), dtype, 1.2)[0]
+    q[..., 1] = 0.0
+    both(b, q, "e4m3")
