@@ -212,7 +212,11 @@ struct WarpAttnQuant {
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[n][q][2 * h + e] *= rf[2 * q + e] * kscale;
+          for (int e = 0; e < 2; ++e) {
+            // in this order: rf kscale may pass fp32's range where the score does not
+            float& y = x[n][q][2 * h + e];
+            y = y * kscale * rf[2 * q + e];
+          }
         }
         if (masked) {
 #pragma unroll

@@ -126,3 +126,18 @@ def test_a_large_key_without_a_score_beside_small_ones(dtype, D, gap):
     q = draw(rng, (2 * len(b.lens), 4, D), dtype, 1.2)[0]
     q[..., 1] = 0.0
     both(b, q, "e4m3")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_large_queries_beside_large_keys_without_a_score(D):
+    """2^110 in a query and 2^60 in a key, in dimensions that the other has not: a score of
+    0, whatever the product of their powers is."""
+    rng = np.random.default_rng([73, D])
+    b = Batch(rng, [(200, [0, 40, 9]), (0, [50])], 1, 4, 2, D, "bf16", "e4m3", 16)
+    for s, n in enumerate(b.lens):
+        k = np.zeros((n + 1, 2, D))
+        k[::3, :, 1] = 2.0 ** 60
+        put(b, 0, s, k)
+    q = torch.zeros(4, 4, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0 ** 110
+    both(b, q, "e4m3")
