@@ -331,6 +331,15 @@ __device__ __forceinline__ bool named_any(int id, int count, bool x) {
   return any != 0;
 }
 
+// l 2^d for d <= 0. Over quantised pages l is up to 2^78 times the number of keys, and 2^d
+// alone may be below fp32's range where the product counts (attn_quant.cuh).
+template <bool Q>
+__device__ __forceinline__ float brought(float l, float d) {
+  if constexpr (!Q) return l * exp2_fast(d);
+  const float half = exp2_fast(0.5f * d);
+  return l * half * half;
+}
+
 // The parts of a prefix that was cut, joined for a block's rows: outputs [R][D]
 // to where `to` says, maxima and sums into row_m and row_l. All threads of the
 // streams; a barrier has to follow. A thread has four dimensions of a row, so
@@ -356,7 +365,7 @@ __device__ __forceinline__ void join_parts(const DecodeParams& p, const Seg& sg,
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(at_ml + k * part));
       const float top = fmaxf(m, ml.x), mu = top == kNegInf ? 0.f : top;
       const float fa = exp2_fast(m - mu), fb = exp2_fast(ml.x - mu);
-      l = l * fa + ml.y * fb;
+      l = brought<C::Q>(l, m - mu) + brought<C::Q>(ml.y, ml.x - mu);
       a.x = a.x * fa + y.x * fb;
       a.y = a.y * fa + y.y * fb;
       a.z = a.z * fa + y.z * fb;
@@ -871,7 +880,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < NG; ++k)
-          sum += sm_l[k * C::ROWS + rr] * exp2_fast(sm_m[k * C::ROWS + rr] - mu);
+          sum += brought<Q>(sm_l[k * C::ROWS + rr], sm_m[k * C::ROWS + rr] - mu);
       }
       inv[e] = 1.f / sum;
       if (grp == 0 && W::tells(lane) && rr < R) {
@@ -982,7 +991,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
                 const float mk = __ldcg(at_part(k) + C::ROWS * D + rr);
                 const float lk = __ldcg(at_part(k) + C::ROWS * (D + 1) + rr);
                 const float to = fmaxf(mx, mk), mu = to == kNegInf ? 0.f : to;
-                sum = sum * exp2_fast(mx - mu) + lk * exp2_fast(mk - mu);
+                sum = brought<Q>(sum, mx - mu) + brought<Q>(lk, mk - mu);
                 mx = to;
               }
             }
@@ -991,7 +1000,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
               const float mk = __shfl_xor_sync(kFull, mx, d), lk = __shfl_xor_sync(kFull, sum, d);
               const float to = fmaxf(mx, mk), mu = to == kNegInf ? 0.f : to;
               // the same order on both sides, so that every lane has the same sum
-              const float a = sum * exp2_fast(mx - mu), b = lk * exp2_fast(mk - mu);
+              const float a = brought<Q>(sum, mx - mu), b = brought<Q>(lk, mk - mu);
               sum = (sub & d) ? b + a : a + b;
               mx = to;
             }

@@ -18,7 +18,8 @@
 // p: m = max_j (x_ij + f_j) - 14 and w <= 2^14; weights down to 2^-28 of the
 // largest keep eleven bits, those below are off by 2^-39 of it. l sums p in fp32,
 // p <= 2^(14 + 64). o and l refer to one m, so streams and parts join as those of
-// other pages.
+// other pages; but where two references lie more than 2^126 apart (values of zeros, f =
+// -64, beside ones of 2^71), l is brought over in two steps.
 //
 // The products are transposed, S' = K q' and O' = V' P': the sixteen rows of an
 // instruction are keys, or dimensions, all of them of use, and its eight columns
@@ -238,10 +239,12 @@ struct WarpAttnQuant {
       for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(kFull, top[e], d));
       const float to = fmaxf(m[e], top[e] - kWeightTop);
       base[e] = to == kNegInf ? 0.f : to;
-      a[e] = exp2_fast(m[e] - base[e]);
+      // in two halves: l, up to 2^78 a key, counts where a alone is below fp32's range
+      const float half = exp2_fast(0.5f * (m[e] - base[e]));
+      a[e] = half * half;
       moved |= a[e] != 1.f;
       m[e] = to;
-      l[e] *= a[e];
+      l[e] = l[e] * half * half;
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {

@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
         const float to = move ? mx - LEFT : m;
         if (j > 0) {
           const float f = to == kNegInf ? 1.f : exp2_fast(m - to);
-          if constexpr (Q8) l *= f;
+          if constexpr (Q8) l = to == kNegInf ? l : brought<true>(l, m - to);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float a, b;

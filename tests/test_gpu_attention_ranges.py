@@ -141,3 +141,18 @@ def test_large_queries_beside_large_keys_without_a_score(D):
     q = torch.zeros(4, 4, D, dtype=torch.bfloat16, device="cuda")
     q[..., 0] = 2.0 ** 110
     both(b, q, "e4m3")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("first", [True, False])
+def test_values_of_zeros_beside_the_largest(D, first):
+    """Powers of two at both ends of their range under scores that are all alike: tokens
+    without a value count in the sum as the others do."""
+    rng = np.random.default_rng([74, D])
+    b = Batch(rng, [(640, [0, 300, 9]), (0, [3000]), (0, [9000])], 1, 4, 2, D, "bf16", "e4m3", 16)
+    for s, n in enumerate(b.lens):
+        v = 2.0 ** 71 * rng.choice((-1.0, 1.0), (n + 1, 2, D)) * rng.uniform(0.9, 1.7, (n + 1, 2, D))
+        none = np.arange(n + 1) < n // 2
+        v[none if first else ~none] = 0.0
+        put(b, 1, s, v)
+    both(b, torch.zeros(len(b.lens), 4, D, dtype=torch.bfloat16, device="cuda"), "e4m3")
