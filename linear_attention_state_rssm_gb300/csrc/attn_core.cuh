@@ -14,6 +14,13 @@
 // bf16 and 2^-11 for fp16, independent from weight to weight, as the rounding of
 // the output); fp32 rounds nothing.
 //
+// fp16 ends at 2^-24, and a long row's many small weights are a part of its answer
+// that rounding them in steps of 2^-24 would lose or double. So its weights are
+// relative to 2^-14 of the largest: m' = max(m, max_j x_ij - 14), weights up to 2^14,
+// eleven bits down to 2^-28 of the largest and 2^-39 of it below. l is a sum of the
+// same weights, so o / l and m + log2 l stay what they were. Where the reference does
+// not follow every step (the tensor-core forms) the largest is 2^9 to 2^15.5.
+//
 // Blocks in shared memory are cut in columns of 128 bytes: row r of a column is
 // 128 bytes after row r - 1, and within it 16-byte unit u lies at unit
 // u ^ (r % 8), so that eight rows' same unit falls in eight different bank
@@ -38,6 +45,12 @@
 namespace rssm {
 
 constexpr float kNegInf = -INFINITY;
+constexpr float kWeightTop = 14.f;  // log2 of the largest weight in fp16
+// log2 of the largest weight after the reference moved, and of what it moves at
+template <typename T>
+constexpr float kWeightLeft = std::is_same<T, __half>::value ? 9.f : 0.f;
+template <typename T>
+constexpr float kWeightMost = std::is_same<T, __half>::value ? 15.5f : 8.f;
 
 __device__ __forceinline__ float attn_f32(float x) { return x; }
 __device__ __forceinline__ float attn_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -388,7 +401,7 @@ struct WarpAttn {
     const bool masked = key0 + 8 * NT > all;
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
-      float mx[2] = {m[b][0], m[b][1]};
+      float mx[2] = {kNegInf, kNegInf};
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -404,6 +417,7 @@ struct WarpAttn {
       for (int h = 0; h < 2; ++h) {
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 1));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(kFull, mx[h], 2));
+        mx[h] = fmaxf(m[b][h], mx[h] - (std::is_same<T, __half>::value ? kWeightTop : 0.f));
         const float base = mx[h] == kNegInf ? 0.f : mx[h];
         a[h] = exp2_fast(m[b][h] - base);
         m[b][h] = mx[h];

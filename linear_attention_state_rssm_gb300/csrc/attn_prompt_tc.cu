@@ -20,7 +20,8 @@
 //
 // The softmax does not depend on what its weights are relative to, as long as
 // they stay in range. So that reference is only moved when a row's true maximum
-// would get a weight above 2^8 (well within both types); moving it costs a pass
+// would get a weight above 2^8 (fp16, whose small weights want the room below:
+// above 2^15.5, and the largest is 2^9 then, attn_core.cuh); moving it costs a pass
 // over O in tensor memory and is rare after the first steps.
 //
 // Products with masked keys are 0 * v, which is not 0 where v is infinite or
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       }
       const float mx = max3(max3(t[0], t[1], t[2]), t[3], m);
       // move the reference: always from -inf, else when the row outgrew it
-      const bool move = (mx - m) * c > 8.f;
+      const bool move = (mx - m) * c > kWeightMost<T> - kWeightLeft<T>;
       if (__any_sync(kFull, move)) {
         const float to = move ? mx : m;
         if (j > 0) {
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
         }
         m = to;
       }
-      const float base = m == kNegInf ? 0.f : m * c;
+      const float base = m == kNegInf ? 0.f : m * c - kWeightLeft<T>;
       const uint64_t c2 = f2(c, c), b2 = f2(-base, -base);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(TcCfg<D>::NT, 1)
       }
     }
     __syncwarp();  // before any of these rows is written again
-    if (mine && p.lse != nullptr) p.lse[orow] = none ? kNegInf : lse_of(m * c, l);
+    if (mine && p.lse != nullptr) p.lse[orow] = none ? kNegInf : lse_of(m * c - kWeightLeft<T>, l);
     if (__any_sync(kFull, bad && mine))
       again<T, D>(p, tl, h, tok0, 32 * (warp & 3), R, min(128 * n_steps, tl.lk), lane);
   }

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
           }
         }
         const float mx = max3(max3(t[0], t[1], t[2]), t[3], m);
-        const bool move = (mx - m) * c > 8.f;
+        const bool move = (mx - m) * c > kWeightMost<T> - kWeightLeft<T>;
         if (j == 0 || __any_sync(kFull, move)) {
           const float to = move ? mx : m;
           if (j > 0) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
           }
           m = to;
         }
-        const float base = m == kNegInf ? 0.f : -m * c;
+        const float base = m == kNegInf ? 0.f : kWeightLeft<T> - m * c;
         const uint64_t c2 = f2(c, c), b2 = f2(base, base);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(TcWide::NT, 1)
         }
       }
       const bool mine = row < R && !dead;
-      if (mine && p.lse != nullptr) p.lse[orow] = none ? kNegInf : lse_of(m * c, l);
+      if (mine && p.lse != nullptr) p.lse[orow] = none ? kNegInf : lse_of(m * c - kWeightLeft<T>, l);
       if (__any_sync(kFull, bad && mine)) {
         __syncwarp();  // these rows' outputs come before what is put in their place
         again<T, D>(p, tl, tt.h, tok0, 32 * (warp & 3), R, min(128 * n_steps, tl.lk), lane);

@@ -44,8 +44,6 @@
 
 namespace rssm {
 
-constexpr float kWeightTop = 14.f;  // log2 of the largest weight
-
 // Byte offset of 16-byte unit u of row r, e4m3 rows of D values in boxes of KR
 // rows: columns of 128 bytes under the 128-byte swizzle, or rows of 64 under the
 // 64-byte one.

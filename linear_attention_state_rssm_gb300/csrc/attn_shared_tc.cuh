@@ -16,7 +16,7 @@
 // joins them. While one step's weights are computed the next one's scores are: a
 // producer warp sends for pages, another warp issues the products, a warpgroup
 // does the softmax, a thread to a row (attn_prompt_tc.cu has the same parts; the
-// reference maximum moves only when a weight would pass 2^8).
+// reference maximum moves only when a weight would pass 2^8, in fp16 2^15.5).
 //
 // e4m3 pages: eight more warps turn codes into fp16 in shared memory, and the
 // products are those of fp16, whatever the cache's type (a query row is scaled by a
@@ -448,10 +448,9 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       }
       const float mx = max3(max3(t[0], t[1], t[2]), t[3], kNegInf);  // largest weight's exponent
       // move the reference: always from -inf, else when the row outgrew it
-      constexpr float MOST = Q8 ? 14.f : 8.f, LEFT = Q8 ? 6.f : 0.f;
-      const bool move = mx - m > MOST;
+      const bool move = mx - m > kWeightMost<M>;
       if (__any_sync(kFull, move)) {
-        const float to = move ? mx - LEFT : m;
+        const float to = move ? mx - kWeightLeft<M> : m;
         if (j > 0) {
           const float f = to == kNegInf ? 1.f : exp2_fast(m - to);
           if constexpr (Q8) l = to == kNegInf ? l : brought<true>(l, m - to);

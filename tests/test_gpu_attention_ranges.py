@@ -156,3 +156,41 @@ def test_values_of_zeros_beside_the_largest(D, first):
         v[none if first else ~none] = 0.0
         put(b, 1, s, v)
     both(b, torch.zeros(len(b.lens), 4, D, dtype=torch.bfloat16, device="cuda"), "e4m3")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("pages", [None, "e4m3"])
+@pytest.mark.parametrize("low", [16.0, 18.0])
+def test_many_small_weights_in_fp16(D, pages, low):
+    """Thousands of keys of a weight of 2^-23 or 2^-26 beside one of weight one, and values
+    448 times its: weights relative to one would lose them in fp16, or round them by half."""
+    rng = np.random.default_rng([75, D])
+    b = Batch(rng, [(20000, [0, 40]), (0, [9000])], 1, 4, 2, D, "f16", pages, 64, scale=1.0)
+    for s, n in enumerate(b.lens):
+        k, v = np.zeros((n + 1, 2, D)), np.full((n + 1, 2, D), 448.0)
+        k[77, :, 0], v[77] = low, 1.0
+        put(b, 0, s, k)
+        put(b, 1, s, v)
+    q = torch.zeros(3, 4, D, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    both(b, q, pages)
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2), (256, 4)])
+@pytest.mark.parametrize("low", [16.0, 18.0])
+def test_many_small_weights_in_fp16_prompts(D, G, low):
+    from linear_attention_state_rssm_gb300.store import KVCache
+    HKV, n, m = 2, 100, 20000
+    c = KVCache(HQ=HKV * G, HKV=HKV, D=D, dtype="f16", scale=1.0)
+    k = torch.zeros(m, HKV, D, dtype=torch.float16, device="cuda")
+    v = torch.full((m, HKV, D), 448.0, dtype=torch.float16, device="cuda")
+    k[77, :, 0], v[77] = low, 1.0
+    q = torch.zeros(n, HKV * G, D, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    o, lse = torch.empty_like(q), torch.empty(n, HKV * G, device="cuda")
+    c.rssm_attn_prefill(q, k, v, ints([0, n]), None, o, cu_keys=ints([0, m]), lse=lse)
+    assert c.rssm_kv_get_device_error() == 0
+    want, wlse, mass = ref.prompt(*(x.double().cpu().numpy() for x in (q, k, v)),
+                                  np.array([0, n]), np.array([0, m]), 1.0)
+    close(o, want, mass, "f16", None)
+    assert np.all(np.abs(lse.double().cpu().numpy() - wlse) <= LSE + 1e-6 * np.abs(wlse))
