@@ -44,8 +44,9 @@
 // seen by all, and what is left is the running maximum, sum and output of every
 // query row, in fp32. OWN: each row from the end of its prefix on, its first stream
 // beginning with what the prefix left. Rows without a group begin at their
-// first key. Behind the tensor cores' launch OWN's CTAs start as its own leave, and
-// wait for its end only there (20 groups of 4 rows, four layers: 191 us, so 179).
+// first key. Behind the tensor cores' launch OWN's CTAs start as its own leave: lengths,
+// tables, queries and a ring of keys are looked up and on their way when it ends, which
+// they wait for (20 groups of 4 rows, four layers: 191 us, so 179).
 #pragma once
 
 #include "attn_core.cuh"
@@ -546,6 +547,7 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
       // the segment's description and its query rows (zeros after the last),
       // into the half that the segment before the last has left
       const int half = ns & 1;
+      if (MODE == DEC_OWN && ns == 2) launch_before_ended();  // as where the ring is full
       if (ns >= 2) dead = !mbar_wait_bounded(&qempty[half], (uint32_t)((ns / 2 - 1) & 1));
       dead = __any_sync(kFull, dead);
       if (dead) break;
@@ -602,6 +604,9 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
         for (int i = 0; i < cnt && (MODE != DEC_PLAIN || Q); i += GRP) {
           const int units = 2 * min(GRP, cnt - i);
           const int u = 2 * n + lane, at_u = u % C::NU;
+          // The streams, who empty the ring, begin when the prefixes' launch has ended: a
+          // wait that could be for that would count it in its limit.
+          if (MODE == DEC_OWN && 2 * n <= C::NU && 2 * n + units > C::NU) launch_before_ended();
           if (lane < units && u >= C::NU)
             dead = !mbar_wait_bounded(&empty[at_u], (uint32_t)((u / C::NU - 1) & 1));
           dead = __any_sync(kFull, dead);
@@ -721,7 +726,10 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
         };
         join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
       }
+    } else {
+      launch_before_ended();
     }
+    // the streams' waits begin here: none counts the prefixes' time in its limit
   }
   const int grp = warp / MW, wr = C::WROWS * (warp % MW);  // the warp's stream, its first row
   int n0 = 0;    // the segment's first chunk among the CTA's
@@ -782,7 +790,6 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
         };
         if (!early) {
           early_bad = !prefix_holds<C::CT>(p, sg, rec, tid);
-          launch_before_ended();
           if (parts > 1) join_parts<C, D>(p, sg, rec, base, R, joined, row_m, row_l, tid);
         }
         const bool lost = __ldcg(p.share.lost) != 0;
@@ -1071,7 +1078,6 @@ __global__ void __launch_bounds__(DecCfg<T, D, MW, NQ>::NT, DecCfg<T, D, MW, NQ>
     __syncwarp();
     if (lane == 0) mbar_arrive(&qempty[half]);
   }
-  nothing_to_do();
   if (dead && lane == 0) {
     atomicOr(p.err, DEVERR_TIMEOUT);
     if constexpr (MODE == DEC_PREFIX) atomicExch(p.share.lost, 1);

@@ -194,3 +194,39 @@ def test_many_small_weights_in_fp16_prompts(D, G, low):
                                   np.array([0, n]), np.array([0, m]), 1.0)
     close(o, want, mass, "f16", None)
     assert np.all(np.abs(lse.double().cpu().numpy() - wlse) <= LSE + 1e-6 * np.abs(wlse))
+
+
+def test_rows_that_wait_long_for_their_prefix():
+    """A prefix of 2^28 keys (one page, named again and again) takes longer than a wait's
+    limit. The rows' launch, whose rings are full by then, does not count that as its own."""
+    from linear_attention_state_rssm_gb300.store import KVCache
+    rng = np.random.default_rng(76)
+    HQ, D, T, page, own = 64, 64, 64, 256, 17
+    most = 1 << 20
+    c = KVCache(n_slots=5, HQ=HQ, HKV=1, D=D, n_pages=1 + 5 * own, page_size=page, max_pages=most)
+    for pool in (c.k_pages, c.v_pages):
+        pool[0] = torch.from_numpy(rng.standard_normal(pool[0].shape)).to(pool)
+    lens, prefix = [], most - own - 1
+    for s in range(5):
+        ids = 1 + own * s + np.arange(own)
+        held = own if s == 4 else prefix + own
+        c.table[s, :held - own] = 0
+        c.table[s, held - own:held] = ints(ids)
+        c.held[s], c.length[s] = held, held * page - T
+        lens.append(held * page - T)
+    q, qd = draw(rng, (5 * T, HQ, D), "bf16")
+    slot, share, o = ints(range(5)), c.new_share(5, T), torch.full_like(q, SENTINEL)
+    c.rssm_kv_share(slot, T, share)
+    n, keys, _ = shared.plan(share, 5)
+    assert n == 1 and keys == [prefix * page] * 4 + [0]
+    t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    t[0].record()
+    c.rssm_attn_decode_shared(0, q, slot, T, share, o)
+    t[1].record()
+    assert c.rssm_kv_get_device_error() == 0
+    assert t[0].elapsed_time(t[1]) > 500            # else nothing was waited for
+    assert not (o == SENTINEL).all(-1).any() and torch.isfinite(o.float()).all()
+    kv = [x[0, 1 + 4 * own:].transpose(1, 2).reshape(-1, 1, D).double().cpu().numpy()
+          for x in (c.k_pages, c.v_pages)]
+    want, _, mass = ref.window(qd[4 * T:], [kv], [lens[4]], T, c.scale)
+    close(o[4 * T:], want, mass, "bf16", None)
