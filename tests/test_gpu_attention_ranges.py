@@ -230,3 +230,31 @@ def test_rows_that_wait_long_for_their_prefix():
           for x in (c.k_pages, c.v_pages)]
     want, _, mass = ref.window(qd[4 * T:], [kv], [lens[4]], T, c.scale)
     close(o[4 * T:], want, mass, "bf16", None)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,HQ,HKV", [(1, 4, 1), (3, 8, 2), (16, 4, 1)])
+def test_quantised_groups_to_the_rounding_of_their_weights(dtype, D, T, HQ, HKV, monkeypatch):
+    """Over quantised pages weights are rounded to fp16 whatever the type: the shapes of the
+    other module again, with that tolerance, and every count of arrivals is zero after."""
+    monkeypatch.setitem(shared.REL, dtype, rel(dtype, "e4m3"))
+    b, _ = shared.run((dtype, "e4m3"), [(64, [0, 1, 17, 200]), (1000, [3, 40, 15]), (0, [50]),
+                                        (16, [0, 0, 0]), (500, [90])], T, HQ, HKV, D, 16, 77)
+    assert not b.c.work[:ARRIVALS].any()
+
+
+@pytest.mark.parametrize("kind", [("bf16", None), ("f32", None), ("bf16", "e4m3")])
+def test_every_arrival_is_counted_off(kind):
+    """Heads of 64 have three CTAs an SM: rows that are split over all of them."""
+    dtype, pages = kind
+    rng = np.random.default_rng(78)
+    b = Batch(rng, [(0, [9000] * 24), (64, [5000, 4000])], 1, 8, 2, 64, dtype, pages, 256)
+    q = draw(rng, (26, 8, 64), dtype)[0]
+    slot, share = ints(range(26)), b.c.new_share(26)
+    b.c.rssm_kv_share(slot, 1, share)
+    for _ in range(2):
+        b.c.rssm_attn_decode(1, q, slot, 1, torch.empty_like(q))
+        b.c.rssm_attn_decode_shared(1, q, slot, 1, share, torch.empty_like(q))
+    assert b.c.rssm_kv_get_device_error() == 0
+    assert not b.c.work[:ARRIVALS].any()
