@@ -81,17 +81,13 @@ cudaError_t attn_shared_launch(DecodeParams p, const void* maps, const void* tc_
                                int dt, int num_sms, cudaStream_t st) {
   const int sms = num_sms < kMaxSms ? num_sms : kMaxSms;
   const bool quant = p.scales != nullptr;
-  // blocks of as many rows as there are
-  auto block = [&](long long rows) {
-    const int n = attn_decode_block_rows(D, dt, quant, rows < 4096 ? (int)rows : 4096);
-    return n == 32 && !quant ? (D == 256 ? 48 : 64) : n;
-  };
   p.cut = dt != DT_F32;
-  const cudaError_t e =
-      dt == DT_F32 ? attn_shared_prefix(&p, maps, D, dt, block((long long)p.B * p.T * p.G), sms, st)
-                   : attn_shared_tc_prefix(&p, tc_maps, D, dt, quant, st);
+  const cudaError_t e = dt == DT_F32 ? attn_shared_prefix(&p, maps, D, dt, 16, sms, st)
+                                     : attn_shared_tc_prefix(&p, tc_maps, D, dt, quant, st);
   if (e != cudaSuccess) return e;
-  const int own = block(p.T * p.G);
+  // OWN has no blocks of 32 rows over unquantised pages (decode_of_size)
+  int own = attn_decode_block_rows(D, dt, quant, p.T * p.G);
+  if (own == 32 && !quant) own = D == 256 ? 48 : 64;
   p.nmb = (p.T * p.G + own - 1) / own;
   return quant ? attn_shared_own_quant(&p, maps, D, dt, own, sms, st)
                : attn_shared_own(&p, maps, D, dt, own, sms, st);

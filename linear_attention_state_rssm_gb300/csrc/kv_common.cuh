@@ -135,8 +135,6 @@ struct GatherParams {
 
 constexpr int kShareSplit = kMaxSms;  // stretches that prefixes are cut into, about
 
-// What rows of a batch share (kv_share.cu), in the caller's buffer: the groups,
-// and what the first of the two launches leaves for the second.
 // Stretches that a call can have: an even split over the SMs, and one more for
 // every block of 128 rows of a group (of two members at least) and key head.
 inline long long share_segments(int B, int T, int G, int HKV) {
@@ -161,6 +159,8 @@ struct ShareRow {  // of a row with a prefix
   int32_t blocks;  // of a key head
   int32_t pad[2];
 };
+// What rows of a batch share (kv_share.cu), in the caller's buffer: the groups,
+// and what the first of the two launches leaves for the second.
 struct ShareView {
   int32_t* of;          // [2] B and T of the plan
   int32_t* groups;      // [1] their number
