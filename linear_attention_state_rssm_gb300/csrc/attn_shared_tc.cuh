@@ -32,12 +32,12 @@
 //        x = (c 2^a) (2^e s),   p = 2^(x - m),   w = 2^f p,   l = l + sum p,
 //    and m follows x + f: no token's size matters for another's.
 // Both are exact but for the rounding of w to fp16. The second takes longer (20 groups of
-// 4 rows, four layers: 317 us if every step goes that way, 187 if none does), and a
+// 4 rows, four layers: 301 us if every step goes that way, 187 if none does), and a
 // model's tokens hardly differ like that.
 //
-// Measured (GB300): a step of heads of 128 takes 0.72 us of 16-bit pages, near the
-// 0.55 of its products, and 1.48 of e4m3 ones (shared memory: codes read, fp16
-// written, operands read). 64 rows behind 8200 keys, four key heads: 9 to 11 us a
+// Measured (GB300): a step of heads of 128 takes 0.85 us of 16-bit pages, of which its
+// products are 0.55, and 1.68 of e4m3 ones (shared memory: codes read, fp16 written,
+// operands read), 64 blocks of rows behind 2.4 to 22 k keys. 64 rows behind 8200 keys, four key heads: 9 to 11 us a
 // layer, of which the bytes would take 2.5 and two steps a CTA 1.5; the rest are the
 // trips to the plan, the queries, the table and the first keys, and the way out.
 //
@@ -404,6 +404,24 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       // of step j: words of two tokens (the softmax's warps read the same at a time)
       [[maybe_unused]] const uint4* powers =
           reinterpret_cast<const uint4*>(sm + C::POWERS + (Q8 ? j % C::NE : 0) * 256);
+      // of a step that is not even: quarter q's scores by their keys' powers (-inf behind
+      // the last), and the powers. A quarter at a time, and from tensor memory for both of
+      // its uses, so that the registers of even steps stay theirs (else those took 2% more).
+      auto keyed = [&](int q, float (&y)[32], uint32_t (&w)[16]) {
+        tmem_ld32(ts + 32 * q, y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = powers[4 * q + i];
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+        tmem_ld_wait32(y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          un2(mul2(f2(y[2 * i], y[2 * i + 1]), key_powers(w[i])), y[2 * i], y[2 * i + 1]);
+          y[2 * i] = 32 * q + 2 * i < n ? y[2 * i] : kNegInf;
+          y[2 * i + 1] = 32 * q + 2 * i + 1 < n ? y[2 * i + 1] : kNegInf;
+        }
+      };
       float x[128], t[4];
       if (!Q8 || even) {
 #pragma unroll
@@ -425,24 +443,17 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
         for (int k = 0; k < 4; ++k) t[k] = t[k] * c + from;  // c is not negative
       } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, x + 32 * q);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_wait32(x + 32 * q);
-#pragma unroll
         for (int k = 0; k < 4; ++k) t[k] = kNegInf;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          float y[32];
+          uint32_t w[16];
+          keyed(q, y, w);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const uint4 w4 = powers[q];
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int i = 8 * q + 2 * k;
-            un2(mul2(f2(x[i], x[i + 1]), key_powers(w[k])), x[i], x[i + 1]);
-            x[i] = i < n ? x[i] : kNegInf;
-            x[i + 1] = i + 1 < n ? x[i + 1] : kNegInf;
+          for (int i = 0; i < 16; ++i) {
             float a, b;
-            un2(fma2(f2(x[i], x[i + 1]), c2, value_exponents(w[k])), a, b);
-            t[k] = max3(t[k], a, b);
+            un2(fma2(f2(y[2 * i], y[2 * i + 1]), c2, value_exponents(w[i])), a, b);
+            t[i & 3] = max3(t[i & 3], a, b);
           }
         }
       }
@@ -476,12 +487,10 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       }
       const float base = m == kNegInf ? 0.f : m - from;
       const uint64_t b2 = f2(-base, -base);
-      auto weigh = [&](auto uneven) {
-        constexpr bool U = decltype(uneven)::value;
+      if (!Q8 || even) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t w[16];
-          [[maybe_unused]] uint4 w4;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a, b;
@@ -489,18 +498,29 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
             a = exp2_fast(a);
             b = exp2_fast(b);
             l2[i & 3] = add2(l2[i & 3], f2(a, b));
-            if constexpr (U) {
-              if (i % 4 == 0) w4 = powers[4 * q + i / 4];
-              const uint32_t two = i % 4 == 0 ? w4.x : i % 4 == 1 ? w4.y : i % 4 == 2 ? w4.z : w4.w;
-              un2(mul2(f2(a, b), value_powers(two)), a, b);
-            }
             w[i] = pack2<M>(a, b);
           }
           tmem_st16u(ts + 16 * q, w);
         }
-      };
-      if (!Q8 || even) weigh(std::false_type{});
-      else weigh(std::true_type{});
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {  // the weights lie over scores that have been read
+          float y[32];
+          uint32_t w[16];
+          keyed(q, y, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            un2(fma2(f2(y[2 * i], y[2 * i + 1]), c2, b2), a, b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            l2[i & 3] = add2(l2[i & 3], f2(a, b));
+            un2(mul2(f2(a, b), value_powers(w[i])), a, b);
+            w[i] = pack2<M>(a, b);
+          }
+          tmem_st16u(ts + 16 * q, w);
+        }
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&pfull[j & 1]);
