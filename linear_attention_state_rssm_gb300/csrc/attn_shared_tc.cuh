@@ -26,8 +26,9 @@
 //    to a difference of 15. A step has one factor for all its scores, c' = c 2^a 2^E,
 //    and one for its values, which the reference m follows,
 //        w = 2^(c' s + F - m),   l = l + 2^-F sum w,   O = O + w V'.
-//    The weights' headroom is that of a token of F, so f may differ by 6 only; and F
-//    itself has its bounds, so that no w falls out of fp32's range beside another step's.
+//    The weights' headroom is that of a token of F, so f may differ by 6 only (a weight
+//    below 2^-17 of the largest is off by 2^-28 of it at most); and F itself has its
+//    bounds, so that no w falls out of fp32's range beside another step's.
 //  - other steps: codes as they are, powers column by column in fp32,
 //        x = (c 2^a) (2^e s),   p = 2^(x - m),   w = 2^f p,   l = l + sum p,
 //    and m follows x + f: no token's size matters for another's.
@@ -37,9 +38,10 @@
 //
 // Measured (GB300): a step of heads of 128 takes 0.85 us of 16-bit pages, of which its
 // products are 0.55, and 1.68 of e4m3 ones (shared memory: codes read, fp16 written,
-// operands read), 64 blocks of rows behind 2.4 to 22 k keys. 64 rows behind 8200 keys, four key heads: 9 to 11 us a
-// layer, of which the bytes would take 2.5 and two steps a CTA 1.5; the rest are the
-// trips to the plan, the queries, the table and the first keys, and the way out.
+// operands read), 64 blocks of rows behind 2.4 to 22 k keys. 64 rows behind 8200 keys,
+// four key heads: 9 to 11 us a layer, of which the bytes would take 2.5 and two steps a
+// CTA 1.7; the rest are the trips to the plan, the queries, the table and the first keys,
+// and the way out.
 //
 // Even a group of few rows takes the whole instruction, whose 128 rows cost less
 // than the prefix's bytes take to arrive: 128 keys of 128 values are 64 KB, 1.5
@@ -606,8 +608,9 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
           for (int k = 0; k < 4; ++k) {
             const bool on = lane + 32 * k < n;
             const unsigned two = bytes[lane + 32 * k];
-            most_k = max(most_k, on ? two & 0xff : 0), least_k = min(least_k, on ? two & 0xff : 255);
-            most_v = max(most_v, on ? two >> 8 : 0), least_v = min(least_v, on ? two >> 8 : 255);
+            const unsigned key = two & 0xff, value = two >> 8;
+            most_k = max(most_k, on ? key : 0), least_k = min(least_k, on ? key : 255);
+            most_v = max(most_v, on ? value : 0), least_v = min(least_v, on ? value : 255);
           }
           most_k = __reduce_max_sync(kFull, most_k);
           most_v = __reduce_max_sync(kFull, most_v);
@@ -626,7 +629,9 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
         }
         // 2^(e - E) or 2^(f - F) in fp16: normal to 2^-14, then its second largest bit
         const int d2 = (int)(i & 1 ? both >> 8 : both & 0xff) - (int)(i & 1 ? most_v : most_k);
-        const uint32_t bits = !even || r >= n ? 0x3c00u : d2 >= -14 ? (uint32_t)(15 + d2) << 10 : 0x200u;
+        const uint32_t bits = !even || r >= n ? 0x3c00u
+                              : d2 >= -14     ? (uint32_t)(15 + d2) << 10
+                                              : 0x200u;
         const uint32_t twice = bits | bits << 16;
         const __half2 by = *reinterpret_cast<const __half2*>(&twice);
         constexpr int WIDE = D == 256 ? 2 : 1, W = D / WIDE;  // a box's width

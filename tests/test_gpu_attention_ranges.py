@@ -161,14 +161,16 @@ def test_values_of_zeros_beside_the_largest(D, first):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("pages", [None, "e4m3"])
 @pytest.mark.parametrize("low", [16.0, 18.0])
-def test_many_small_weights_in_fp16(D, pages, low):
+@pytest.mark.parametrize("top", [1.0, 14.0])
+def test_many_small_weights_in_fp16(D, pages, low, top):
     """Thousands of keys of a weight of 2^-23 or 2^-26 beside one of weight one, and values
-    448 times its: weights relative to one would lose them in fp16, or round them by half."""
+    448 or 32 times its: weights relative to one would lose them in fp16, or round them by
+    half."""
     rng = np.random.default_rng([75, D])
     b = Batch(rng, [(20000, [0, 40]), (0, [9000])], 1, 4, 2, D, "f16", pages, 64, scale=1.0)
     for s, n in enumerate(b.lens):
         k, v = np.zeros((n + 1, 2, D)), np.full((n + 1, 2, D), 448.0)
-        k[77, :, 0], v[77] = low, 1.0
+        k[77, :, 0], v[77] = low, top
         put(b, 0, s, k)
         put(b, 1, s, v)
     q = torch.zeros(3, 4, D, dtype=torch.float16, device="cuda")
