@@ -610,8 +610,9 @@ typedef struct rssm_head_norm {
  * with v_out (may be null, contiguous [N][HKV][D], 16-byte aligned; may be v
  * itself where that is contiguous), which takes the values in a row as k_out
  * takes the keys. Both take what the pages hold: from quantised pages the
- * values that the codes stand for, rounded to dtype, so that the attention of a
- * prompt over k_out and v_out sees what later tokens will see.
+ * values that the codes stand for, rounded to dtype (an F16 input above 63488
+ * may be held as 65536, which F16 has as an infinity), so that the attention of
+ * a prompt over k_out and v_out sees what later tokens will see.
  */
 rssm_status rssm_kv_append_norm(rssm_kv_handle *h, int32_t layer, const void *q,
                                 const void *k, const void *v, int64_t q_stride,

@@ -32,11 +32,11 @@
 //
 // Quantised pages (Q): the same with e4m3 boxes and, beside each, two bytes a key
 // with its powers of two (attn_quant.cuh); blocks of 8 rows too. Measured: 56 rows
-// of 1 to 8 k tokens, 16/4 heads of 256: 78 us, 5.6 TB/s (83% of the copy rate);
-// two rows of 109 to 131 k tokens, 32/8 heads of 128: 89 us, 5.8 TB/s (86%). What a
+// of 1 to 8 k tokens, 16/4 heads of 256: 79 us, 5.6 TB/s (83% of the copy rate);
+// two rows of 109 to 131 k tokens, 32/8 heads of 128: 88 us, 5.9 TB/s (87%). What a
 // step costs besides its bytes holds them back: half the bytes, as many keys.
-// Windows of 8 tokens (32 rows to a head): 74 us, 2.1 TB/s, bound by two warps'
-// steps per stream, one instruction after the other.
+// Windows of 8 tokens (32 rows to a head): 77 us, 2.0 TB/s, bound by two warps'
+// steps per stream, one instruction after the other (16-bit pages: 69 us).
 //
 // Prefixes that rows share (kv_share.cu) come in two launches. PREFIX, here for
 // fp32 alone (else attn_shared_tc.cuh): a line of groups instead of rows; the query
@@ -85,8 +85,8 @@ struct DecCfg {
   // Sixteen rows a warp of heads of 128: as many warps as 168 registers leave room
   // for, in two CTAs, or in one where a stream is several warps, whose steps then wait
   // less for one another (125 windows of 8 tokens over 3300 tokens, 16/4 heads: two
-  // CTAs of four warps 166 us, one of ten 151, of twelve 202; of 16 tokens, four warps
-  // to a stream: two of four 485, one of eight 329).
+  // CTAs of four warps 166 us, one of ten 153, of twelve 202; of 16 tokens, four warps
+  // to a stream: two of four 485, one of eight 315).
   static constexpr bool WIDE = NQ == 2 && D == 128 && MW > 1;
   static constexpr int CPS = NQ == 1              ? (D == 64 ? 3 : 2)
                              : D == 256 || WIDE   ? 1

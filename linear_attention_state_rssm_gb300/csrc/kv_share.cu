@@ -9,7 +9,7 @@
 // in two parts of its keys, which meet in the running maximum, sum and output
 // (attn_decode.cuh): what the second launch begins with is what the first left.
 //
-// It is bound by trips to memory: one CTA, seven phases one after the other, 10 us
+// It is bound by trips to memory: one CTA, seven phases one after the other, 11 us
 // for 64 rows of 130 pages. Once a step, so beside all layers' attention it is small;
 // more CTAs would need waits over the grid.
 //
