@@ -33,7 +33,7 @@
 //        x = (c 2^a) (2^e s),   p = 2^(x - m),   w = 2^f p,   l = l + sum p,
 //    and m follows x + f: no token's size matters for another's.
 // Both are exact but for the rounding of w to fp16. The second takes longer (20 groups of
-// 4 rows, four layers: 301 us if every step goes that way, 187 if none does), and a
+// 4 rows, four layers: 310 us if every step goes that way, 187 if none does), and a
 // model's tokens hardly differ like that.
 //
 // Measured (GB300): a step of heads of 128 takes 0.85 us of 16-bit pages, of which its
@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(SharedTcCfg<D, Q8>::NT, 1)
       if constexpr (Q8) {
         tc_wait(&efull[j % C::NE], (uint32_t)((j / C::NE) & 1), dead, gave_up);
         const int2 e = largest[j % C::NE];
-        even = e.x != kUneven;
+        // (a vote: the warp stays together where a wait ran out and E is still being written)
+        even = __all_sync(kFull, e.x != kUneven);
         // Not 0 for tiny queries, by which the -inf of a score behind the last key would be
         // NaN: a score is below 2^31, times its key's power below 2^95, so what this keeps
         // is nothing. Nor infinite for large ones, by which a score of 0 would be.
